@@ -18,7 +18,10 @@ def __getattr__(name):
                 "ep_experts", "ep_combine", "EpWorkspace", "forward_boundary",
                 "forward_nvfp4_a16", "NVFP4_A16", "ep_experts_nvfp4", "forward_fp8",
                 "Fp8Weight", "FP8", "fp8_quantize_rows", "ep_experts_fp8", "BF16",
-                "forward_mxfp8", "Mxfp8Weight", "MXFP8"):
+                "forward_mxfp8", "Mxfp8Weight", "MXFP8", "OpWorkspace",
+                "grouped_matmul", "grouped_matmul_dx", "grouped_matmul_dw",
+                "grouped_matmul_workspace_size", "swiglu", "swiglu_grad", "orthogonalize",
+                "orthogonalize_workspace_size"):
         from . import api
         return getattr(api, name)
     raise AttributeError(name)

@@ -41,7 +41,11 @@ EXPORTS = ("beam_moe_workspace_size", "beam_moe_workspace_layout", "beam_moe_rou
            "beam_moe_ep_experts_nvfp4", "beam_moe_forward_fp8", "beam_moe_fp8_quantize_rows",
            "beam_moe_ep_experts_fp8", "beam_moe_forward_nvfp4_boundary",
            "beam_moe_forward_nvfp4_a16_boundary", "beam_moe_forward_fp8_boundary",
-           "beam_moe_forward_mxfp8", "beam_moe_forward_mxfp8_boundary")
+           "beam_moe_forward_mxfp8", "beam_moe_forward_mxfp8_boundary",
+           "beam_moe_grouped_matmul_workspace_size", "beam_moe_grouped_matmul",
+           "beam_moe_grouped_matmul_dx", "beam_moe_grouped_matmul_dw", "beam_moe_swiglu",
+           "beam_moe_swiglu_grad", "beam_moe_orthogonalize_workspace_size",
+           "beam_moe_orthogonalize")
 
 
 class BeamError(RuntimeError):
@@ -73,6 +77,27 @@ class _Fp8Weight(ctypes.Structure):
 
 class _Mxfp8Weight(ctypes.Structure):
     _fields_ = [("q", ctypes.c_void_p), ("sf", ctypes.c_void_p)]
+
+
+class _Grouped(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n_groups", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("K", ctypes.c_int32), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("x_ld", ctypes.c_int64), ("y_ld", ctypes.c_int64),
+                ("w_stride_e", ctypes.c_int64), ("w_stride_n", ctypes.c_int64),
+                ("w_stride_k", ctypes.c_int64)]
+
+
+class _Gate(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("F", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("gate_ld", ctypes.c_int64), ("up_ld", ctypes.c_int64)]
+
+
+class _Ortho(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float),
+                ("c", ctypes.c_float), ("eps", ctypes.c_float), ("stride_batch", ctypes.c_int64),
+                ("stride_row", ctypes.c_int64), ("stride_col", ctypes.c_int64)]
 
 
 def library_path() -> str:
@@ -159,6 +184,24 @@ def lib():
         L.beam_moe_ep_experts_nvfp4.restype = _ST
         L.beam_moe_ep_combine.argtypes = [cfgp, _P, _I64, _P, _P, _SZ, _P]
         L.beam_moe_ep_combine.restype = _ST
+        gp = ctypes.POINTER(_Grouped)
+        L.beam_moe_grouped_matmul_workspace_size.argtypes = [gp, ctypes.c_int32]
+        L.beam_moe_grouped_matmul_workspace_size.restype = _SZ
+        for name in ("beam_moe_grouped_matmul", "beam_moe_grouped_matmul_dx"):
+            f = getattr(L, name)
+            f.argtypes = [gp, _P, _P, _P, _P, _P, _SZ, _P]
+            f.restype = _ST
+        L.beam_moe_grouped_matmul_dw.argtypes = [gp, _P, _P, _P, ctypes.c_int32, _P, _P, _SZ, _P]
+        L.beam_moe_grouped_matmul_dw.restype = _ST
+        ap = ctypes.POINTER(_Gate)
+        L.beam_moe_swiglu.argtypes = [ap, _P, _P, _P, _P, _I64, _P]
+        L.beam_moe_swiglu.restype = _ST
+        L.beam_moe_swiglu_grad.argtypes = [ap, _P, _I64, _P, _P, _P, _P, _I64, _P, _I64, _P, _P]
+        L.beam_moe_swiglu_grad.restype = _ST
+        L.beam_moe_orthogonalize_workspace_size.argtypes = [ctypes.c_int32] * 4
+        L.beam_moe_orthogonalize_workspace_size.restype = _SZ
+        L.beam_moe_orthogonalize.argtypes = [ctypes.POINTER(_Ortho), _P, _P, _P, _SZ, _P]
+        L.beam_moe_orthogonalize.restype = _ST
         L.beam_status_string.argtypes = [_ST]
         L.beam_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -680,3 +723,306 @@ def ep_combine(cfg, y_back, T: int, ws: Workspace, out=None, stream=None):
                                      o.data_ptr(), ws.ptr, ws.nbytes, _stream(stream)),
            "beam_moe_ep_combine")
     return o
+
+
+# ---------------------------------------------------------------- training
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class OpWorkspace:
+    """Caller-owned device workspace of one training operator (a status word,
+    then scratch); calls that share it must be on one stream."""
+
+    def __init__(self, nbytes: int, device=None):
+        self.nbytes = int(nbytes)
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8,
+                               device=device if device is not None else torch.device("cuda"))
+        self.buf[:256].zero_()
+
+    @property
+    def ptr(self) -> int:
+        return self.buf.data_ptr()
+
+
+def _type(dtype, name: str, allowed) -> int:
+    if dtype not in allowed:
+        raise TypeError(f"{name} must be one of {', '.join(map(str, allowed))}, got {dtype}")
+    return _DTYPES[dtype]
+
+
+_HALVES = (torch.bfloat16, torch.float16)
+
+
+def _rows2d(t: torch.Tensor, name: str, dtype=None, width=None) -> int:
+    """Check a CUDA matrix with contiguous rows; returns its row stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (width is not None and t.shape[1] != width):
+        raise ValueError(f"{name} must be a matrix"
+                         + (f" with {width} columns" if width is not None else "")
+                         + f", got shape {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if ld < t.shape[1]:
+        raise ValueError(f"{name} must not have overlapping rows, got strides {t.stride()}")
+    return ld
+
+
+def _same_device(first: torch.Tensor, **others) -> None:
+    for name, t in others.items():
+        if isinstance(t, torch.Tensor) and t.device != first.device:
+            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+
+
+def _offsets(offsets, n_groups=None) -> int:
+    ptr = _dev(offsets, torch.int32, "offsets")
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must be a vector of at least 2 boundaries, "
+                         f"got shape {tuple(offsets.shape)}")
+    if n_groups is not None and offsets.numel() != n_groups + 1:
+        raise ValueError(f"offsets must hold {n_groups + 1} boundaries, got {offsets.numel()}")
+    return ptr
+
+
+def _grouped_desc(rows, E, N, K, dtype, out_dtype, x_ld, y_ld, w_strides) -> _Grouped:
+    if not 1 <= E <= 1024:
+        raise ValueError(f"1 to 1024 groups, got {E}")
+    return _Grouped(rows, E, N, K, _type(dtype, "operands", _HALVES),
+                    _type(out_dtype, "out_dtype", (dtype, torch.float32)), x_ld, y_ld, *w_strides)
+
+
+def _w_strides(w, dtype) -> tuple:
+    if not isinstance(w, torch.Tensor) or not w.is_cuda:
+        raise TypeError("w must be a CUDA tensor")
+    if w.dtype != dtype:
+        raise TypeError(f"w must be {dtype}, got {w.dtype}")
+    if w.dim() != 3 or w.numel() == 0:
+        raise ValueError(f"w must be [groups, N, K], got shape {tuple(w.shape)}")
+    E, N, K = w.shape
+    e, n, k = w.stride()
+    if K == 1 and n != 1:
+        k = 1
+    if N == 1 and k != 1:
+        n = 1
+    if k == 1 and (N == 1 or n >= K):
+        n = K if N == 1 else n
+    elif n == 1 and (K == 1 or k >= N):
+        k = N if K == 1 else k
+    else:
+        raise ValueError(f"w must be contiguous along N or K, got strides {w.stride()}")
+    return (e if E > 1 else N * K), n, k
+
+
+def grouped_matmul_workspace_size(rows: int, n_groups: int, N: int, K: int,
+                                  dtype=torch.bfloat16, unaligned: bool = False) -> int:
+    """Workspace bytes of the grouped products on contiguous operands (with
+    ``unaligned``, of views whose base or strides are not 16-byte multiples)."""
+    d = _grouped_desc(rows, n_groups, N, K, dtype, dtype, K, N, (N * K, K, 1))
+    n = lib().beam_moe_grouped_matmul_workspace_size(ctypes.byref(d), int(unaligned))
+    if n == 0:
+        raise BeamError(1, "beam_moe_grouped_matmul_workspace_size")
+    return int(n)
+
+
+def _op_ws(ws, device, size) -> "OpWorkspace":
+    return OpWorkspace(size(), device) if ws is None else ws
+
+
+def _grouped_ws(ws, d, device, *operands):
+    def size():
+        odd = any(t.data_ptr() % 16 for t in operands)
+        n = lib().beam_moe_grouped_matmul_workspace_size(ctypes.byref(d), int(odd))
+        if n == 0:
+            raise BeamError(1, "beam_moe_grouped_matmul_workspace_size")
+        return n
+    return _op_ws(ws, device, size)
+
+
+def _grouped_rows(a, a_name, w, offsets, out, out_dtype, ws, transpose):
+    """y = x W^T or, with ``transpose``, dx = dy W, group by group."""
+    strides = _w_strides(w, a.dtype if isinstance(a, torch.Tensor) else None)
+    E, N, K = w.shape
+    width_in, width_out = (N, K) if transpose else (K, N)
+    ld = _rows2d(a, a_name, width=width_in)
+    _same_device(a, w=w, offsets=offsets, out=out)
+    dt = out_dtype if out_dtype is not None else out.dtype if out is not None else a.dtype
+    off = _offsets(offsets, E)
+    if out is None:
+        out = torch.empty(a.shape[0], width_out, dtype=dt, device=a.device)
+    out_ld = _rows2d(out, "out", dt, width_out)
+    if out.shape[0] != a.shape[0]:
+        raise ValueError(f"out must have {a.shape[0]} rows, got {out.shape[0]}")
+    x_ld, y_ld = (out_ld, ld) if transpose else (ld, out_ld)
+    d = _grouped_desc(a.shape[0], E, N, K, a.dtype, dt, x_ld, y_ld, strides)
+    ws = _grouped_ws(ws, d, a.device, a, w)
+    return d, off, out, ws
+
+
+def grouped_matmul(x, w, offsets, out=None, out_dtype=None, ws: OpWorkspace | None = None,
+                   stream=None):
+    """y[r] = W[e] x[r] for the rows offsets[e] <= r < offsets[e + 1] of every
+    group e; rows outside all groups are zero.
+
+    x [rows, K] and w [E, N, K] are BF16 or F16 (w contiguous along N or K, so
+    ``w.transpose(1, 2)`` of a [E, K, N] tensor is read in place), offsets
+    int32 [E + 1].  y [rows, N] has x's type or FP32."""
+    d, off, y, ws = _grouped_rows(x, "x", w, offsets, out, out_dtype, ws, False)
+    with torch.cuda.device(x.device):
+        _check(lib().beam_moe_grouped_matmul(ctypes.byref(d), x.data_ptr(), w.data_ptr(), off,
+                                             y.data_ptr(), ws.ptr, ws.nbytes, _stream(stream)),
+               "beam_moe_grouped_matmul")
+    return y
+
+
+def grouped_matmul_dx(dy, w, offsets, out=None, out_dtype=None, ws: OpWorkspace | None = None,
+                      stream=None):
+    """The input gradient of ``grouped_matmul``: dx[r] = W[e]^T dy[r]."""
+    d, off, dx, ws = _grouped_rows(dy, "dy", w, offsets, out, out_dtype, ws, True)
+    with torch.cuda.device(dy.device):
+        _check(lib().beam_moe_grouped_matmul_dx(ctypes.byref(d), dy.data_ptr(), w.data_ptr(), off,
+                                                dx.data_ptr(), ws.ptr, ws.nbytes,
+                                                _stream(stream)), "beam_moe_grouped_matmul_dx")
+    return dx
+
+
+def grouped_matmul_dw(dy, x, offsets, out=None, accumulate: bool = False, out_dtype=None,
+                      ws: OpWorkspace | None = None, stream=None):
+    """The weight gradient of ``grouped_matmul``: dW[e] = sum over the rows of
+    group e of dy[r] x[r]^T, [E, N, K] in the operands' type or FP32; zero for
+    a group without rows.  ``accumulate`` adds to ``out`` (FP32)."""
+    y_ld = _rows2d(dy, "dy")
+    x_ld = _rows2d(x, "x", dy.dtype)
+    if x.shape[0] != dy.shape[0]:
+        raise ValueError(f"x and dy must have the same rows, got {x.shape[0]} and {dy.shape[0]}")
+    _same_device(dy, x=x, offsets=offsets, out=out)
+    off = _offsets(offsets)
+    E, N, K = offsets.numel() - 1, dy.shape[1], x.shape[1]
+    dt = out_dtype if out_dtype is not None else out.dtype if out is not None else dy.dtype
+    if accumulate and (out is None or dt != torch.float32):
+        raise ValueError("accumulate needs an FP32 out to add to")
+    d = _grouped_desc(x.shape[0], E, N, K, dy.dtype, dt, x_ld, y_ld, (N * K, K, 1))
+    if out is None:
+        out = torch.empty(E, N, K, dtype=dt, device=dy.device)
+    if tuple(out.shape) != (E, N, K):
+        raise ValueError(f"out must be {(E, N, K)}, got {tuple(out.shape)}")
+    dst = _dev(out, dt, "out")
+    if ws is None:
+        # W takes no part: describe one that needs no copy
+        d.w_stride_n, d.w_stride_e = (K + 7) // 8 * 8, (K + 7) // 8 * 8 * N
+    ws = _grouped_ws(ws, d, dy.device, dy, x)
+    with torch.cuda.device(dy.device):
+        _check(lib().beam_moe_grouped_matmul_dw(ctypes.byref(d), dy.data_ptr(), x.data_ptr(), off,
+                                                int(accumulate), dst, ws.ptr, ws.nbytes,
+                                                _stream(stream)), "beam_moe_grouped_matmul_dw")
+    return out
+
+
+def _row_weight(row_weight, rows: int):
+    if row_weight is None:
+        return None
+    ptr = _dev(row_weight, torch.float32, "row_weight")
+    if tuple(row_weight.shape) != (rows,):
+        raise ValueError(f"row_weight must be [{rows}], got {tuple(row_weight.shape)}")
+    return ptr
+
+
+def _gate_desc(gate, up):
+    g_ld = _rows2d(gate, "gate")
+    u_ld = _rows2d(up, "up", gate.dtype, gate.shape[1])
+    if up.shape[0] != gate.shape[0]:
+        raise ValueError(f"gate and up must have the same rows, got {gate.shape[0]} "
+                         f"and {up.shape[0]}")
+    return _Gate(gate.shape[0], gate.shape[1], _type(gate.dtype, "gate", _HALVES), g_ld, u_ld)
+
+
+def _like(out, like, name):
+    if out is None:
+        out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    ld = _rows2d(out, name, like.dtype, like.shape[1])
+    if out.shape[0] != like.shape[0]:
+        raise ValueError(f"{name} must have {like.shape[0]} rows, got {out.shape[0]}")
+    _same_device(like, **{name: out})
+    return out, ld
+
+
+def swiglu(gate, up, row_weight=None, out=None, stream=None):
+    """h = row_weight[r] * silu(gate) * up (BF16 or F16 [rows, F], row strides
+    free; FP32 inside, rounded once).  Without row_weight the factor is 1."""
+    d = _gate_desc(gate, up)
+    _same_device(gate, up=up, row_weight=row_weight)
+    h, h_ld = _like(out, gate, "out")
+    w = _row_weight(row_weight, gate.shape[0])
+    with torch.cuda.device(gate.device):
+        _check(lib().beam_moe_swiglu(ctypes.byref(d), gate.data_ptr(), up.data_ptr(), w,
+                                     h.data_ptr(), h_ld, _stream(stream)), "beam_moe_swiglu")
+    return h
+
+
+def swiglu_grad(dh, gate, up, row_weight=None, out=None, stream=None):
+    """The gradient of ``swiglu``: (dgate, dup) and, with row_weight, its own
+    gradient (FP32 [rows]).  ``out``: (dgate, dup) to write to; they may be
+    gate and up themselves."""
+    d = _gate_desc(gate, up)
+    dh_ld = _rows2d(dh, "dh", gate.dtype, gate.shape[1])
+    if dh.shape[0] != gate.shape[0]:
+        raise ValueError(f"dh must have {gate.shape[0]} rows, got {dh.shape[0]}")
+    _same_device(gate, up=up, dh=dh, row_weight=row_weight)
+    dg, dg_ld = _like(None if out is None else out[0], gate, "dgate")
+    du, du_ld = _like(None if out is None else out[1], gate, "dup")
+    w = _row_weight(row_weight, gate.shape[0])
+    dw = None if w is None else torch.empty(gate.shape[0], dtype=torch.float32, device=gate.device)
+    with torch.cuda.device(gate.device):
+        _check(lib().beam_moe_swiglu_grad(ctypes.byref(d), dh.data_ptr(), dh_ld, gate.data_ptr(),
+                                          up.data_ptr(), w, dg.data_ptr(), dg_ld, du.data_ptr(),
+                                          du_ld, None if dw is None else dw.data_ptr(),
+                                          _stream(stream)), "beam_moe_swiglu_grad")
+    return (dg, du) if dw is None else (dg, du, dw)
+
+
+def orthogonalize_workspace_size(batch: int, rows: int, cols: int, dtype=torch.float32) -> int:
+    """Workspace bytes of ``orthogonalize`` (FP32 input needs the most)."""
+    n = lib().beam_moe_orthogonalize_workspace_size(
+        batch, rows, cols, _type(dtype, "m", _HALVES + (torch.float32,)))
+    if n == 0:
+        raise BeamError(1, "beam_moe_orthogonalize_workspace_size")
+    return int(n)
+
+
+def orthogonalize(m, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                  out=None, out_dtype=None, ws: OpWorkspace | None = None, stream=None):
+    """The update m [..., R, C] orthogonalised matrix by matrix: X = M / (|M|_F
+    + eps), then ``steps`` times X <- a X + (b A + c A^2) X with A = X X^T (the
+    Muon optimiser's Newton-Schulz products).
+
+    m is BF16, F16 or FP32 with any strides; the result is BF16 or F16
+    (``out_dtype``; m's own 16-bit type, BF16 for FP32) and accurate to about
+    2e-3 of its norm."""
+    if not isinstance(m, torch.Tensor) or not m.is_cuda:
+        raise TypeError("m must be a CUDA tensor")
+    if m.dim() < 2:
+        raise ValueError(f"m must be a matrix or a stack of them, got shape {tuple(m.shape)}")
+    kind = _type(m.dtype, "m", _HALVES + (torch.float32,))
+    dt = out_dtype if out_dtype is not None else out.dtype if out is not None else \
+        m.dtype if m.dtype in _HALVES else torch.bfloat16
+    out_kind = _type(dt, "out_dtype", _HALVES)
+    R, C = m.shape[-2:]
+    stack = m if m.dim() == 3 else m.reshape(-1, R, C) if m.numel() else m.new_empty(0, R, C)
+    batch = stack.shape[0]
+    if out is None:
+        out = torch.empty(m.shape, dtype=dt, device=m.device)
+    if out.shape != m.shape:
+        raise ValueError(f"out must be {tuple(m.shape)}, got {tuple(out.shape)}")
+    _same_device(m, out=out)
+    dst = _dev(out, dt, "out")
+    if m.numel() == 0:
+        return out
+    d = _Ortho(batch, R, C, kind, out_kind, int(steps), *(float(v) for v in coeffs), float(eps),
+               *stack.stride())
+    ws = _op_ws(ws, m.device, lambda: orthogonalize_workspace_size(batch, R, C, m.dtype))
+    with torch.cuda.device(m.device):
+        _check(lib().beam_moe_orthogonalize(ctypes.byref(d), stack.data_ptr(), dst, ws.ptr,
+                                            ws.nbytes, _stream(stream)), "beam_moe_orthogonalize")
+    return out

@@ -14,12 +14,19 @@
 #include "../../include/beam_moe.h"
 #include "common.cuh"
 #include "expert_gemm.cuh"
+#include "host.cuh"
 
 namespace {
 
 using beam::GemmArgs;
+using beam::host::align_up;
+using beam::host::aligned16;
+using beam::host::device_info;
+using beam::host::DevInfo;
+using beam::host::encoder;
+using beam::host::g_encode;
+using beam::host::kAlign;
 
-constexpr size_t kAlign = 256;
 constexpr int kMinRows = 256;  // token-operand buffers hold at least one full tile
 constexpr int64_t kTensorRouterMinT = 256;  // from here on the router runs on tensor cores
 // SM count the router's split-K partials are sized for (a workspace is sized
@@ -27,33 +34,11 @@ constexpr int64_t kTensorRouterMinT = 256;  // from here on the router runs on t
 constexpr int kSizingSms = 160;
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
 // ---------------------------------------------------------------- settings
 cudaEvent_t g_events[8];
 int g_num_events = 0;
 uint64_t g_wait_ns = kDefaultWaitNs;
 int g_withhold = 0;
-
-// ---------------------------------------------------------------- driver entry
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiledFn g_encode = nullptr;
-std::once_flag g_encode_once;
-
-bool encoder() {
-  std::call_once(g_encode_once, [] {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-  });
-  return g_encode != nullptr;
-}
 
 // 2-D BF16 tensor [rows, cols] (cols contiguous), box {64, box_rows}, 128-byte swizzle.
 bool tmap_bf16(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
@@ -80,31 +65,6 @@ bool tmap_u8(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uin
                   box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
-}
-
-// ---------------------------------------------------------------- device facts
-struct DevInfo {
-  int sms = 0;
-  bool supported = false;
-};
-
-bool device_info(DevInfo* out) {
-  static DevInfo cache[64];
-  static std::mutex mu;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
-  std::lock_guard<std::mutex> lock(mu);
-  if (cache[dev].sms == 0) {
-    int sms = 0, major = 0, minor = 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-      return false;
-    cache[dev].sms = sms;
-    cache[dev].supported = (major == 10 && minor == 3);
-  }
-  *out = cache[dev];
-  return true;
 }
 
 // ---------------------------------------------------------------- shapes
@@ -232,8 +192,6 @@ Layout make_layout(const beam_moe_config_t& c, int64_t T_max, int32_t fmt = BEAM
   L.total = off;
   return L;
 }
-
-bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 template <typename T>
 T* at(void* ws, size_t off) {
@@ -1006,6 +964,12 @@ void* noalloc_scratch_address() {
 }
 
 }  // namespace
+
+namespace beam {
+namespace host {
+uint64_t wait_limit_ns() { return g_wait_ns; }
+}  // namespace host
+}  // namespace beam
 
 extern "C" {
 

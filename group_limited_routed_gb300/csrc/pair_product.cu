@@ -1,0 +1,106 @@
+// Launchers of the training operators' matrix products (device code:
+// pair_product_kernel.cuh).
+#include <algorithm>
+#include <mutex>
+
+#include "launch_once.cuh"
+#include "pair_product_kernel.cuh"
+
+namespace beam {
+namespace {
+
+template <auto Kern>
+int resident_clusters_once(const cudaLaunchConfig_t& cfg) {
+  static std::mutex mu;
+  static int cached[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cached[dev] == 0) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, Kern, &cfg) != cudaSuccess) return 0;
+    cached[dev] = n;
+  }
+  return cached[dev];
+}
+
+template <int NT, bool A_MN, bool B_MN, int KIND, bool WIDE>
+cudaError_t launch_impl(const CUtensorMap& a, const CUtensorMap& b, const ProductArgs& p,
+                        int64_t max_tiles, bool dependent, cudaStream_t s) {
+  using C = ProductCfg<NT>;
+  constexpr auto kern = pair_product_kernel<NT, A_MN, B_MN, KIND, WIDE>;
+  const cudaError_t err = smem_limit_once<kern>(static_cast<int>(C::SMEM_BYTES));
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kPThreads);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;  // the occupancy query takes the cluster shape only
+  cfg.gridDim = dim3(2);
+  const int resident = resident_clusters_once<kern>(cfg);
+  if (resident <= 0) return cudaErrorUnknown;
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(resident, max_tiles));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.numAttrs = dependent ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, b, p);
+}
+
+template <int NT>
+cudaError_t launch_rows(bool a_mn, const CUtensorMap& a, const CUtensorMap& b,
+                        const ProductArgs& p, int64_t tiles, bool dep, cudaStream_t s) {
+  const bool wide = p.out_type == kF32;
+  if (a_mn)
+    return wide ? launch_impl<NT, true, false, kProductRows, true>(a, b, p, tiles, dep, s)
+                : launch_impl<NT, true, false, kProductRows, false>(a, b, p, tiles, dep, s);
+  return wide ? launch_impl<NT, false, false, kProductRows, true>(a, b, p, tiles, dep, s)
+              : launch_impl<NT, false, false, kProductRows, false>(a, b, p, tiles, dep, s);
+}
+
+}  // namespace
+
+cudaError_t launch_pair_product(int kind, int nt, bool a_mn, bool b_mn, const CUtensorMap& a,
+                                const CUtensorMap& b, const ProductArgs& p, bool dependent,
+                                cudaStream_t s) {
+  const int64_t mt = (p.M + kProductTileM - 1) / kProductTileM;
+  if (kind == kProductRows && !b_mn) {
+    // at most one ragged block more than rows / nt per group that has rows
+    const int64_t tiles = mt * (p.rows / nt + std::min(p.groups, p.rows));
+    switch (nt) {
+      case 32: return launch_rows<32>(a_mn, a, b, p, tiles, dependent, s);
+      case 64: return launch_rows<64>(a_mn, a, b, p, tiles, dependent, s);
+      case 128: return launch_rows<128>(a_mn, a, b, p, tiles, dependent, s);
+      case 256: return launch_rows<256>(a_mn, a, b, p, tiles, dependent, s);
+    }
+    return cudaErrorInvalidValue;
+  }
+  const int64_t tiles = mt * ((p.N + nt - 1) / nt) * p.groups;
+  if (kind == kProductGroups && a_mn && b_mn && nt == 256)
+    return p.out_type == kF32
+               ? launch_impl<256, true, true, kProductGroups, true>(a, b, p, tiles, dependent, s)
+               : launch_impl<256, true, true, kProductGroups, false>(a, b, p, tiles, dependent, s);
+  if (kind == kProductDense && p.out_type != kF32) {
+    if (!a_mn && !b_mn && nt == 256)
+      return launch_impl<256, false, false, kProductDense, false>(a, b, p, tiles, dependent, s);
+    if (!a_mn && !b_mn && nt == 64)
+      return launch_impl<64, false, false, kProductDense, false>(a, b, p, tiles, dependent, s);
+    if (a_mn && !b_mn && nt == 256)
+      return launch_impl<256, true, false, kProductDense, false>(a, b, p, tiles, dependent, s);
+    if (a_mn && !b_mn && nt == 64)
+      return launch_impl<64, true, false, kProductDense, false>(a, b, p, tiles, dependent, s);
+    if (a_mn && b_mn && nt == 256)
+      return launch_impl<256, true, true, kProductDense, false>(a, b, p, tiles, dependent, s);
+    if (a_mn && b_mn && nt == 128)
+      return launch_impl<128, true, true, kProductDense, false>(a, b, p, tiles, dependent, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace beam

@@ -1,0 +1,687 @@
+// Device code of the training operators' matrix products (included by
+// pair_product.cu only).
+//
+// One persistent kernel, a cluster of two CTAs on an SM pair, computes
+// out[z][j, i] = sum_k A[z][i, k] B[z][j, k] in tiles of 256 columns i by up
+// to 256 rows j.  The pair shares M = 256 tcgen05 MMAs (cta_group::2): CTA r
+// stages columns [128 r, 128 r + 128) of the tile and rows [r n/2, r n/2 +
+// n/2) in its own shared memory, the leader issues, and each CTA's TMEM
+// receives its 128 columns for all n rows.  So each SM moves 128 x 64 of A
+// and n/2 x 64 of B per 64-wide k block for the tensor work of 128 x n.
+//
+// Putting the contiguous output axis on the MMA's M (TMEM lanes) makes the
+// ragged axis of grouped rows the MMA's N, which comes in steps of 16: a
+// group of 130 rows costs 144 columns of tensor time, not 256.  It also lets
+// a warp store 32 consecutive output columns without a transpose.
+//
+// Either operand may be k-contiguous or contiguous along its own axis (the
+// MN-major descriptors), so one kernel serves the product and both gradients:
+//   kProductRows    y[r, :] = x[r, :] W[e]^T: A = W[e] [N, K], B = x rows;
+//                   the input gradient is the same with W[e] read as [K, N]
+//                   through its MN-major form (no transposed copy of W).
+//   kProductGroups  dW[e] = sum over the group's rows: k is the row axis and
+//                   both operands are MN-major.  The last 16-row MMA step of
+//                   a group also covers rows of the next group; those rows
+//                   are zeroed in shared memory (in both operands: 0 * inf
+//                   would not be 0) before the MMA reads them.
+//   kProductDense   stacks of equal products (the orthogonalisation), with an
+//                   affine epilogue and, for symmetric results, one triangle
+//                   of tiles that writes its mirror image as well.
+//
+// Sums: FP32 in TMEM.  A chain of MMAs into one accumulator truncates at
+// every step, an error that grows with the chain and reaches 1e-5 relative
+// over thousands of k.  16-bit outputs round at 2^-9 or 2^-12 and take one
+// chain; FP32 outputs (kWide) restart the accumulator every kWideBlocks k
+// blocks, alternating the two TMEM buffers, and the epilogue warps add the
+// pieces in FP32 registers.
+//
+// Every wait is bounded (gemm::Waiter); after an abort all roles still reach
+// the cluster barrier that precedes the release of TMEM.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "gemm_common.cuh"
+#include "pair_product.cuh"
+#include "ptx.cuh"
+
+namespace beam {
+namespace {
+
+using gemm::Waiter;
+
+constexpr int kPBK = 64;                       // k elements per block (128 bytes)
+constexpr uint32_t kPABytes = 128 * 128;       // one CTA's A per stage
+constexpr int kPEpiWarps = 16;
+constexpr int kPThreads = 96 + 32 * kPEpiWarps;
+constexpr uint32_t kPRing = 216 * 1024;
+constexpr int kWideBlocks = 4;                 // k blocks per accumulator chain, FP32 outputs
+constexpr uint64_t kPPeerDrainNs = 1000000ull; // see the producer's teardown
+constexpr uint32_t kAtom = 64 * 128;           // MN-major atom: 64 k rows of 64 elements
+
+template <int NT>
+struct ProductCfg {
+  static constexpr uint32_t B_BYTES = NT / 2 * 128;
+  static constexpr uint32_t STAGE = kPABytes + B_BYTES;
+  static constexpr int S_RAW = static_cast<int>(kPRing / STAGE);
+  static constexpr int S = S_RAW > 12 ? 12 : S_RAW;
+  static constexpr uint32_t TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
+  static constexpr uint32_t NUM_BARS = 3 * S + 5;
+  static constexpr uint32_t MISC = 16 + 4 * (2 * (kProductMaxGroups + 1) + 2);
+  static constexpr uint32_t SMEM_BYTES = 1024 + S * STAGE + NUM_BARS * 8 + MISC;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+  static_assert(STAGE % 1024 == 0, "swizzle atoms are 1024-byte aligned");
+  static_assert(TMEM_COLS <= 512, "TMEM columns");
+};
+
+// 3-D tiled load into this CTA's shared memory, bytes counted on a barrier of
+// either CTA of the pair.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m,
+                                                 uint32_t cluster_bar, int32_t x, int32_t y,
+                                                 int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar), "l"(policy)
+      : "memory");
+}
+
+// Shared-memory descriptor of an MN-major operand as a 128-byte-swizzled TMA
+// load of a 64 x 64 box leaves it: each k row is 128 bytes of 64 consecutive
+// elements; 8 k rows make a 1024-byte group (stride byte offset); the next 64
+// elements of the operand's own axis are one box further (leading byte offset).
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(kAtom >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+__device__ __forceinline__ void fence_acquire_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+struct ProductTile {
+  int z;         // group or matrix
+  int i0;        // first column
+  int j0;        // first row (kProductRows: of all rows)
+  int nvalid;    // rows of the tile
+  int n_mma;     // rounded up to the MMA's step
+  int k_blocks;  // 64-wide k blocks
+  int k0;        // kProductGroups: first row of the group
+  int k_count;   // kProductGroups: rows of the group
+};
+
+template <int NT, int KIND>
+__device__ __forceinline__ ProductTile product_tile(int tile, const ProductArgs& p,
+                                                    const int32_t* s_off, const int32_t* s_start) {
+  ProductTile t;
+  const int mt = (p.M + kProductTileM - 1) / kProductTileM;
+  if constexpr (KIND == kProductRows) {
+    int lo = 0, hi = p.groups;  // s_start[lo] <= tile < s_start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_start[mid] <= tile)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int local = tile - s_start[lo];
+    const int cnt = s_off[lo + 1] - s_off[lo];
+    // blocks of nearly equal size, each a multiple of 16 rows
+    const int nb = (cnt + NT - 1) / NT;
+    const int per = (((cnt + nb - 1) / nb) + 15) & ~15;
+    const int b = local % nb;
+    t.z = lo;
+    t.i0 = local / nb * kProductTileM;
+    t.j0 = s_off[lo] + b * per;
+    t.nvalid = min(per, cnt - b * per);
+    t.k_blocks = p.k_blocks;
+    t.k0 = t.k_count = 0;
+  } else {
+    const int nt = (p.N + NT - 1) / NT;
+    int i, j;
+    if (KIND == kProductDense && p.symmetric) {
+      // tiles with j >= i, in units of 256 columns and NT rows
+      constexpr int R = kProductTileM / NT;
+      const int per_z = mt * nt - R * (mt * (mt - 1) / 2);
+      t.z = tile / per_z;
+      int left = tile - t.z * per_z;
+      i = 0;
+      while (left >= nt - i * R) {
+        left -= nt - i * R;
+        ++i;
+      }
+      j = i * R + left;
+    } else {
+      const int per_z = mt * nt;
+      t.z = tile / per_z;
+      const int local = tile - t.z * per_z;
+      i = local / nt;
+      j = local - i * nt;
+    }
+    t.i0 = i * kProductTileM;
+    t.j0 = j * NT;
+    t.nvalid = min(NT, p.N - t.j0);
+    if constexpr (KIND == kProductGroups) {
+      t.k0 = s_off[t.z];
+      t.k_count = s_off[t.z + 1] - t.k0;
+      t.k_blocks = (t.k_count + kPBK - 1) / kPBK;
+    } else {
+      t.k_blocks = p.k_blocks;
+      t.k0 = t.k_count = 0;
+    }
+  }
+  t.n_mma = (t.nvalid + 15) & ~15;
+  return t;
+}
+
+template <int NT, int KIND>
+__device__ __forceinline__ int product_tiles(const ProductArgs& p, const int32_t* s_start) {
+  const int mt = (p.M + kProductTileM - 1) / kProductTileM;
+  const int nt = (p.N + NT - 1) / NT;
+  if constexpr (KIND == kProductRows) {
+    return s_start[p.groups];
+  } else if (KIND == kProductDense && p.symmetric) {
+    constexpr int R = kProductTileM / NT;
+    return p.groups * (mt * nt - R * (mt * (mt - 1) / 2));
+  } else {
+    return p.groups * mt * nt;
+  }
+}
+
+__device__ __forceinline__ uint32_t to16(float v, bool f16) {
+  return f16 ? static_cast<uint32_t>(__half_as_ushort(__float2half_rn(v)))
+             : static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v)));
+}
+
+// Two 16-bit values of one lane's column (rows j, j + 1) and its neighbour's
+// -> the word this lane stores: even lanes row j, odd lanes row j + 1, two
+// columns each.
+__device__ __forceinline__ uint32_t swap_pair(uint32_t mine, int lane) {
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+  return (lane & 1) ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+}
+
+template <int NT, bool A_MN, bool B_MN, int KIND, bool WIDE>
+__global__ void __launch_bounds__(kPThreads, 1)
+    pair_product_kernel(const __grid_constant__ CUtensorMap tm_a,
+                        const __grid_constant__ CUtensorMap tm_b, const ProductArgs p) {
+  using C = ProductCfg<NT>;
+  constexpr bool RAGGED_K = KIND == kProductGroups;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = ptx::smem_addr(smem_raw);
+  const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t ring = raw_addr + pad;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::S * C::STAGE);
+  int32_t* misc = reinterpret_cast<int32_t*>(bars + C::NUM_BARS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
+  volatile int32_t* abort_flag = misc + 1;
+  int32_t* s_off = misc + 4;
+  int32_t* s_start = s_off + kProductMaxGroups + 1;
+
+  const uint32_t bar0 = ptx::smem_addr(bars);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (C::S + s); };
+  auto landed = [&](int s) { return bar0 + 8u * (2 * C::S + s); };  // ragged last blocks
+  auto tfull = [&](int a) { return bar0 + 8u * (3 * C::S + a); };
+  auto tempty = [&](int a) { return bar0 + 8u * (3 * C::S + 2 + a); };
+  const uint32_t done_bar = bar0 + 8u * (3 * C::S + 4);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+  const int num_pairs = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::S; ++s) {
+      // ragged k: both CTAs arrive on the leader's barrier for every stage
+      ptx::mbar_init(full(s), RAGGED_K ? 2 : 1);
+      ptx::mbar_init(empty(s), 1);
+      ptx::mbar_init(landed(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(tfull(a), 1);
+      ptx::mbar_init(tempty(a), 2 * kPEpiWarps);
+    }
+    ptx::mbar_init(done_bar, 1);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tmap(&tm_a);
+    ptx::prefetch_tmap(&tm_b);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), C::TMEM_COLS);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  if constexpr (KIND != kProductDense) {
+    // group boundaries, made safe to index with: monotonic and inside the
+    // rows.  What had to be changed is reported, not followed.
+    for (int e = threadIdx.x; e <= p.groups; e += kPThreads) {
+      const int v = p.offsets[e];
+      const int c = min(max(v, 0), p.rows);
+      if (c != v) latch_status(p.status, kStatusDeviceCheck);
+      s_off[e] = c;
+    }
+    __syncthreads();
+    if (warp == 0) {  // running maximum, then tiles of each group
+      int top = 0, running = 0;
+      for (int base = 0; base <= p.groups; base += 32) {
+        const int e = base + lane;
+        int v = e <= p.groups ? s_off[e] : 0;
+        const int own = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int n = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v = max(v, n);
+        }
+        v = max(v, top);
+        if (e <= p.groups) {
+          if (v != own) latch_status(p.status, kStatusDeviceCheck);
+          s_off[e] = v;
+        }
+        top = __shfl_sync(0xffffffffu, v, 31);
+      }
+      __syncwarp();
+      if constexpr (KIND == kProductRows) {
+        const int mt = (p.M + kProductTileM - 1) / kProductTileM;
+        for (int base = 0; base < p.groups; base += 32) {
+          const int e = base + lane;
+          const int cnt = e < p.groups ? s_off[e + 1] - s_off[e] : 0;
+          const int v = mt * ((cnt + NT - 1) / NT);
+          int incl = v;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int n = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += n;
+          }
+          if (e < p.groups) s_start[e] = running + incl - v;
+          running += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (lane == 0) s_start[p.groups] = running;
+      }
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int num_tiles = product_tiles<NT, KIND>(p, s_start);
+  const Waiter W{abort_flag, p.status, p.wait_limit_ns};
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- producer
+    if (lane == 0) {
+      const uint64_t pol = ptx::policy_evict_normal();
+      int last_parity[C::S];
+#pragma unroll
+      for (int s = 0; s < C::S; ++s) last_parity[s] = -1;
+      int stage = 0;
+      uint32_t phase = 0;
+      uint64_t last_issue = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
+        const ProductTile t = product_tile<NT, KIND>(tile, p, s_off, s_start);
+        const int i = t.i0 + static_cast<int>(rank) * 128;
+        const int j = t.j0 + static_cast<int>(rank) * (t.n_mma / 2);
+        for (int kb = 0; kb < t.k_blocks; ++kb) {
+          if (!W.wait(empty(stage), phase ^ 1u)) {
+            ok = false;
+            break;
+          }
+          const uint32_t lead_full = ptx::map_to_rank(full(stage), 0);
+          uint32_t bar = lead_full;
+          if constexpr (RAGGED_K) {
+            if ((kb + 1) * kPBK > t.k_count) {
+              // the group's ragged last block: this CTA's own barrier, then
+              // the warp that clears foreign rows arrives on the leader's
+              bar = landed(stage);
+              ptx::mbar_arrive_expect_tx(bar, C::STAGE);
+              bar = ptx::map_to_rank(bar, rank);
+            } else if (leader) {
+              ptx::mbar_arrive_expect_tx(full(stage), 2 * C::STAGE);
+            } else {
+              ptx::mbar_arrive_cluster(lead_full);
+            }
+          } else {
+            if (leader) ptx::mbar_arrive_expect_tx(full(stage), 2 * C::STAGE);
+          }
+          const uint32_t sa = ring + stage * C::STAGE;
+          const uint32_t sb = sa + kPABytes;
+          int k = kb, za = t.z * p.a_z, zb = t.z;
+          if constexpr (KIND == kProductDense) {
+            if (kb >= p.k_wrap) {
+              k -= p.k_wrap;
+              za += p.wrap_za;
+              zb += p.wrap_zb;
+            }
+          }
+          k *= kPBK;
+          if constexpr (A_MN) {
+            const int ky = RAGGED_K ? t.k0 + k : k;
+            const int z = RAGGED_K ? 0 : za;
+            tma_load_3d_pair(sa, &tm_a, bar, i, ky, z, pol);
+            tma_load_3d_pair(sa + kAtom, &tm_a, bar, i + 64, ky, z, pol);
+          } else {
+            tma_load_3d_pair(sa, &tm_a, bar, k, i, za, pol);
+          }
+          if constexpr (B_MN) {
+            const int ky = RAGGED_K ? t.k0 + k : k;
+            const int z = RAGGED_K ? 0 : zb;
+#pragma unroll
+            for (int c = 0; c < NT / 128; ++c)
+              tma_load_3d_pair(sb + c * kAtom, &tm_b, bar, j + c * 64, ky, z, pol);
+          } else {
+            tma_load_3d_pair(sb, &tm_b, bar, k, j, KIND == kProductRows ? 0 : zb, pol);
+          }
+          last_issue = ptx::globaltimer();
+          last_parity[stage] = static_cast<int>(phase);
+          if (++stage == C::S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // No CTA exits with a copy into its shared memory in flight.  The
+      // leader's full barriers count both CTAs' bytes, so once it has seen
+      // its last phases complete the peer's copies have landed too, and the
+      // cluster barrier below keeps the peer until then.  After an abort the
+      // peer may have issued copies for phases the leader never armed, and
+      // either CTA copies that only its own landed barrier counts: they are
+      // given time to land.
+      if (!ok || *abort_flag) {
+        while (ptx::globaltimer() - last_issue < kPPeerDrainNs) {
+        }
+      } else if (leader) {
+#pragma unroll
+        for (int s = 0; s < C::S; ++s)
+          if (last_parity[s] >= 0) W.wait_final(full(s), static_cast<uint32_t>(last_parity[s]));
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0 && leader) {
+      const uint32_t fmt = p.in_type == kBf16 ? 1u : 0u;
+      const uint32_t idesc_m = (1u << 4) | (fmt << 7) | (fmt << 10) |
+                               (static_cast<uint32_t>(A_MN) << 15) |
+                               (static_cast<uint32_t>(B_MN) << 16) | ((256u >> 4) << 24);
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
+        const ProductTile t = product_tile<NT, KIND>(tile, p, s_off, s_start);
+        if (RAGGED_K && t.k_blocks == 0) continue;
+        const uint32_t idesc = idesc_m | (static_cast<uint32_t>(t.n_mma >> 3) << 17);
+        uint32_t d0 = 0;
+        for (int kb = 0; kb < t.k_blocks; ++kb) {
+          if (kb == 0 || (WIDE && kb % kWideBlocks == 0)) {
+            if (!W.wait(tempty(acc), acc_phase ^ 1u)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+            d0 = tmem_base + acc * NT;
+          }
+          if (!W.wait(full(stage), phase)) {
+            ok = false;
+            break;
+          }
+          // a cleared last block was also written by the peer's threads
+          if (RAGGED_K && (kb + 1) * kPBK > t.k_count) fence_acquire_cluster();
+          ptx::tc_fence_after();
+          const uint32_t sa = ring + stage * C::STAGE;
+          const uint32_t sb = sa + kPABytes;
+          const bool fresh = kb == 0 || (WIDE && kb % kWideBlocks == 0);
+          int steps = kPBK / 16;
+          if constexpr (RAGGED_K) steps = min(steps, (t.k_count - kb * kPBK + 15) / 16);
+#pragma unroll
+          for (int kk = 0; kk < kPBK / 16; ++kk) {
+            if (RAGGED_K && kk >= steps) break;
+            const uint64_t ad = A_MN ? sdesc_mn_sw128(sa + kk * 2048) : ptx::sdesc_sw128(sa + kk * 32);
+            const uint64_t bd = B_MN ? sdesc_mn_sw128(sb + kk * 2048) : ptx::sdesc_sw128(sb + kk * 32);
+            ptx::mma_bf16_pair(d0, ad, bd, idesc, (fresh && kk == 0) ? 0u : 1u);
+          }
+          ptx::mma_commit_pair_both(empty(stage));
+          if (++stage == C::S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (kb + 1 == t.k_blocks || (WIDE && (kb + 1) % kWideBlocks == 0)) {
+            ptx::mma_commit_pair_both(tfull(acc));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
+          }
+        }
+      }
+      // every MMA issued completes before TMEM is released
+      ptx::mma_commit_pair_self(done_bar);
+      W.wait_final(done_bar, 0);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------- foreign rows of ragged last blocks
+    if constexpr (RAGGED_K) {
+      int stage = 0;
+      uint32_t parity[C::S];
+#pragma unroll
+      for (int s = 0; s < C::S; ++s) parity[s] = 0;
+      for (int tile = pair; tile < num_tiles; tile += num_pairs) {
+        const ProductTile t = product_tile<NT, KIND>(tile, p, s_off, s_start);
+        stage = (stage + t.k_blocks) % C::S;
+        const int tail = t.k_count % kPBK;
+        if (tail == 0) continue;
+        const int s = (stage + C::S - 1) % C::S;
+        uint32_t par = 0;
+#pragma unroll
+        for (int q = 0; q < C::S; ++q)
+          if (q == s) {
+            par = parity[q];
+            parity[q] ^= 1u;
+          }
+        if (!W.wait(landed(s), par)) break;
+        const int last = (tail + 15) & ~15;
+        const uint32_t base = ring + s * C::STAGE;
+        // rows [tail, last) of every 64-element atom of both operands
+        constexpr int ATOMS = 2 + NT / 128;
+        const int n = (last - tail) * ATOMS * 8;
+        for (int q = lane; q < n; q += 32) {
+          const int row = tail + q / (ATOMS * 8);
+          const int atom = q / 8 % ATOMS;
+          const uint32_t at = base + atom * kAtom + row * 128 + (q & 7) * 16;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(full(s), 0));
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // TMEM lane quarter this warp may access
+    constexpr int GROUPS = kPEpiWarps / 4;
+    constexpr int COLS = NT / GROUPS < 16 ? 16 : NT / GROUPS;  // rows j per warp
+    const int col_begin = ((warp - 3) >> 2) * COLS;
+    const bool f16 = p.out_type == kF16;
+    // two columns per store where every address of it is 4-byte aligned
+    const bool paired = (p.M & 1) == 0 && (p.ld_out & 1) == 0 && (p.z_out & 1) == 0 &&
+                        (reinterpret_cast<uintptr_t>(p.out) & 3) == 0;
+    if constexpr (KIND == kProductRows) {
+      // rows outside every group are zero
+      const int first = s_off[0], last = s_off[p.groups];
+      const int64_t gap = static_cast<int64_t>(first) + (p.rows - last);
+      const int64_t n = gap * p.M;
+      const int64_t step = static_cast<int64_t>(gridDim.x) * (32 * kPEpiWarps);
+      for (int64_t at = static_cast<int64_t>(blockIdx.x) * (32 * kPEpiWarps) + (threadIdx.x - 96);
+           at < n; at += step) {
+        const int64_t r = at / p.M;
+        const int64_t dst = (r < first ? r : r - first + last) * p.ld_out + at % p.M;
+        if (WIDE)
+          static_cast<float*>(p.out)[dst] = 0.f;
+        else
+          static_cast<uint16_t*>(p.out)[dst] = 0;
+      }
+    }
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    bool ok = true;
+    for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
+      const ProductTile t = product_tile<NT, KIND>(tile, p, s_off, s_start);
+      const int i = t.i0 + static_cast<int>(rank) * 128 + q * 32 + lane;
+      const int64_t zbase = KIND == kProductRows ? 0 : static_cast<int64_t>(t.z) * p.z_out;
+      const int ncols = min(t.nvalid - col_begin, COLS);  // <= 0: nothing for this warp
+      if constexpr (WIDE) {
+        float sum[COLS];
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) sum[c] = 0.f;
+        for (int kb = 0; kb < t.k_blocks; kb += kWideBlocks) {
+          if (!W.wait(tfull(acc), acc_phase)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NT + col_begin;
+#pragma unroll
+          for (int c = 0; c < COLS; c += 16) {
+            if (c < ncols) {
+              uint32_t r[16];
+              ptx::tmem_ld16(tq + c, r);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int u = 0; u < 16; ++u) sum[c + u] += __uint_as_float(r[u]);
+            }
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(tempty(acc), 0));
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
+        }
+        if (!ok) break;
+        if (i < p.M) {
+          float* dst = static_cast<float*>(p.out) + zbase +
+                       (static_cast<int64_t>(t.j0) + col_begin) * p.ld_out + i;
+#pragma unroll
+          for (int c = 0; c < COLS; ++c) {
+            if (c < ncols) {
+              float* at = dst + c * p.ld_out;
+              __stcs(at, p.accumulate ? *at + sum[c] : sum[c]);
+            }
+          }
+        }
+      } else {
+        const bool live = t.k_blocks > 0;
+        if (live) {
+          if (!W.wait(tfull(acc), acc_phase)) break;
+          ptx::tc_fence_after();
+        }
+        const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NT + col_begin;
+        float alpha = p.alpha;
+        if (KIND == kProductDense && p.alpha_z) alpha *= p.alpha_z[t.z];
+        uint16_t* out = static_cast<uint16_t*>(p.out) + zbase;
+        const uint16_t* add = KIND == kProductDense && p.add ? p.add + zbase : nullptr;
+        uint32_t packed[COLS / 2];  // rows (2c, 2c + 1) of this lane's column
+#pragma unroll
+        for (int c = 0; c < COLS; c += 16) {
+          if (c < ncols) {
+            uint32_t r[16];
+            float extra[16];
+            if (live) ptx::tmem_ld16(tq + c, r);
+            if (KIND == kProductDense) {
+#pragma unroll
+              for (int u = 0; u < 16; ++u) {
+                const int j = t.j0 + col_begin + c + u;
+                extra[u] = (add && i < p.M && c + u < ncols)
+                               ? p.beta * __half2float(__ushort_as_half(add[static_cast<int64_t>(j) * p.ld_out + i]))
+                               : 0.f;
+                if (j == i) extra[u] += p.diag;
+              }
+            }
+            if (live) ptx::tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 16; u += 2) {
+              float v0 = live ? __uint_as_float(r[u]) : 0.f;
+              float v1 = live ? __uint_as_float(r[u + 1]) : 0.f;
+              if (KIND == kProductDense) {
+                v0 = fmaf(alpha, v0, extra[u]);
+                v1 = fmaf(alpha, v1, extra[u + 1]);
+              }
+              packed[(c + u) / 2] = to16(v0, f16) | (to16(v1, f16) << 16);
+            }
+          }
+        }
+        if (live) {
+          // the accumulator is free before any store
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(tempty(acc), 0));
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
+        }
+        const int64_t j = static_cast<int64_t>(t.j0) + col_begin;
+        if (paired) {
+          uint16_t* dst = out + (j + (lane & 1)) * p.ld_out + (i & ~1);
+#pragma unroll
+          for (int c = 0; c < COLS; c += 2) {
+            if (c < ncols) {  // the same on every lane of the warp
+              const uint32_t v = swap_pair(packed[c / 2], lane);
+              if (i < p.M && c + (lane & 1) < ncols)
+                *reinterpret_cast<uint32_t*>(dst + c * p.ld_out) = v;
+            }
+          }
+        } else if (i < p.M) {
+          uint16_t* dst = out + j * p.ld_out + i;
+#pragma unroll
+          for (int c = 0; c < COLS; ++c)
+            if (c < ncols)
+              dst[c * p.ld_out] = static_cast<uint16_t>(packed[c / 2] >> (16 * (c & 1)));
+        }
+        if (KIND == kProductDense && p.symmetric && t.j0 >= t.i0 + kProductTileM && i < p.M) {
+          // the mirror image: row i, columns j (16 at a time; rows are padded
+          // to multiples of 16 elements)
+          uint16_t* dst = out + static_cast<int64_t>(i) * p.ld_out + j;
+#pragma unroll
+          for (int c = 0; c < COLS; c += 8)
+            if (c < ncols)
+              *reinterpret_cast<uint4*>(dst + c) = make_uint4(packed[c / 2], packed[c / 2 + 1],
+                                                              packed[c / 2 + 2], packed[c / 2 + 3]);
+        }
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  // no signal, copy or MMA read crosses between the two CTAs after this
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+  }
+}
+
+}  // namespace
+}  // namespace beam

@@ -1,0 +1,508 @@
+// Host side of the training operators declared in include/beam_moe.h:
+// grouped products with their gradients, the gated activation, and the
+// orthogonalised update.  Argument checks, workspace carve-up, tensor maps
+// and launches on the caller's stream; no allocation, no synchronisation.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/beam_moe.h"
+#include "common.cuh"
+#include "host.cuh"
+#include "pair_product.cuh"
+#include "train_ops.cuh"
+
+namespace {
+
+using beam::ProductArgs;
+using beam::host::align_up;
+using beam::host::aligned16;
+using beam::host::kAlign;
+
+constexpr int64_t kMaxExtent = int64_t(1) << 30;   // rows, widths: int32 TMA coordinates
+constexpr int64_t kMaxStride = int64_t(1) << 38;   // elements; TMA strides are below 2^40 bytes
+
+int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+
+bool is16(int32_t t) { return t == BEAM_DTYPE_BF16 || t == BEAM_DTYPE_F16; }
+bool known_type(int32_t t) { return is16(t) || t == BEAM_DTYPE_F32; }
+size_t type_bytes(int32_t t) { return t == BEAM_DTYPE_F32 ? 4 : 2; }
+
+// 16-bit tensor [z][outer][inner] (inner contiguous), box {64, box_rows, 1},
+// 128-byte swizzle.
+bool tmap3(CUtensorMap* m, const void* base, int32_t type, int64_t inner, int64_t outer, int64_t z,
+           int64_t ld, int64_t zs, uint32_t box_rows) {
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer),
+                        static_cast<cuuint64_t>(z)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(zs) * 2};
+  cuuint32_t box[3] = {64, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return beam::host::g_encode(
+             m, type == BEAM_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+             3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+beam_status_t device_ready(beam::host::DevInfo* dev) {
+  if (!beam::host::device_info(dev)) return BEAM_ERR_CUDA;
+  if (!dev->supported) return BEAM_ERR_UNSUPPORTED;
+  return BEAM_OK;
+}
+
+beam_status_t launched(cudaError_t e) { return e == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA; }
+
+// ------------------------------------------------------------------ operands
+// A 16-bit operand [z][outer][inner]: where TMA can read it in place (16-byte
+// base and strides) it does, else an aligned copy in the workspace stands in.
+struct Operand {
+  const void* base;
+  int64_t inner, outer, z;
+  int64_t ld, zs;   // elements between outer rows, between z
+
+  void normalise() {
+    if (outer <= 1) ld = round_up(inner, 8);
+    if (z <= 1) zs = std::max<int64_t>(ld * outer, 8) / 8 * 8;
+  }
+  bool in_place() const {
+    return (reinterpret_cast<uintptr_t>(base) & 15u) == 0 && ld % 8 == 0 && zs % 8 == 0;
+  }
+  size_t packed_bytes() const {
+    return align_up(static_cast<size_t>(z) * outer * round_up(inner, 8) * 2);
+  }
+  void pack_into(void* dst, cudaStream_t s) {
+    beam::PackArgs p;
+    p.src = static_cast<const uint16_t*>(base);
+    p.sz = zs;
+    p.sr = ld;
+    p.sc = 1;
+    p.zs = z;
+    p.rows = outer;
+    p.cols = static_cast<int32_t>(inner);
+    p.ld = static_cast<int32_t>(round_up(inner, 8));
+    p.dst = static_cast<uint16_t*>(dst);
+    beam::launch_pack(p, s);
+    base = dst;
+    ld = p.ld;
+    zs = ld * outer;
+  }
+};
+
+bool good_ld(int64_t ld, int64_t width) { return ld >= width && ld <= kMaxStride; }
+
+bool valid_grouped(const beam_moe_grouped_t* g) {
+  if (!g) return false;
+  if (g->n_groups < 1 || g->n_groups > beam::kProductMaxGroups) return false;
+  if (g->rows < 0 || g->rows > kMaxExtent || g->N < 1 || g->N > kMaxExtent || g->K < 1 ||
+      g->K > kMaxExtent)
+    return false;
+  if (!is16(g->dtype) || !(g->out_dtype == g->dtype || g->out_dtype == BEAM_DTYPE_F32)) return false;
+  if (!good_ld(g->x_ld, g->K) || !good_ld(g->y_ld, g->N)) return false;
+  // one axis of W contiguous, the other stepping past it, groups apart or shared
+  const int64_t e = g->w_stride_e, n = g->w_stride_n, k = g->w_stride_k;
+  const bool k_inner = k == 1 && (g->N == 1 || good_ld(n, g->K));
+  const bool n_inner = n == 1 && (g->K == 1 || good_ld(k, g->N));
+  if (!k_inner && !n_inner) return false;
+  if (e < 0 || e > kMaxStride) return false;
+  return true;
+}
+
+bool w_k_inner(const beam_moe_grouped_t& g) {
+  return g.w_stride_k == 1 && (g.N == 1 || good_ld(g.w_stride_n, g.K));
+}
+
+Operand operand_x(const beam_moe_grouped_t& g, const void* x) {
+  Operand o{x, g.K, g.rows, 1, g.x_ld, 0};
+  o.normalise();
+  return o;
+}
+Operand operand_y(const beam_moe_grouped_t& g, const void* y) {
+  Operand o{y, g.N, g.rows, 1, g.y_ld, 0};
+  o.normalise();
+  return o;
+}
+Operand operand_w(const beam_moe_grouped_t& g, const void* w) {
+  const bool ki = w_k_inner(g);
+  // groups that share one matrix (stride 0) read it as a stack of one
+  const int64_t z = g.n_groups > 1 && g.w_stride_e == 0 ? 1 : g.n_groups;
+  Operand o{w, ki ? g.K : g.N, ki ? g.N : g.K, z, ki ? g.w_stride_n : g.w_stride_k, g.w_stride_e};
+  o.normalise();
+  return o;
+}
+
+// Rows per tile.  A tile costs at least its weights' bytes whatever its rows,
+// so the tile follows the mean group: narrow tiles leave the ring to weight
+// stages (12 in flight instead of 6) and load no rows of later groups; wide
+// ones read each weight once for up to 256 rows.
+int rows_tile(const beam_moe_grouped_t& g) {
+  const int64_t mean = g.rows / g.n_groups;
+  return mean <= 12 ? 32 : mean <= 40 ? 64 : mean <= 96 ? 128 : 256;
+}
+
+// Common tail of the three products.
+beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool a_mn, bool b_mn,
+                             Operand a, Operand b, int64_t M, int64_t N, int64_t k,
+                             const int32_t* offsets, void* out, int64_t ld_out, int64_t z_out,
+                             int accumulate, void* ws, size_t ws_bytes, cudaStream_t s) {
+  const bool pack_a = !a.in_place(), pack_b = !b.in_place();
+  size_t need = kAlign;
+  const size_t at_a = need;
+  if (pack_a) need += a.packed_bytes();
+  const size_t at_b = need;
+  if (pack_b) need += b.packed_bytes();
+  if (ws_bytes < need) return BEAM_ERR_WORKSPACE;
+  beam::host::DevInfo dev;
+  const beam_status_t st = device_ready(&dev);
+  if (st != BEAM_OK) return st;
+  if (!beam::host::encoder()) return BEAM_ERR_CUDA;
+  if (pack_a) a.pack_into(static_cast<uint8_t*>(ws) + at_a, s);
+  if (pack_b) b.pack_into(static_cast<uint8_t*>(ws) + at_b, s);
+  CUtensorMap ta, tb;
+  if (!tmap3(&ta, a.base, g.dtype, a.inner, a.outer, a.z, a.ld, a.zs, a_mn ? 64 : 128) ||
+      !tmap3(&tb, b.base, g.dtype, b.inner, b.outer, b.z, b.ld, b.zs, b_mn ? 64 : nt / 2))
+    return BEAM_ERR_CUDA;
+  ProductArgs p = {};
+  p.M = static_cast<int32_t>(M);
+  p.N = static_cast<int32_t>(N);
+  p.k_blocks = static_cast<int32_t>((k + 63) / 64);
+  p.k_wrap = p.k_blocks;
+  p.a_z = a.z > 1 ? 1 : 0;
+  p.groups = g.n_groups;
+  p.rows = static_cast<int32_t>(g.rows);
+  p.offsets = offsets;
+  p.out = out;
+  p.ld_out = ld_out;
+  p.z_out = z_out;
+  p.out_type = g.out_dtype;
+  p.in_type = g.dtype;
+  p.accumulate = accumulate;
+  p.alpha = 1.f;
+  p.status = static_cast<uint32_t*>(ws);
+  p.wait_limit_ns = beam::host::wait_limit_ns();
+  return launched(beam::launch_pair_product(kind, nt, a_mn, b_mn, ta, tb, p, false, s));
+}
+
+// ------------------------------------------------------ orthogonalised update
+// F16 scales of the three intermediates (powers of two; see the kernel's
+// note in beam_moe_orthogonalize): singular values stay near or below one,
+// so elements stay below these and the small ones keep their bits.
+constexpr float kScaleX = 1024.f, kScaleGram = 1024.f, kScalePoly = 256.f;
+
+struct OrthoLayout {
+  int64_t m, ld, ldm;   // smaller extent, row strides of X and of the m x m products
+  size_t amax, sumsq, alpha_gram, alpha_step, x0, x1, gram, poly, total;
+};
+
+bool ortho_layout(int32_t batch, int32_t rows, int32_t cols, int32_t dtype, OrthoLayout* L) {
+  if (batch < 0 || batch > 65535 || rows < 0 || cols < 0 || rows > 65536 || cols > 65536 ||
+      !known_type(dtype))
+    return false;
+  L->m = std::min(rows, cols);
+  L->ld = round_up(cols, 64);
+  L->ldm = round_up(L->m, 64);
+  size_t off = kAlign;  // status word
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align_up(off + bytes);
+    return at;
+  };
+  const size_t x = static_cast<size_t>(batch) * rows * L->ld * 2;
+  const size_t mm = static_cast<size_t>(batch) * L->m * L->ldm * 2;
+  L->amax = take(static_cast<size_t>(batch) * beam::kNormBlocks * 4);
+  L->sumsq = take(static_cast<size_t>(batch) * beam::kNormBlocks * 4);
+  L->alpha_gram = take(static_cast<size_t>(batch) * 4);
+  L->alpha_step = take(static_cast<size_t>(batch) * 4);
+  // a 32-bit update starts as two F16 parts, stacked
+  L->x0 = take(dtype == BEAM_DTYPE_F32 ? 2 * x : x);
+  L->x1 = take(x);
+  L->gram = take(mm);
+  L->poly = take(mm);
+  L->total = off;
+  return true;
+}
+
+template <typename T>
+T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t beam_moe_grouped_matmul_workspace_size(const beam_moe_grouped_t* g, int32_t unaligned) {
+  if (!valid_grouped(g)) return 0;
+  size_t need = kAlign;
+  // a null base stands for an aligned one
+  const Operand ops[3] = {operand_x(*g, nullptr), operand_y(*g, nullptr), operand_w(*g, nullptr)};
+  for (const Operand& o : ops)
+    if (unaligned || !o.in_place()) need += o.packed_bytes();
+  return need;
+}
+
+beam_status_t beam_moe_grouped_matmul(const beam_moe_grouped_t* g, const void* x, const void* w,
+                                      const int32_t* offsets, void* y, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+  if (!valid_grouped(g)) return BEAM_ERR_INVALID_ARG;
+  if (g->rows == 0) return BEAM_OK;
+  if (!x || !w || !offsets || !y || !aligned16(workspace)) return BEAM_ERR_INVALID_ARG;
+  return grouped_launch(*g, beam::kProductRows, rows_tile(*g), !w_k_inner(*g), false,
+                        operand_w(*g, w), operand_x(*g, x), g->N, g->rows, g->K, offsets, y,
+                        g->y_ld, 0, 0, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+beam_status_t beam_moe_grouped_matmul_dx(const beam_moe_grouped_t* g, const void* dy,
+                                         const void* w, const int32_t* offsets, void* dx,
+                                         void* workspace, size_t ws_bytes, void* stream) {
+  if (!valid_grouped(g)) return BEAM_ERR_INVALID_ARG;
+  if (g->rows == 0) return BEAM_OK;
+  if (!dy || !w || !offsets || !dx || !aligned16(workspace)) return BEAM_ERR_INVALID_ARG;
+  return grouped_launch(*g, beam::kProductRows, rows_tile(*g), w_k_inner(*g), false,
+                        operand_w(*g, w), operand_y(*g, dy), g->K, g->rows, g->N, offsets, dx,
+                        g->x_ld, 0, 0, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+beam_status_t beam_moe_grouped_matmul_dw(const beam_moe_grouped_t* g, const void* dy,
+                                         const void* x, const int32_t* offsets, int32_t accumulate,
+                                         void* dw, void* workspace, size_t ws_bytes,
+                                         void* stream) {
+  if (!valid_grouped(g)) return BEAM_ERR_INVALID_ARG;
+  // the gradient is written dense, and only 32-bit sums are added to
+  if (accumulate && g->out_dtype != BEAM_DTYPE_F32) return BEAM_ERR_INVALID_ARG;
+  if (!dw || !aligned16(workspace)) return BEAM_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t per = static_cast<int64_t>(g->N) * g->K;
+  if (g->rows == 0) {
+    if (accumulate) return BEAM_OK;
+    return launched(cudaMemsetAsync(dw, 0, g->n_groups * per * type_bytes(g->out_dtype), s));
+  }
+  if (!dy || !x || !offsets) return BEAM_ERR_INVALID_ARG;
+  return grouped_launch(*g, beam::kProductGroups, 256, true, true, operand_x(*g, x),
+                        operand_y(*g, dy), g->K, g->N, 0, offsets, dw, g->K, per,
+                        accumulate ? 1 : 0, workspace, ws_bytes, s);
+}
+
+static beam_status_t gate_checks(const beam_moe_gate_t* d, beam::host::DevInfo* dev, bool* empty) {
+  if (!d || d->rows < 0 || d->F < 0 || d->F > kMaxExtent || !is16(d->dtype))
+    return BEAM_ERR_INVALID_ARG;
+  *empty = d->rows == 0;
+  if (*empty) return BEAM_OK;
+  if (d->F > 0 && (!good_ld(d->gate_ld, d->F) || !good_ld(d->up_ld, d->F)))
+    return BEAM_ERR_INVALID_ARG;
+  return device_ready(dev);
+}
+
+beam_status_t beam_moe_swiglu(const beam_moe_gate_t* d, const void* gate, const void* up,
+                              const float* row_w, void* h, int64_t h_ld, void* stream) {
+  beam::host::DevInfo dev;
+  bool empty = false;
+  const beam_status_t st = gate_checks(d, &dev, &empty);
+  if (st != BEAM_OK) return st;
+  if (empty || d->F == 0) return BEAM_OK;
+  if (!gate || !up || !h || !good_ld(h_ld, d->F)) return BEAM_ERR_INVALID_ARG;
+  beam::GateArgs p = {};
+  p.gate = gate;
+  p.up = up;
+  p.row_w = row_w;
+  p.h = h;
+  p.ld_gate = d->gate_ld;
+  p.ld_up = d->up_ld;
+  p.ld_h = h_ld;
+  p.rows = d->rows;
+  p.F = d->F;
+  p.type = d->dtype;
+  beam::launch_gate(p, dev.sms, static_cast<cudaStream_t>(stream));
+  return launched(cudaGetLastError());
+}
+
+beam_status_t beam_moe_swiglu_grad(const beam_moe_gate_t* d, const void* dh, int64_t dh_ld,
+                                   const void* gate, const void* up, const float* row_w,
+                                   void* dgate, int64_t dgate_ld, void* dup, int64_t dup_ld,
+                                   float* drow_w, void* stream) {
+  beam::host::DevInfo dev;
+  bool empty = false;
+  const beam_status_t st = gate_checks(d, &dev, &empty);
+  if (st != BEAM_OK) return st;
+  if (empty) return BEAM_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d->F == 0)  // an empty sum
+    return drow_w ? launched(cudaMemsetAsync(drow_w, 0, d->rows * sizeof(float), s)) : BEAM_OK;
+  if (!dh || !gate || !up || !dgate || !dup || !good_ld(dh_ld, d->F) ||
+      !good_ld(dgate_ld, d->F) || !good_ld(dup_ld, d->F))
+    return BEAM_ERR_INVALID_ARG;
+  beam::GateArgs p = {};
+  p.gate = gate;
+  p.up = up;
+  p.dh = dh;
+  p.row_w = row_w;
+  p.dgate = dgate;
+  p.dup = dup;
+  p.drow_w = drow_w;
+  p.ld_gate = d->gate_ld;
+  p.ld_up = d->up_ld;
+  p.ld_dh = dh_ld;
+  p.ld_dgate = dgate_ld;
+  p.ld_dup = dup_ld;
+  p.rows = d->rows;
+  p.F = d->F;
+  p.type = d->dtype;
+  beam::launch_gate_grad(p, dev.sms, s);
+  return launched(cudaGetLastError());
+}
+
+size_t beam_moe_orthogonalize_workspace_size(int32_t batch, int32_t rows, int32_t cols,
+                                             int32_t dtype) {
+  OrthoLayout L;
+  return ortho_layout(batch, rows, cols, dtype, &L) ? L.total : 0;
+}
+
+// Newton-Schulz steps X <- (a I + b A + c A^2) X, A = X X^T, in F16 operands
+// with FP32 sums.  F16 rather than BF16: the same tensor rate, and 11 bits
+// instead of 8 -- against 64 bits the result is off by 1-2e-3 of its norm
+// where BF16 intermediates give 1-3e-2 (an error of X0 grows by a, the slope
+// of the polynomial at 0, in every step).  Its narrower exponent is covered
+// by powers of two: X and A are held times 1024, the polynomial times 256.
+// The first step's X is the update's own bits times a power of two (exact for
+// 16-bit updates; a 32-bit one keeps a second F16 part that the first
+// X <- P X adds in), its norm a factor of the epilogues.  Both m x m products
+// are symmetric: one triangle of tiles is computed.  a X is folded into the
+// polynomial's diagonal, so X <- P X reads no addend.
+beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src, void* out,
+                                     void* workspace, size_t ws_bytes, void* stream) {
+  OrthoLayout L;
+  if (!d || !ortho_layout(d->batch, d->rows, d->cols, d->dtype, &L) || !is16(d->out_dtype) ||
+      d->steps < 1 || d->steps > 64 || !(d->eps >= 0.f) || !(d->eps <= 1e30f))
+    return BEAM_ERR_INVALID_ARG;
+  for (float c : {d->a, d->b, d->c})
+    if (!(std::fabs(c) <= 16.f)) return BEAM_ERR_INVALID_ARG;
+  if (d->batch == 0 || d->rows == 0 || d->cols == 0) return BEAM_OK;
+  if (!src || !out || !aligned16(workspace)) return BEAM_ERR_INVALID_ARG;
+  if (ws_bytes < L.total) return BEAM_ERR_WORKSPACE;
+  beam::host::DevInfo dev;
+  const beam_status_t st = device_ready(&dev);
+  if (st != BEAM_OK) return st;
+  if (!beam::host::encoder()) return BEAM_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+  const int64_t batch = d->batch, R = d->rows, C = d->cols, m = L.m;
+  const bool wide = R <= C;
+  const bool split = d->dtype == BEAM_DTYPE_F32;
+  uint16_t* x[2] = {at<uint16_t>(workspace, L.x0), at<uint16_t>(workspace, L.x1)};
+  uint16_t* gram = at<uint16_t>(workspace, L.gram);
+  uint16_t* poly = at<uint16_t>(workspace, L.poly);
+
+  beam::NormArgs n = {};
+  n.src = src;
+  n.sz = d->stride_batch;
+  n.sr = d->stride_row;
+  n.sc = d->stride_col;
+  n.batch = d->batch;
+  n.rows = d->rows;
+  n.cols = d->cols;
+  n.type = d->dtype;
+  n.blocks = static_cast<int32_t>(
+      std::min<int64_t>(beam::kNormBlocks, (R * C + 2047) / 2048));
+  n.amax = at<uint32_t>(workspace, L.amax);
+  n.sumsq = at<float>(workspace, L.sumsq);
+  n.hi = x[0];
+  n.lo = split ? x[0] + batch * R * L.ld : nullptr;
+  n.ld = L.ld;
+  n.alpha_gram = at<float>(workspace, L.alpha_gram);
+  n.alpha_step = at<float>(workspace, L.alpha_step);
+  n.scale_gram = kScaleGram;
+  n.scale_step = (d->steps == 1 ? 1.f : kScaleX) / kScalePoly;
+  n.eps = d->eps;
+  if (beam::launch_norm(n, s) != cudaSuccess) return BEAM_ERR_CUDA;
+
+  // rows j per tile: narrow tiles where wide ones would leave SMs idle
+  const int64_t sms2 = dev.sms / 2;
+  auto tiles = [&](int64_t cols_, int64_t rows_, int nt) {
+    return batch * ((cols_ + 255) / 256) * ((rows_ + nt - 1) / nt);
+  };
+  const int nt_gram = tiles(m, m, 256) / 2 >= sms2 ? 256 : wide ? 64 : 128;
+  const int nt_poly = tiles(m, m, 256) / 2 >= sms2 ? 256 : 64;
+  const int nt_step = tiles(C, R, 256) >= sms2 ? 256 : 64;
+
+  const int32_t F16 = BEAM_DTYPE_F16;
+  CUtensorMap ga[2], gb[2], pa, pb, sx[2], sp;  // gram, polynomial, step
+  for (int i = 0; i < 2; ++i) {
+    const int64_t z = i == 0 && split ? 2 * batch : batch;
+    if (!tmap3(&ga[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? 128 : 64) ||
+        !tmap3(&gb[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? nt_gram / 2 : 64) ||
+        !tmap3(&sx[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? 64 : nt_step / 2))
+      return BEAM_ERR_CUDA;
+  }
+  if (!tmap3(&pa, gram, F16, m, m, batch, L.ldm, m * L.ldm, 128) ||
+      !tmap3(&pb, gram, F16, m, m, batch, L.ldm, m * L.ldm, nt_poly / 2) ||
+      !tmap3(&sp, poly, F16, m, m, batch, L.ldm, m * L.ldm, wide ? nt_step / 2 : 128))
+    return BEAM_ERR_CUDA;
+
+  ProductArgs base = {};
+  base.a_z = 1;
+  base.groups = d->batch;
+  base.in_type = F16;
+  base.out_type = F16;
+  base.status = static_cast<uint32_t*>(workspace);
+  base.wait_limit_ns = beam::host::wait_limit_ns();
+  for (int t = 0; t < d->steps; ++t) {
+    const bool last = t + 1 == d->steps;
+    const int cur = t & 1;
+    ProductArgs g = base;  // A = X X^T (wide) or X^T X (tall)
+    g.M = g.N = static_cast<int32_t>(m);
+    g.k_blocks = static_cast<int32_t>((std::max(R, C) + 63) / 64);
+    g.k_wrap = g.k_blocks;
+    g.out = gram;
+    g.ld_out = L.ldm;
+    g.z_out = m * L.ldm;
+    g.symmetric = 1;
+    g.alpha = t == 0 ? 1.f : kScaleGram / (kScaleX * kScaleX);
+    g.alpha_z = t == 0 ? n.alpha_gram : nullptr;
+    cudaError_t e = beam::launch_pair_product(beam::kProductDense, nt_gram, !wide, !wide, ga[cur],
+                                              gb[cur], g, true, s);
+    if (e != cudaSuccess) return BEAM_ERR_CUDA;
+
+    ProductArgs q = base;  // P = a I + b A + c A A
+    q.M = q.N = static_cast<int32_t>(m);
+    q.k_blocks = static_cast<int32_t>((m + 63) / 64);
+    q.k_wrap = q.k_blocks;
+    q.out = poly;
+    q.ld_out = L.ldm;
+    q.z_out = m * L.ldm;
+    q.symmetric = 1;
+    q.alpha = kScalePoly * d->c / (kScaleGram * kScaleGram);
+    q.beta = kScalePoly * d->b / kScaleGram;
+    q.diag = kScalePoly * d->a;
+    q.add = gram;
+    e = beam::launch_pair_product(beam::kProductDense, nt_poly, false, false, pa, pb, q, true, s);
+    if (e != cudaSuccess) return BEAM_ERR_CUDA;
+
+    ProductArgs u = base;  // X <- P X (wide) or X P (tall)
+    u.M = d->cols;
+    u.N = d->rows;
+    u.k_blocks = q.k_blocks;
+    u.k_wrap = q.k_blocks;
+    if (t == 0 && split) {
+      u.k_blocks *= 2;
+      (wide ? u.wrap_za : u.wrap_zb) = d->batch;
+    }
+    u.out = last ? out : x[cur ^ 1];
+    u.out_type = last ? d->out_dtype : F16;
+    u.ld_out = last ? C : L.ld;
+    u.z_out = last ? R * C : R * L.ld;
+    const float out_scale = last ? 1.f : kScaleX;
+    u.alpha = t == 0 ? 1.f : out_scale / (kScalePoly * kScaleX);
+    u.alpha_z = t == 0 ? n.alpha_step : nullptr;
+    e = wide ? beam::launch_pair_product(beam::kProductDense, nt_step, true, false, sx[cur], sp, u,
+                                         true, s)
+             : beam::launch_pair_product(beam::kProductDense, nt_step, false, false, sp, sx[cur],
+                                         u, true, s);
+    if (e != cudaSuccess) return BEAM_ERR_CUDA;
+  }
+  return BEAM_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,353 @@
+// Memory-bound kernels of the training operators: aligned copies of operands
+// TMA cannot address, the gated activation with its gradient, and the scaled
+// start of the orthogonalised update.
+#include "train_ops.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "launch_once.cuh"
+#include "pair_product.cuh"
+#include "ptx.cuh"
+
+namespace beam {
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+
+template <bool F16>
+__device__ __forceinline__ float from16(uint32_t bits) {
+  return F16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(bits)))
+             : __uint_as_float(bits << 16);
+}
+
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (F16) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+// ------------------------------------------------------------ aligned copies
+// One thread per 8 elements of the destination: the store is one 16-byte
+// word; the source is read element by element, as its alignment allows no
+// more.  Memory bound (2 bytes read, 2 written per element).
+__global__ void __launch_bounds__(256) pack_kernel(const PackArgs p) {
+  const int64_t words = p.zs * p.rows * (p.ld / 8);
+  for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < words;
+       at += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t row = at / (p.ld / 8);
+    const int c = static_cast<int>(at - row * (p.ld / 8)) * 8;
+    const int64_t z = row / p.rows;
+    const uint16_t* src = p.src + z * p.sz + (row - z * p.rows) * p.sr;
+    uint32_t v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = c + u < p.cols ? src[(c + u) * p.sc] : 0u;
+    *reinterpret_cast<uint4*>(p.dst + row * p.ld + c) =
+        make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  }
+}
+
+// -------------------------------------------------------------- gated rows
+// h = w_r * g * sigma(g) * u with sigma(g) = 1 / (1 + e^-g), in FP32, rounded
+// once.  Fast exponential and divide: a few parts in 10^7, far below the
+// 16-bit results and, averaged over a row, below FP32 summation error in dw.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+
+// Eight consecutive elements, as one 16-byte access where rows are aligned.
+template <bool VEC>
+__device__ __forceinline__ uint4 load8(const uint16_t* p, int n) {
+  if constexpr (VEC) {
+    return __ldcs(reinterpret_cast<const uint4*>(p));
+  } else {
+    uint32_t v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = u < n ? p[u] : 0u;
+    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(uint16_t* p, int n, const uint32_t (&v)[4]) {
+  if constexpr (VEC) {
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(v[0], v[1], v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (u < n) p[u] = static_cast<uint16_t>(v[u / 2] >> (16 * (u & 1)));
+  }
+}
+
+template <bool F16, bool VEC>
+__global__ void __launch_bounds__(256) gate_kernel(const GateArgs p) {
+  const int per_row = (p.F + 7) / 8;
+  const int64_t n = p.rows * per_row;
+  for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < n;
+       at += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = at / per_row;
+    const int c = static_cast<int>(at - r * per_row) * 8;
+    const uint4 gv = load8<VEC>(static_cast<const uint16_t*>(p.gate) + r * p.ld_gate + c, p.F - c);
+    const uint4 uv = load8<VEC>(static_cast<const uint16_t*>(p.up) + r * p.ld_up + c, p.F - c);
+    const float w = p.row_w ? p.row_w[r] : 1.f;
+    const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w}, uw[4] = {uv.x, uv.y, uv.z, uv.w};
+    uint32_t out[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float h[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const float g = from16<F16>(gw[k] >> (16 * b) & 0xffffu);
+        const float u = from16<F16>(uw[k] >> (16 * b) & 0xffffu);
+        h[b] = w * g * sigmoid(g) * u;
+      }
+      out[k] = pack16<F16>(h[0], h[1]);
+    }
+    store8<VEC>(static_cast<uint16_t*>(p.h) + r * p.ld_h + c, p.F - c, out);
+  }
+}
+
+// dg = dh w u s (1 + g (1 - s)), du = dh w g s, dw_r = sum_f dh g s u, with
+// s = sigma(g).  TPR threads share a row and sum dw_r in a fixed order: a
+// warp when the rows alone fill the GPU, else the whole block.
+template <bool F16, bool VEC, int TPR>
+__global__ void __launch_bounds__(256) gate_grad_kernel(const GateArgs p) {
+  constexpr int ROWS = 256 / TPR;
+  __shared__ float part[8];
+  const int t = threadIdx.x % TPR;
+  const int per_row = (p.F + 7) / 8;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * ROWS; base < p.rows;
+       base += static_cast<int64_t>(gridDim.x) * ROWS) {
+    const int64_t r = base + threadIdx.x / TPR;
+    float dw = 0.f;
+    if (r < p.rows) {
+      const float w = p.row_w ? p.row_w[r] : 1.f;
+      const uint16_t* gp = static_cast<const uint16_t*>(p.gate) + r * p.ld_gate;
+      const uint16_t* up = static_cast<const uint16_t*>(p.up) + r * p.ld_up;
+      const uint16_t* hp = static_cast<const uint16_t*>(p.dh) + r * p.ld_dh;
+      uint16_t* dgp = static_cast<uint16_t*>(p.dgate) + r * p.ld_dgate;
+      uint16_t* dup = static_cast<uint16_t*>(p.dup) + r * p.ld_dup;
+#pragma unroll 2
+      for (int q = t; q < per_row; q += TPR) {
+        const int c = q * 8;
+        const uint4 gv = load8<VEC>(gp + c, p.F - c);
+        const uint4 uv = load8<VEC>(up + c, p.F - c);
+        const uint4 hv = load8<VEC>(hp + c, p.F - c);
+        const uint32_t gw[4] = {gv.x, gv.y, gv.z, gv.w}, uw[4] = {uv.x, uv.y, uv.z, uv.w},
+                       hw[4] = {hv.x, hv.y, hv.z, hv.w};
+        uint32_t og[4], ou[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float dg[2], du[2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float g = from16<F16>(gw[k] >> (16 * b) & 0xffffu);
+            const float u = from16<F16>(uw[k] >> (16 * b) & 0xffffu);
+            const float d = from16<F16>(hw[k] >> (16 * b) & 0xffffu);
+            const float s = sigmoid(g);
+            const float gs = g * s;
+            const float dgs = d * gs;
+            dg[b] = d * w * u * (s * (1.f + g * (1.f - s)));
+            du[b] = dgs * w;
+            // elements past the row's end hold g = u = dh = 0
+            dw = fmaf(dgs, u, dw);
+          }
+          og[k] = pack16<F16>(dg[0], dg[1]);
+          ou[k] = pack16<F16>(du[0], du[1]);
+        }
+        store8<VEC>(dgp + c, p.F - c, og);
+        store8<VEC>(dup + c, p.F - c, ou);
+      }
+    }
+    if (p.drow_w) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) dw += __shfl_xor_sync(kAll, dw, o);
+      if constexpr (TPR == 32) {
+        if (t == 0 && r < p.rows) p.drow_w[r] = dw;
+      } else {
+        if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = dw;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          float sum = 0.f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum += part[k];
+          p.drow_w[r] = sum;
+        }
+        __syncthreads();
+      }
+    }
+  }
+}
+
+bool gate_aligned(const GateArgs& p, bool grad) {
+  auto ok = [&](const void* q, int64_t ld) {
+    return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ld % 8 == 0;
+  };
+  if (p.F % 8 || !ok(p.gate, p.ld_gate) || !ok(p.up, p.ld_up)) return false;
+  return grad ? ok(p.dh, p.ld_dh) && ok(p.dgate, p.ld_dgate) && ok(p.dup, p.ld_dup)
+              : ok(p.h, p.ld_h);
+}
+
+// ------------------------------------------------------ orthogonalised update
+template <int TYPE>
+__device__ __forceinline__ float element(const void* src, int64_t at) {
+  if constexpr (TYPE == kF32)
+    return static_cast<const float*>(src)[at];
+  else
+    return from16<TYPE == kF16>(static_cast<const uint16_t*>(src)[at]);
+}
+
+// The power of two that brings the largest magnitude into [2^13, 2^14): F16
+// then keeps every bit of a 16-bit update down to 2^-27 of its largest
+// element, and no product or norm over- or underflows.  Zero, infinite and
+// NaN maxima take 1 (and then give zeros, or NaN throughout).
+__device__ __forceinline__ float range_scale(uint32_t amax_bits) {
+  const int e = static_cast<int>(amax_bits >> 23);
+  if (amax_bits == 0 || e == 255) return 1.f;
+  const int k = min(13 + 127 - e, 120);
+  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+}
+
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+  if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = v;
+  __syncthreads();
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m = max(m, s[k]);
+  return m;
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(256) amax_kernel(const NormArgs p) {
+  __shared__ uint32_t s[8];
+  const int z = blockIdx.y;
+  const int64_t n = static_cast<int64_t>(p.rows) * p.cols;
+  uint32_t m = 0;
+  for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < n;
+       at += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = at / p.cols;
+    const float v = element<TYPE>(p.src, z * p.sz + r * p.sr + (at - r * p.cols) * p.sc);
+    // as integers, so that a NaN is larger than every number
+    m = max(m, __float_as_uint(v) & 0x7fffffffu);
+  }
+  m = block_max(m, s);
+  if (threadIdx.x == 0) p.amax[z * kNormBlocks + blockIdx.x] = m;
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(256) scale_kernel(const NormArgs p) {
+  __shared__ uint32_t s[8];
+  __shared__ float f[8];
+  const int z = blockIdx.y;
+  const float k = range_scale(block_max(
+      threadIdx.x < p.blocks ? p.amax[z * kNormBlocks + threadIdx.x] : 0u, s));
+  const int64_t n = static_cast<int64_t>(p.rows) * p.cols;
+  float sum = 0.f;
+  for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < n;
+       at += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = at / p.cols;
+    const int64_t c = at - r * p.cols;
+    const float v = element<TYPE>(p.src, z * p.sz + r * p.sr + c * p.sc) * k;
+    const __half h = __float2half_rn(v);
+    const int64_t dst = (static_cast<int64_t>(z) * p.rows + r) * p.ld + c;
+    p.hi[dst] = __half_as_ushort(h);
+    if (p.lo) p.lo[dst] = __half_as_ushort(__float2half_rn(v - __half2float(h)));
+    sum = fmaf(v, v, sum);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  if (threadIdx.x % 32 == 0) f[threadIdx.x / 32] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    sum = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) sum += f[q];
+    p.sumsq[z * kNormBlocks + blockIdx.x] = sum;
+  }
+}
+
+// Per matrix: X = s * (scaled copy) with s = 1 / (norm + eps), the norm and
+// eps both in the copy's scale.
+__global__ void __launch_bounds__(256) norm_kernel(const NormArgs p) {
+  __shared__ uint32_t s[8];
+  const int z = blockIdx.x;
+  const float k = range_scale(block_max(
+      threadIdx.x < p.blocks ? p.amax[z * kNormBlocks + threadIdx.x] : 0u, s));
+  if (threadIdx.x == 0) {
+    float sum = 0.f;
+    for (int q = 0; q < p.blocks; ++q) sum += p.sumsq[z * kNormBlocks + q];
+    const float inv = 1.f / (sqrtf(sum) + p.eps * k);
+    // an all-zero matrix with eps = 0 stays 0 / 0
+    p.alpha_gram[z] = p.scale_gram * inv * inv;
+    p.alpha_step[z] = p.scale_step * inv;
+  }
+}
+
+template <int TYPE>
+cudaError_t norm_impl(const NormArgs& p, cudaStream_t s) {
+  const dim3 grid(p.blocks, p.batch);
+  amax_kernel<TYPE><<<grid, 256, 0, s>>>(p);
+  scale_kernel<TYPE><<<grid, 256, 0, s>>>(p);
+  norm_kernel<<<p.batch, 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+void launch_pack(const PackArgs& p, cudaStream_t s) {
+  const int64_t words = p.zs * p.rows * (p.ld / 8);
+  const int64_t blocks = std::min<int64_t>((words + 255) / 256, 1 << 20);
+  if (blocks > 0) pack_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(p);
+}
+
+void launch_gate(const GateArgs& p, int num_sms, cudaStream_t s) {
+  const int64_t n = p.rows * ((p.F + 7) / 8);
+  const unsigned blocks =
+      static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, static_cast<int64_t>(num_sms) * 32));
+  const bool vec = gate_aligned(p, false);
+  if (p.type == kF16)
+    vec ? gate_kernel<true, true><<<blocks, 256, 0, s>>>(p)
+        : gate_kernel<true, false><<<blocks, 256, 0, s>>>(p);
+  else
+    vec ? gate_kernel<false, true><<<blocks, 256, 0, s>>>(p)
+        : gate_kernel<false, false><<<blocks, 256, 0, s>>>(p);
+}
+
+template <bool F16, bool VEC>
+static void gate_grad_impl(const GateArgs& p, int num_sms, cudaStream_t s) {
+  // a warp per row from as many rows as the GPU holds warps of this kernel
+  // at once; below, a block per row shortens the row's chain of loads
+  if (p.rows >= static_cast<int64_t>(num_sms) * 16) {
+    const int64_t blocks = std::min<int64_t>((p.rows + 7) / 8, static_cast<int64_t>(num_sms) * 32);
+    gate_grad_kernel<F16, VEC, 32><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p);
+  } else {
+    gate_grad_kernel<F16, VEC, 256><<<static_cast<unsigned>(p.rows), 256, 0, s>>>(p);
+  }
+}
+
+void launch_gate_grad(const GateArgs& p, int num_sms, cudaStream_t s) {
+  const bool vec = gate_aligned(p, true);
+  if (p.type == kF16)
+    vec ? gate_grad_impl<true, true>(p, num_sms, s) : gate_grad_impl<true, false>(p, num_sms, s);
+  else
+    vec ? gate_grad_impl<false, true>(p, num_sms, s) : gate_grad_impl<false, false>(p, num_sms, s);
+}
+
+cudaError_t launch_norm(const NormArgs& p, cudaStream_t s) {
+  switch (p.type) {
+    case kBf16: return norm_impl<kBf16>(p, s);
+    case kF16: return norm_impl<kF16>(p, s);
+    case kF32: return norm_impl<kF32>(p, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace beam

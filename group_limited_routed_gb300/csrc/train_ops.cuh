@@ -1,0 +1,62 @@
+// Launchers of the training operators' memory-bound kernels (train_ops.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace beam {
+
+// ------------------------------------------------------------ aligned copies
+// 16-bit elements src[z * sz + r * sr + c * sc], r < rows, c < cols, to
+// dst[(z * rows + r) * ld + c] (ld a multiple of 8, at least cols; the
+// padding is zeroed).
+struct PackArgs {
+  const uint16_t* src;
+  int64_t sz, sr, sc;
+  int64_t zs, rows;
+  int32_t cols, ld;
+  uint16_t* dst;
+};
+void launch_pack(const PackArgs& p, cudaStream_t s);
+
+// -------------------------------------------------------------- gated rows
+struct GateArgs {
+  const void* gate;
+  const void* up;
+  const void* dh;          // gradient only
+  const float* row_w;      // [rows] or nullptr (1)
+  void* h;                 // forward only
+  void* dgate;             // gradient only
+  void* dup;
+  float* drow_w;           // gradient only: [rows] or nullptr
+  int64_t ld_gate, ld_up, ld_dh, ld_h, ld_dgate, ld_dup;
+  int64_t rows;
+  int32_t F;
+  int32_t type;            // kBf16 or kF16
+};
+void launch_gate(const GateArgs& p, int num_sms, cudaStream_t s);
+void launch_gate_grad(const GateArgs& p, int num_sms, cudaStream_t s);
+
+// ------------------------------------------------------ orthogonalised update
+constexpr int kNormBlocks = 64;  // partial sums per matrix, at most
+
+struct NormArgs {
+  const void* src;         // kBf16, kF16 or kF32, src[z * sz + r * sr + c * sc]
+  int64_t sz, sr, sc;
+  int32_t batch, rows, cols;
+  int32_t type;
+  int32_t blocks;          // partial sums per matrix (<= kNormBlocks)
+  uint32_t* amax;          // [batch, kNormBlocks] bits of the largest magnitudes
+  float* sumsq;            // [batch, kNormBlocks]
+  uint16_t* hi;            // F16 [batch, rows, ld]: the update times a power of two
+  uint16_t* lo;            // F16, what hi leaves of a 32-bit update; or nullptr
+  int64_t ld;
+  float* alpha_gram;       // [batch] scale_gram / norm^2
+  float* alpha_step;       // [batch] scale_step / norm
+  float scale_gram, scale_step, eps;
+};
+// Three launches: magnitudes, scaled F16 copy with its sum of squares, norms.
+cudaError_t launch_norm(const NormArgs& p, cudaStream_t s);
+
+}  // namespace beam

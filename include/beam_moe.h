@@ -479,6 +479,107 @@ beam_status_t beam_moe_ep_experts_fp8(const beam_moe_config_t *cfg, int32_t n_ra
 beam_status_t beam_moe_ep_combine(const beam_moe_config_t *cfg, const float *y_back, int64_t T,
                                   void *out, void *workspace, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------ training
+ * Operators that train the experts: products grouped by expert with both
+ * gradients, the gated activation with the routing weight, and the
+ * orthogonalised update of stacked weights.  Conventions as above, except
+ * that sizes are free (no multiples), row strides are arguments, and only
+ * `workspace` has to be 16-byte aligned; elements are naturally aligned. */
+
+typedef enum {
+  BEAM_DTYPE_BF16 = 0,
+  BEAM_DTYPE_F16 = 1,
+  BEAM_DTYPE_F32 = 2
+} beam_dtype_t;
+
+/* Rows in groups: group e holds rows offsets[e] <= r < offsets[e + 1]
+ * (int32 [n_groups + 1] in device memory, e.g. the `offsets` of the layer's
+ * workspace).  x and dx are [rows, K], y and dy [rows, N], W and dW
+ * [n_groups, N, K].  Strides are in elements; x and y rows are contiguous, of
+ * W either k or n is (stride 1), so a transposed view is read in place.
+ * w_stride_e 0 shares one matrix among all groups. */
+typedef struct {
+  int64_t rows;
+  int32_t n_groups;          /* 1 .. 1024 */
+  int32_t N, K;
+  int32_t dtype;             /* BF16 or F16: x, y as operands, W          */
+  int32_t out_dtype;         /* dtype or F32: the product's result        */
+  int64_t x_ld, y_ld;        /* elements between rows of x / dx, y / dy   */
+  int64_t w_stride_e, w_stride_n, w_stride_k;
+} beam_moe_grouped_t;
+
+/* Bytes of workspace the three products need: a status word, and room for an
+ * aligned copy of every operand whose strides are not multiples of 8 elements
+ * (with unaligned != 0, of all: bases may then be unaligned too).  0 for an
+ * invalid description. */
+size_t beam_moe_grouped_matmul_workspace_size(const beam_moe_grouped_t *g, int32_t unaligned);
+
+/* y[r] = W[e] x[r] for every row r of every group e (single-token batches
+ * included: weights of groups without rows are not read).  Rows outside all
+ * groups become zero.  FP32 sums, one rounding.  Boundaries that decrease or
+ * leave [0, rows] are clamped and latch BEAM_ERR_DEVICE_CHECK. */
+beam_status_t beam_moe_grouped_matmul(const beam_moe_grouped_t *g, const void *x, const void *w,
+                                      const int32_t *offsets, void *y, void *workspace,
+                                      size_t ws_bytes, void *stream);
+
+/* The input gradient dx[r] = W[e]^T dy[r] (out_dtype is dx's type). */
+beam_status_t beam_moe_grouped_matmul_dx(const beam_moe_grouped_t *g, const void *dy,
+                                         const void *w, const int32_t *offsets, void *dx,
+                                         void *workspace, size_t ws_bytes, void *stream);
+
+/* The weight gradient dW[e] = sum over the group's rows of dy[r] x[r]^T
+ * (out_dtype is dW's type), dense [n_groups, N, K]; zero for a group without
+ * rows.  accumulate != 0 (F32 only) adds to dW instead.  w_stride_* must be
+ * valid but are not used. */
+beam_status_t beam_moe_grouped_matmul_dw(const beam_moe_grouped_t *g, const void *dy,
+                                         const void *x, const int32_t *offsets, int32_t accumulate,
+                                         void *dw, void *workspace, size_t ws_bytes, void *stream);
+
+/* Gate and up rows [rows, F] (BF16 or F16), e.g. the halves of one
+ * [rows, 2F] buffer. */
+typedef struct {
+  int64_t rows;
+  int32_t F;
+  int32_t dtype;
+  int64_t gate_ld, up_ld;
+} beam_moe_gate_t;
+
+/* h = row_w[r] * silu(gate) * up in FP32, rounded once (row_w FP32 [rows], or
+ * NULL for 1).  With the routing weight here the down product needs none. */
+beam_status_t beam_moe_swiglu(const beam_moe_gate_t *d, const void *gate, const void *up,
+                              const float *row_w, void *h, int64_t h_ld, void *stream);
+
+/* Its gradient: dgate, dup [rows, F] and, unless NULL, drow_w[r] = the sum of
+ * dh * silu(gate) * up over the row (FP32, fixed order).  dgate and dup may
+ * be gate and up themselves. */
+beam_status_t beam_moe_swiglu_grad(const beam_moe_gate_t *d, const void *dh, int64_t dh_ld,
+                                   const void *gate, const void *up, const float *row_w,
+                                   void *dgate, int64_t dgate_ld, void *dup, int64_t dup_ld,
+                                   float *drow_w, void *stream);
+
+/* A stack of matrices [batch, rows, cols] (any strides, in elements). */
+typedef struct {
+  int32_t batch, rows, cols;   /* batch <= 65535, rows and cols <= 65536 */
+  int32_t dtype;               /* BF16, F16 or F32                       */
+  int32_t out_dtype;           /* BF16 or F16                            */
+  int32_t steps;               /* 1 .. 64                                */
+  float a, b, c;               /* |.| <= 16                              */
+  float eps;
+  int64_t stride_batch, stride_row, stride_col;
+} beam_moe_ortho_t;
+
+size_t beam_moe_orthogonalize_workspace_size(int32_t batch, int32_t rows, int32_t cols,
+                                             int32_t dtype);
+
+/* The update orthogonalised by Newton-Schulz products, each matrix by itself:
+ * X = M / (|M|_F + eps), then `steps` times X <- a X + (b A + c A^2) X with
+ * A = X X^T (tall matrices: the same from the right).  out [batch, rows,
+ * cols] dense.  Operands between the steps are F16, sums FP32: the result is
+ * accurate to about 2e-3 of its norm.  A matrix with a NaN or an infinity
+ * becomes NaN. */
+beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t *d, const void *m, void *out,
+                                     void *workspace, size_t ws_bytes, void *stream);
+
 /* Synchronises `stream`, returns the workspace's latched status and clears
  * it.  The only entry point that waits for the device. */
 beam_status_t beam_moe_check_status(void *workspace, void *stream);
