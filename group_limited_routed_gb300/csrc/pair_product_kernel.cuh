@@ -72,7 +72,7 @@ struct ProductCfg {
   static constexpr int S_RAW = static_cast<int>(kPRing / STAGE);
   static constexpr int S = S_RAW > 12 ? 12 : S_RAW;
   static constexpr uint32_t TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
-  static constexpr uint32_t NUM_BARS = 3 * S + 5;
+  static constexpr uint32_t NUM_BARS = 4 * S + 5;
   static constexpr uint32_t MISC = 16 + 4 * (2 * (kProductMaxGroups + 1) + 2);
   static constexpr uint32_t SMEM_BYTES = 1024 + S * STAGE + NUM_BARS * 8 + MISC;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
@@ -106,6 +106,13 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
   return d;
 }
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
 __device__ __forceinline__ void fence_acquire_cluster() {
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
 }
@@ -124,69 +131,126 @@ struct ProductTile {
   int k_count;   // kProductGroups: rows of the group
 };
 
+// a / b for 0 <= a, 0 < b; exact.  The reciprocal's error is far below half
+// of 1 / b while a < 2^20.
+__device__ __forceinline__ int small_div(int a, int b) {
+  if (a < (1 << 20)) return static_cast<int>((static_cast<float>(a) + 0.5f) * __frcp_rn(static_cast<float>(b)));
+  return a / b;
+}
+
+// One role's walk over this pair's tiles: tile, tile + num_pairs, ...  With a
+// few k blocks per tile (kProductGroups) finding the next tile must cost less
+// than a block, so positions advance by addition where they can.
 template <int NT, int KIND>
-__device__ __forceinline__ ProductTile product_tile(int tile, const ProductArgs& p,
-                                                    const int32_t* s_off, const int32_t* s_start) {
-  ProductTile t;
-  const int mt = (p.M + kProductTileM - 1) / kProductTileM;
-  if constexpr (KIND == kProductRows) {
-    int lo = 0, hi = p.groups;  // s_start[lo] <= tile < s_start[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_start[mid] <= tile)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    const int local = tile - s_start[lo];
-    const int cnt = s_off[lo + 1] - s_off[lo];
-    // blocks of nearly equal size, each a multiple of 16 rows
-    const int nb = (cnt + NT - 1) / NT;
-    const int per = (((cnt + nb - 1) / nb) + 15) & ~15;
-    const int b = local % nb;
-    t.z = lo;
-    t.i0 = local / nb * kProductTileM;
-    t.j0 = s_off[lo] + b * per;
-    t.nvalid = min(per, cnt - b * per);
-    t.k_blocks = p.k_blocks;
-    t.k0 = t.k_count = 0;
-  } else {
-    const int nt = (p.N + NT - 1) / NT;
-    int i, j;
-    if (KIND == kProductDense && p.symmetric) {
-      // tiles with j >= i, in units of 256 columns and NT rows
-      constexpr int R = kProductTileM / NT;
-      const int per_z = mt * nt - R * (mt * (mt - 1) / 2);
-      t.z = tile / per_z;
-      int left = tile - t.z * per_z;
-      i = 0;
-      while (left >= nt - i * R) {
-        left -= nt - i * R;
-        ++i;
-      }
-      j = i * R + left;
-    } else {
-      const int per_z = mt * nt;
-      t.z = tile / per_z;
-      const int local = tile - t.z * per_z;
-      i = local / nt;
-      j = local - i * nt;
-    }
-    t.i0 = i * kProductTileM;
-    t.j0 = j * NT;
-    t.nvalid = min(NT, p.N - t.j0);
+struct ProductWalk {
+  const ProductArgs& p;
+  const int32_t* s_off;
+  const int32_t* s_start;
+  int tile, step, total;
+  int mt, nt;       // tiles along i and j
+  int group = 0;    // kProductRows: group of the last tile
+  int z = 0, i = 0, j = 0, dz = 0, di = 0, dj = 0;
+
+  __device__ ProductWalk(const ProductArgs& args, const int32_t* off, const int32_t* start,
+                         int first, int stride, int tiles)
+      : p(args), s_off(off), s_start(start), tile(first), step(stride), total(tiles) {
+    mt = (p.M + kProductTileM - 1) / kProductTileM;
+    nt = (p.N + NT - 1) / NT;
     if constexpr (KIND == kProductGroups) {
-      t.k0 = s_off[t.z];
-      t.k_count = s_off[t.z + 1] - t.k0;
+      // i fastest: neighbouring pairs write neighbouring pieces of the same rows
+      z = first / (mt * nt);
+      j = (first - z * mt * nt) / mt;
+      i = first - (z * nt + j) * mt;
+      dz = step / (mt * nt);
+      dj = (step - dz * mt * nt) / mt;
+      di = step - (dz * nt + dj) * mt;
+    }
+  }
+
+  __device__ bool done() const { return tile >= total; }
+
+  __device__ void next() {
+    tile += step;
+    if constexpr (KIND == kProductGroups) {
+      i += di;
+      j += dj;
+      z += dz;
+      if (i >= mt) {
+        i -= mt;
+        ++j;
+      }
+      if (j >= nt) {
+        j -= nt;
+        ++z;
+      }
+    }
+  }
+
+  __device__ ProductTile get() {
+    ProductTile t;
+    if constexpr (KIND == kProductRows) {
+      if (s_start[group + 1] <= tile) {
+        int lo = group + 1, hi = p.groups;  // s_start[lo] <= tile < s_start[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (s_start[mid] <= tile)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        group = lo;
+      }
+      const int local = tile - s_start[group];
+      const int cnt = s_off[group + 1] - s_off[group];
+      // blocks of nearly equal size, each a multiple of 16 rows
+      const int nb = (cnt + NT - 1) / NT;
+      const int per = (small_div(cnt + nb - 1, nb) + 15) & ~15;
+      const int block_i = small_div(local, nb);
+      const int b = local - block_i * nb;
+      t.z = group;
+      t.i0 = block_i * kProductTileM;
+      t.j0 = s_off[group] + b * per;
+      t.nvalid = min(per, cnt - b * per);
+      t.k_blocks = p.k_blocks;
+      t.k0 = t.k_count = 0;
+    } else if constexpr (KIND == kProductGroups) {
+      t.z = z;
+      t.i0 = i * kProductTileM;
+      t.j0 = j * NT;
+      t.nvalid = min(NT, p.N - t.j0);
+      t.k0 = s_off[z];
+      t.k_count = s_off[z + 1] - t.k0;
       t.k_blocks = (t.k_count + kPBK - 1) / kPBK;
     } else {
+      int bi, bj;
+      if (p.symmetric) {
+        // tiles with j >= i, in units of 256 columns and NT rows
+        constexpr int R = kProductTileM / NT;
+        const int per_z = mt * nt - R * (mt * (mt - 1) / 2);
+        t.z = tile / per_z;
+        int left = tile - t.z * per_z;
+        bi = 0;
+        while (left >= nt - bi * R) {
+          left -= nt - bi * R;
+          ++bi;
+        }
+        bj = bi * R + left;
+      } else {
+        t.z = tile / (mt * nt);
+        const int local = tile - t.z * mt * nt;
+        bi = local / nt;
+        bj = local - bi * nt;
+      }
+      t.i0 = bi * kProductTileM;
+      t.j0 = bj * NT;
+      t.nvalid = min(NT, p.N - t.j0);
       t.k_blocks = p.k_blocks;
       t.k0 = t.k_count = 0;
     }
+    t.n_mma = (t.nvalid + 15) & ~15;
+    return t;
   }
-  t.n_mma = (t.nvalid + 15) & ~15;
-  return t;
-}
+};
 
 template <int NT, int KIND>
 __device__ __forceinline__ int product_tiles(const ProductArgs& p, const int32_t* s_start) {
@@ -236,10 +300,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
   const uint32_t bar0 = ptx::smem_addr(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
   auto empty = [&](int s) { return bar0 + 8u * (C::S + s); };
-  auto landed = [&](int s) { return bar0 + 8u * (2 * C::S + s); };  // ragged last blocks
-  auto tfull = [&](int a) { return bar0 + 8u * (3 * C::S + a); };
-  auto tempty = [&](int a) { return bar0 + 8u * (3 * C::S + 2 + a); };
-  const uint32_t done_bar = bar0 + 8u * (3 * C::S + 4);
+  // ragged last blocks: loaded (this CTA's), cleared (both CTAs', the leader's barrier)
+  auto landed = [&](int s) { return bar0 + 8u * (2 * C::S + s); };
+  auto cleared = [&](int s) { return bar0 + 8u * (3 * C::S + s); };
+  auto tfull = [&](int a) { return bar0 + 8u * (4 * C::S + a); };
+  auto tempty = [&](int a) { return bar0 + 8u * (4 * C::S + 2 + a); };
+  const uint32_t done_bar = bar0 + 8u * (4 * C::S + 4);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -250,10 +316,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::S; ++s) {
-      // ragged k: both CTAs arrive on the leader's barrier for every stage
-      ptx::mbar_init(full(s), RAGGED_K ? 2 : 1);
+      ptx::mbar_init(full(s), 1);  // the leader's producer; bytes of both CTAs
       ptx::mbar_init(empty(s), 1);
       ptx::mbar_init(landed(s), 1);
+      ptx::mbar_init(cleared(s), 2);
     }
     for (int a = 0; a < 2; ++a) {
       ptx::mbar_init(tfull(a), 1);
@@ -333,15 +399,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // -------------------------------------------------------------- producer
     if (lane == 0) {
       const uint64_t pol = ptx::policy_evict_normal();
-      int last_parity[C::S];
-#pragma unroll
-      for (int s = 0; s < C::S; ++s) last_parity[s] = -1;
+      uint32_t used = 0, parities = 0;  // bit s: stage s was filled, its last phase
       int stage = 0;
       uint32_t phase = 0;
-      uint64_t last_issue = 0;
       bool ok = true;
-      for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
-        const ProductTile t = product_tile<NT, KIND>(tile, p, s_off, s_start);
+      for (ProductWalk<NT, KIND> walk(p, s_off, s_start, pair, num_pairs, num_tiles);
+           ok && !walk.done(); walk.next()) {
+        const ProductTile t = walk.get();
         const int i = t.i0 + static_cast<int>(rank) * 128;
         const int j = t.j0 + static_cast<int>(rank) * (t.n_mma / 2);
         for (int kb = 0; kb < t.k_blocks; ++kb) {
@@ -349,22 +413,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t lead_full = ptx::map_to_rank(full(stage), 0);
-          uint32_t bar = lead_full;
-          if constexpr (RAGGED_K) {
-            if ((kb + 1) * kPBK > t.k_count) {
-              // the group's ragged last block: this CTA's own barrier, then
-              // the warp that clears foreign rows arrives on the leader's
-              bar = landed(stage);
-              ptx::mbar_arrive_expect_tx(bar, C::STAGE);
-              bar = ptx::map_to_rank(bar, rank);
-            } else if (leader) {
-              ptx::mbar_arrive_expect_tx(full(stage), 2 * C::STAGE);
-            } else {
-              ptx::mbar_arrive_cluster(lead_full);
-            }
-          } else {
-            if (leader) ptx::mbar_arrive_expect_tx(full(stage), 2 * C::STAGE);
+          uint32_t bar = ptx::map_to_rank(full(stage), 0);
+          if (RAGGED_K && (kb + 1) * kPBK > t.k_count) {
+            // the group's ragged last block: its bytes count on this CTA's
+            // own barrier, for the warp that clears foreign rows
+            bar = ptx::map_to_rank(landed(stage), rank);
+            ptx::mbar_arrive_expect_tx(landed(stage), C::STAGE);
+            if (leader) ptx::mbar_arrive(full(stage));
+          } else if (leader) {
+            ptx::mbar_arrive_expect_tx(full(stage), 2 * C::STAGE);
           }
           const uint32_t sa = ring + stage * C::STAGE;
           const uint32_t sb = sa + kPABytes;
@@ -394,8 +451,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           } else {
             tma_load_3d_pair(sb, &tm_b, bar, k, j, KIND == kProductRows ? 0 : zb, pol);
           }
-          last_issue = ptx::globaltimer();
-          last_parity[stage] = static_cast<int>(phase);
+          used |= 1u << stage;
+          parities = (parities & ~(1u << stage)) | (phase << stage);
           if (++stage == C::S) {
             stage = 0;
             phase ^= 1u;
@@ -403,81 +460,112 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
       }
       // No CTA exits with a copy into its shared memory in flight.  The
-      // leader's full barriers count both CTAs' bytes, so once it has seen
-      // its last phases complete the peer's copies have landed too, and the
-      // cluster barrier below keeps the peer until then.  After an abort the
-      // peer may have issued copies for phases the leader never armed, and
-      // either CTA copies that only its own landed barrier counts: they are
-      // given time to land.
+      // leader's full barriers count both CTAs' bytes (a ragged block's its
+      // own CTA's landed barrier, which the clearing warp has waited for), so
+      // once it has seen its last phases complete the peer's copies have
+      // landed too, and the cluster barrier below keeps the peer until then.
+      // After an abort the peer may have issued copies for phases the leader
+      // never armed, and ragged blocks may be unseen: they get time to land.
       if (!ok || *abort_flag) {
-        while (ptx::globaltimer() - last_issue < kPPeerDrainNs) {
+        const uint64_t t0 = ptx::globaltimer();
+        while (ptx::globaltimer() - t0 < kPPeerDrainNs) {
         }
       } else if (leader) {
-#pragma unroll
         for (int s = 0; s < C::S; ++s)
-          if (last_parity[s] >= 0) W.wait_final(full(s), static_cast<uint32_t>(last_parity[s]));
+          if (used >> s & 1u) W.wait_final(full(s), parities >> s & 1u);
       }
     }
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && leader) {
+    // The whole warp walks and waits, so that control flow and descriptors
+    // stay uniform (in uniform registers); one elected lane issues.
+    if (leader) {
       const uint32_t fmt = p.in_type == kBf16 ? 1u : 0u;
       const uint32_t idesc_m = (1u << 4) | (fmt << 7) | (fmt << 10) |
                                (static_cast<uint32_t>(A_MN) << 15) |
                                (static_cast<uint32_t>(B_MN) << 16) | ((256u >> 4) << 24);
+      // descriptors of stage 0; a stage, and a step of 16 k in it, add to the
+      // address field alone (shared memory ends below 2^18: no carry)
+      const uint64_t a_desc0 = A_MN ? sdesc_mn_sw128(ring) : ptx::sdesc_sw128(ring);
+      const uint64_t b_desc0 =
+          B_MN ? sdesc_mn_sw128(ring + kPABytes) : ptx::sdesc_sw128(ring + kPABytes);
+      constexpr uint32_t A_STEP = (A_MN ? 2048 : 32) >> 4, B_STEP = (B_MN ? 2048 : 32) >> 4;
+      const bool elected = elect_one();
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
       uint32_t acc_phase = 0;
+      uint32_t cleared_parity = 0;  // bit s: phase of cleared(s)
       bool ok = true;
-      for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
-        const ProductTile t = product_tile<NT, KIND>(tile, p, s_off, s_start);
-        if (RAGGED_K && t.k_blocks == 0) continue;
+      ProductWalk<NT, KIND> walk(p, s_off, s_start, pair, num_pairs, num_tiles);
+      ProductTile ahead;
+      if (!walk.done()) ahead = walk.get();
+      while (ok && !walk.done()) {
+        const ProductTile t = ahead;
+        if (RAGGED_K && t.k_blocks == 0) {
+          walk.next();
+          if (!walk.done()) ahead = walk.get();
+          continue;
+        }
         const uint32_t idesc = idesc_m | (static_cast<uint32_t>(t.n_mma >> 3) << 17);
         uint32_t d0 = 0;
         for (int kb = 0; kb < t.k_blocks; ++kb) {
-          if (kb == 0 || (WIDE && kb % kWideBlocks == 0)) {
+          const bool fresh = kb == 0 || (WIDE && kb % kWideBlocks == 0);
+          if (fresh) {
             if (!W.wait(tempty(acc), acc_phase ^ 1u)) {
               ok = false;
               break;
             }
-            ptx::tc_fence_after();
             d0 = tmem_base + acc * NT;
           }
           if (!W.wait(full(stage), phase)) {
             ok = false;
             break;
           }
-          // a cleared last block was also written by the peer's threads
-          if (RAGGED_K && (kb + 1) * kPBK > t.k_count) fence_acquire_cluster();
-          ptx::tc_fence_after();
-          const uint32_t sa = ring + stage * C::STAGE;
-          const uint32_t sb = sa + kPABytes;
-          const bool fresh = kb == 0 || (WIDE && kb % kWideBlocks == 0);
-          int steps = kPBK / 16;
-          if constexpr (RAGGED_K) steps = min(steps, (t.k_count - kb * kPBK + 15) / 16);
-#pragma unroll
-          for (int kk = 0; kk < kPBK / 16; ++kk) {
-            if (RAGGED_K && kk >= steps) break;
-            const uint64_t ad = A_MN ? sdesc_mn_sw128(sa + kk * 2048) : ptx::sdesc_sw128(sa + kk * 32);
-            const uint64_t bd = B_MN ? sdesc_mn_sw128(sb + kk * 2048) : ptx::sdesc_sw128(sb + kk * 32);
-            ptx::mma_bf16_pair(d0, ad, bd, idesc, (fresh && kk == 0) ? 0u : 1u);
+          const bool ragged = RAGGED_K && (kb + 1) * kPBK > t.k_count;
+          if (ragged) {
+            if (!W.wait(cleared(stage), cleared_parity >> stage & 1u)) {
+              ok = false;
+              break;
+            }
+            cleared_parity ^= 1u << stage;
+            // the block was also written by the peer's threads
+            fence_acquire_cluster();
           }
-          ptx::mma_commit_pair_both(empty(stage));
+          ptx::tc_fence_after();
+          const bool last = kb + 1 == t.k_blocks || (WIDE && (kb + 1) % kWideBlocks == 0);
+          if (elected) {
+            const uint64_t ad = a_desc0 + stage * (C::STAGE >> 4);
+            const uint64_t bd = b_desc0 + stage * (C::STAGE >> 4);
+            const int steps = ragged ? (t.k_count - kb * kPBK + 15) / 16 : kPBK / 16;
+#pragma unroll
+            for (int kk = 0; kk < kPBK / 16; ++kk)
+              if (!RAGGED_K || kk < steps)
+                ptx::mma_bf16_pair(d0, ad + kk * A_STEP, bd + kk * B_STEP, idesc,
+                                   (fresh && kk == 0) ? 0u : 1u);
+            ptx::mma_commit_pair_both(empty(stage));
+            if (last) ptx::mma_commit_pair_both(tfull(acc));
+          }
+          __syncwarp();
+          if (kb == 0) {
+            // the next tile's place, found while the tensor cores work
+            walk.next();
+            if (!walk.done()) ahead = walk.get();
+          }
           if (++stage == C::S) {
             stage = 0;
             phase ^= 1u;
           }
-          if (kb + 1 == t.k_blocks || (WIDE && (kb + 1) % kWideBlocks == 0)) {
-            ptx::mma_commit_pair_both(tfull(acc));
+          if (last) {
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
           }
         }
       }
       // every MMA issued completes before TMEM is released
-      ptx::mma_commit_pair_self(done_bar);
+      if (elected) ptx::mma_commit_pair_self(done_bar);
+      __syncwarp();
       W.wait_final(done_bar, 0);
     }
     __syncwarp();
@@ -485,23 +573,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // ------------------------------------- foreign rows of ragged last blocks
     if constexpr (RAGGED_K) {
       int stage = 0;
-      uint32_t parity[C::S];
-#pragma unroll
-      for (int s = 0; s < C::S; ++s) parity[s] = 0;
-      for (int tile = pair; tile < num_tiles; tile += num_pairs) {
-        const ProductTile t = product_tile<NT, KIND>(tile, p, s_off, s_start);
+      uint32_t parity = 0;  // bit s: phase of landed(s)
+      for (ProductWalk<NT, KIND> walk(p, s_off, s_start, pair, num_pairs, num_tiles);
+           !walk.done(); walk.next()) {
+        const ProductTile t = walk.get();
         stage = (stage + t.k_blocks) % C::S;
         const int tail = t.k_count % kPBK;
         if (tail == 0) continue;
         const int s = (stage + C::S - 1) % C::S;
-        uint32_t par = 0;
-#pragma unroll
-        for (int q = 0; q < C::S; ++q)
-          if (q == s) {
-            par = parity[q];
-            parity[q] ^= 1u;
-          }
-        if (!W.wait(landed(s), par)) break;
+        if (!W.wait(landed(s), parity >> s & 1u)) break;
+        parity ^= 1u << s;
         const int last = (tail + 15) & ~15;
         const uint32_t base = ring + s * C::STAGE;
         // rows [tail, last) of every 64-element atom of both operands
@@ -515,7 +596,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(full(s), 0));
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(cleared(s), 0));
       }
     }
     __syncwarp();
@@ -548,8 +629,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (int tile = pair; ok && tile < num_tiles; tile += num_pairs) {
-      const ProductTile t = product_tile<NT, KIND>(tile, p, s_off, s_start);
+    for (ProductWalk<NT, KIND> walk(p, s_off, s_start, pair, num_pairs, num_tiles);
+         ok && !walk.done(); walk.next()) {
+      const ProductTile t = walk.get();
       const int i = t.i0 + static_cast<int>(rank) * 128 + q * 32 + lane;
       const int64_t zbase = KIND == kProductRows ? 0 : static_cast<int64_t>(t.z) * p.z_out;
       const int ncols = min(t.nvalid - col_begin, COLS);  // <= 0: nothing for this warp
