@@ -37,6 +37,7 @@ struct ProductArgs {
   int32_t out_type;        // kBf16, kF16 or kF32
   int32_t in_type;         // kBf16 or kF16
   int32_t accumulate;      // out += (kF32 outputs)
+  int32_t staged;          // `tm_out` describes out: results may leave by bulk copy
   int32_t symmetric;       // kDense, M == N: compute one triangle of tiles, mirror it
   // out = alpha * product (+ beta * add) (+ diag on i == j); add: F16, laid
   // out as out; alpha_z: a factor of each z, or nullptr
@@ -52,12 +53,18 @@ constexpr int kProductMaxTile = 256;
 constexpr int kProductTileM = 256;
 constexpr int kProductMaxGroups = 1024;
 
+// Rows j of one box of a k-contiguous B (nt / 2 where that is less).
+constexpr int kProductBoxRows = 32;
+inline int product_box_rows(int nt) { return nt / 2 < kProductBoxRows ? nt / 2 : kProductBoxRows; }
+
 // nt: rows j per tile, 32, 64, 128 or 256 (kProductGroups: 256).  a_mn, b_mn:
 // the operand's contiguous axis is i (j) rather than k.  Tensor maps are
-// three-dimensional (contiguous, row, z) with 128-byte swizzle; boxes:
-// 64 x 128 (a, k contiguous), 64 x 64 (a_mn, b_mn), 64 x nt/2 (b, k contiguous).
+// three-dimensional (contiguous, row, z); a and b with 128-byte swizzle and
+// boxes 64 x 128 (a, k contiguous), 64 x 64 (a_mn, b_mn), 64 x
+// product_box_rows(nt) (b, k contiguous); out (only read with p.staged)
+// without swizzle, boxes 32 x 16 (FP32) or 32 x 32 (16-bit).
 cudaError_t launch_pair_product(int kind, int nt, bool a_mn, bool b_mn, const CUtensorMap& a,
-                                const CUtensorMap& b, const ProductArgs& p, bool dependent,
-                                cudaStream_t s);
+                                const CUtensorMap& b, const CUtensorMap& out,
+                                const ProductArgs& p, bool dependent, cudaStream_t s);
 
 }  // namespace beam

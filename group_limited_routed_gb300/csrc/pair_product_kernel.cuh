@@ -65,16 +65,23 @@ constexpr int kWideBlocks = 4;                 // k blocks per accumulator chain
 constexpr uint64_t kPPeerDrainNs = 1000000ull; // see the producer's teardown
 constexpr uint32_t kAtom = 64 * 128;           // MN-major atom: 64 k rows of 64 elements
 
-template <int NT>
+// Results that leave through shared memory: a warp stages 2 KB (16 rows of 32
+// FP32 columns, or 32 rows of 16-bit ones) and one bulk copy writes them.
+constexpr uint32_t kStaging = kPEpiWarps * 2048;
+
+template <int NT, int KIND, bool WIDE>
 struct ProductCfg {
+  static constexpr bool STAGED = KIND == kProductGroups || WIDE;
   static constexpr uint32_t B_BYTES = NT / 2 * 128;
   static constexpr uint32_t STAGE = kPABytes + B_BYTES;
-  static constexpr int S_RAW = static_cast<int>(kPRing / STAGE);
+  static constexpr int S_RAW = static_cast<int>((kPRing - (STAGED ? kStaging : 0)) / STAGE);
   static constexpr int S = S_RAW > 12 ? 12 : S_RAW;
   static constexpr uint32_t TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
   static constexpr uint32_t NUM_BARS = 4 * S + 5;
   static constexpr uint32_t MISC = 16 + 4 * (2 * (kProductMaxGroups + 1) + 2);
-  static constexpr uint32_t SMEM_BYTES = 1024 + S * STAGE + NUM_BARS * 8 + MISC;
+  static constexpr uint32_t STAGING = S * STAGE;  // offset
+  static constexpr uint32_t BARS = STAGING + (STAGED ? kStaging : 0);
+  static constexpr uint32_t SMEM_BYTES = 1024 + BARS + NUM_BARS * 8 + MISC;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
   static_assert(STAGE % 1024 == 0, "swizzle atoms are 1024-byte aligned");
   static_assert(TMEM_COLS <= 512, "TMEM columns");
@@ -112,6 +119,13 @@ __device__ __forceinline__ bool elect_one() {
       "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok));
   return ok != 0;
+}
+// Arrive on either CTA's barrier without a release.  It frees TMEM columns
+// whose loads have completed (tcgen05.wait::ld): no memory is handed over,
+// and a release would wait for the warp's earlier global stores.
+__device__ __forceinline__ void arrive_relaxed_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
 }
 __device__ __forceinline__ void fence_acquire_cluster() {
   asm volatile("fence.acq_rel.cluster;" ::: "memory");
@@ -252,6 +266,9 @@ struct ProductWalk {
   }
 };
 
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[16]) { ptx::tmem_ld16(at, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[32]) { ptx::tmem_ld32(at, r); }
+
 template <int NT, int KIND>
 __device__ __forceinline__ int product_tiles(const ProductArgs& p, const int32_t* s_start) {
   const int mt = (p.M + kProductTileM - 1) / kProductTileM;
@@ -266,9 +283,40 @@ __device__ __forceinline__ int product_tiles(const ProductArgs& p, const int32_t
   }
 }
 
-__device__ __forceinline__ uint32_t to16(float v, bool f16) {
-  return f16 ? static_cast<uint32_t>(__half_as_ushort(__float2half_rn(v)))
-             : static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(v)));
+// Two values rounded to the 16-bit output type, the first in the low half.
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi, bool f16) {
+  if (f16) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Bulk copy of a warp's staged rows, shared -> global; ADD: += in FP32.
+template <bool ADD>
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int32_t x,
+                                             int32_t y, int32_t z) {
+  if constexpr (ADD)
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group "
+        "[%0, {%1, %2, %3}], [%4];" ::"l"(reinterpret_cast<uint64_t>(m)),
+        "r"(x), "r"(y), "r"(z), "r"(src)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::
+            "l"(reinterpret_cast<uint64_t>(m)),
+        "r"(x), "r"(y), "r"(z), "r"(src)
+        : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Every staged row of this thread's copies has been read / written.
+__device__ __forceinline__ void tma_store_read_done() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // Two 16-bit values of one lane's column (rows j, j + 1) and its neighbour's
@@ -282,15 +330,16 @@ __device__ __forceinline__ uint32_t swap_pair(uint32_t mine, int lane) {
 template <int NT, bool A_MN, bool B_MN, int KIND, bool WIDE>
 __global__ void __launch_bounds__(kPThreads, 1)
     pair_product_kernel(const __grid_constant__ CUtensorMap tm_a,
-                        const __grid_constant__ CUtensorMap tm_b, const ProductArgs p) {
-  using C = ProductCfg<NT>;
+                        const __grid_constant__ CUtensorMap tm_b,
+                        const __grid_constant__ CUtensorMap tm_out, const ProductArgs p) {
+  using C = ProductCfg<NT, KIND, WIDE>;
   constexpr bool RAGGED_K = KIND == kProductGroups;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = ptx::smem_addr(smem_raw);
   const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
   const uint32_t ring = raw_addr + pad;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::S * C::STAGE);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BARS);
   int32_t* misc = reinterpret_cast<int32_t*>(bars + C::NUM_BARS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int32_t* abort_flag = misc + 1;
@@ -397,8 +446,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
-    if (lane == 0) {
+    // The whole warp walks and waits (uniform control flow and addresses);
+    // one elected lane arms the barriers and issues the copies.
+    {
       const uint64_t pol = ptx::policy_evict_normal();
+      const bool elected = elect_one();
       uint32_t used = 0, parities = 0;  // bit s: stage s was filled, its last phase
       int stage = 0;
       uint32_t phase = 0;
@@ -408,24 +460,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const ProductTile t = walk.get();
         const int i = t.i0 + static_cast<int>(rank) * 128;
         const int j = t.j0 + static_cast<int>(rank) * (t.n_mma / 2);
+        // k-contiguous B comes in boxes of BOX rows, as many as the tile has
+        constexpr int BOX = NT / 2 < kProductBoxRows ? NT / 2 : kProductBoxRows;
+        const int boxes = (t.n_mma / 2 + BOX - 1) / BOX;
+        const uint32_t bytes = kPABytes + (B_MN ? C::B_BYTES : boxes * BOX * 128u);
         for (int kb = 0; kb < t.k_blocks; ++kb) {
           if (!W.wait(empty(stage), phase ^ 1u)) {
             ok = false;
             break;
           }
-          uint32_t bar = ptx::map_to_rank(full(stage), 0);
-          if (RAGGED_K && (kb + 1) * kPBK > t.k_count) {
-            // the group's ragged last block: its bytes count on this CTA's
-            // own barrier, for the warp that clears foreign rows
-            bar = ptx::map_to_rank(landed(stage), rank);
-            ptx::mbar_arrive_expect_tx(landed(stage), C::STAGE);
-            if (leader) ptx::mbar_arrive(full(stage));
-          } else if (leader) {
-            ptx::mbar_arrive_expect_tx(full(stage), 2 * C::STAGE);
-          }
-          const uint32_t sa = ring + stage * C::STAGE;
-          const uint32_t sb = sa + kPABytes;
-          int k = kb, za = t.z * p.a_z, zb = t.z;
+          const bool ragged = RAGGED_K && (kb + 1) * kPBK > t.k_count;
+          int k = kb, za = t.z * p.a_z, zb = KIND == kProductRows ? 0 : t.z;
           if constexpr (KIND == kProductDense) {
             if (kb >= p.k_wrap) {
               k -= p.k_wrap;
@@ -434,23 +479,42 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
           }
           k *= kPBK;
-          if constexpr (A_MN) {
-            const int ky = RAGGED_K ? t.k0 + k : k;
-            const int z = RAGGED_K ? 0 : za;
-            tma_load_3d_pair(sa, &tm_a, bar, i, ky, z, pol);
-            tma_load_3d_pair(sa + kAtom, &tm_a, bar, i + 64, ky, z, pol);
-          } else {
-            tma_load_3d_pair(sa, &tm_a, bar, k, i, za, pol);
+          if constexpr (RAGGED_K) {
+            k += t.k0;
+            za = zb = 0;
           }
-          if constexpr (B_MN) {
-            const int ky = RAGGED_K ? t.k0 + k : k;
-            const int z = RAGGED_K ? 0 : zb;
+          const uint32_t sa = ring + stage * C::STAGE;
+          const uint32_t sb = sa + kPABytes;
+          // the leader's full barrier counts both CTAs' bytes; a group's
+          // ragged last block counts on this CTA's own barrier, for the warp
+          // that clears foreign rows
+          const uint32_t bar = ragged ? ptx::map_to_rank(landed(stage), rank)
+                                      : ptx::map_to_rank(full(stage), 0);
+          if (elected) {
+            if (ragged) {
+              ptx::mbar_arrive_expect_tx(landed(stage), bytes);
+              if (leader) ptx::mbar_arrive(full(stage));
+            } else if (leader) {
+              ptx::mbar_arrive_expect_tx(full(stage), 2 * bytes);
+            }
+            if constexpr (A_MN) {
+              tma_load_3d_pair(sa, &tm_a, bar, i, k, za, pol);
+              tma_load_3d_pair(sa + kAtom, &tm_a, bar, i + 64, k, za, pol);
+            } else {
+              tma_load_3d_pair(sa, &tm_a, bar, k, i, za, pol);
+            }
+            if constexpr (B_MN) {
 #pragma unroll
-            for (int c = 0; c < NT / 128; ++c)
-              tma_load_3d_pair(sb + c * kAtom, &tm_b, bar, j + c * 64, ky, z, pol);
-          } else {
-            tma_load_3d_pair(sb, &tm_b, bar, k, j, KIND == kProductRows ? 0 : zb, pol);
+              for (int c = 0; c < NT / 128; ++c)
+                tma_load_3d_pair(sb + c * kAtom, &tm_b, bar, j + c * 64, k, zb, pol);
+            } else {
+#pragma unroll
+              for (int c = 0; c < NT / 2 / BOX; ++c)
+                if (c < boxes)
+                  tma_load_3d_pair(sb + c * (BOX * 128), &tm_b, bar, k, j + c * BOX, zb, pol);
+            }
           }
+          __syncwarp();
           used |= 1u << stage;
           parities = (parities & ~(1u << stage)) | (phase << stage);
           if (++stage == C::S) {
@@ -606,6 +670,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
     constexpr int GROUPS = kPEpiWarps / 4;
     constexpr int COLS = NT / GROUPS < 16 ? 16 : NT / GROUPS;  // rows j per warp
     const int col_begin = ((warp - 3) >> 2) * COLS;
+    // TMEM columns per load; the affine epilogue needs the registers itself
+    constexpr int LD = COLS < 32 || KIND == kProductDense ? 16 : 32;
+    const uint32_t stage_at = ring + C::STAGING + (warp - 3) * 2048;
     const bool f16 = p.out_type == kF16;
     // two columns per store where every address of it is 4-byte aligned
     const bool paired = (p.M & 1) == 0 && (p.ld_out & 1) == 0 && (p.z_out & 1) == 0 &&
@@ -647,30 +714,54 @@ __global__ void __launch_bounds__(kPThreads, 1)
           ptx::tc_fence_after();
           const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NT + col_begin;
 #pragma unroll
-          for (int c = 0; c < COLS; c += 16) {
+          for (int c = 0; c < COLS; c += LD) {
             if (c < ncols) {
-              uint32_t r[16];
-              ptx::tmem_ld16(tq + c, r);
+              uint32_t r[LD];
+              tmem_ld(tq + c, r);
               ptx::tmem_wait_ld();
 #pragma unroll
-              for (int u = 0; u < 16; ++u) sum[c + u] += __uint_as_float(r[u]);
+              for (int u = 0; u < LD; ++u) sum[c + u] += __uint_as_float(r[u]);
             }
           }
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(tempty(acc), 0));
+          if (lane == 0) arrive_relaxed_cluster(ptx::map_to_rank(tempty(acc), 0));
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1u;
         }
         if (!ok) break;
-        if (i < p.M) {
-          float* dst = static_cast<float*>(p.out) + zbase +
-                       (static_cast<int64_t>(t.j0) + col_begin) * p.ld_out + i;
+        float* dst = static_cast<float*>(p.out) + zbase +
+                     (static_cast<int64_t>(t.j0) + col_begin) * p.ld_out + i;
 #pragma unroll
-          for (int c = 0; c < COLS; ++c) {
-            if (c < ncols) {
-              float* at = dst + c * p.ld_out;
-              __stcs(at, p.accumulate ? *at + sum[c] : sum[c]);
+        for (int c = 0; c < COLS; c += 16) {
+          if (c < ncols) {
+            // whole pieces of 16 rows leave by bulk copy (a group's last rows
+            // do not: the copy would reach into the next group's)
+            if (p.staged && (KIND == kProductGroups || c + 16 <= ncols)) {
+              if (lane == 0) tma_store_read_done();
+              __syncwarp();
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage_at + u * 128 + lane * 4),
+                             "f"(sum[c + u])
+                             : "memory");
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0 && i < p.M) {
+                const int z = KIND == kProductRows ? 0 : t.z;
+                if (p.accumulate)
+                  tma_store_3d<true>(&tm_out, stage_at, i, t.j0 + col_begin + c, z);
+                else
+                  tma_store_3d<false>(&tm_out, stage_at, i, t.j0 + col_begin + c, z);
+              }
+            } else if (i < p.M) {
+#pragma unroll
+              for (int u = 0; u < 16; ++u) {
+                if (c + u < ncols) {
+                  float* at = dst + (c + u) * p.ld_out;
+                  __stcs(at, p.accumulate ? *at + sum[c + u] : sum[c + u]);
+                }
+              }
             }
           }
         }
@@ -687,14 +778,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const uint16_t* add = KIND == kProductDense && p.add ? p.add + zbase : nullptr;
         uint32_t packed[COLS / 2];  // rows (2c, 2c + 1) of this lane's column
 #pragma unroll
-        for (int c = 0; c < COLS; c += 16) {
+        for (int c = 0; c < COLS; c += LD) {
           if (c < ncols) {
-            uint32_t r[16];
-            float extra[16];
-            if (live) ptx::tmem_ld16(tq + c, r);
-            if (KIND == kProductDense) {
+            uint32_t r[LD];
+            float extra[KIND == kProductDense ? LD : 1];
+            if (live) tmem_ld(tq + c, r);
+            if constexpr (KIND == kProductDense) {
 #pragma unroll
-              for (int u = 0; u < 16; ++u) {
+              for (int u = 0; u < LD; ++u) {
                 const int j = t.j0 + col_begin + c + u;
                 extra[u] = (add && i < p.M && c + u < ncols)
                                ? p.beta * __half2float(__ushort_as_half(add[static_cast<int64_t>(j) * p.ld_out + i]))
@@ -702,16 +793,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 if (j == i) extra[u] += p.diag;
               }
             }
-            if (live) ptx::tmem_wait_ld();
+            if (live) {
+              ptx::tmem_wait_ld();
+            } else {
 #pragma unroll
-            for (int u = 0; u < 16; u += 2) {
-              float v0 = live ? __uint_as_float(r[u]) : 0.f;
-              float v1 = live ? __uint_as_float(r[u + 1]) : 0.f;
-              if (KIND == kProductDense) {
+              for (int u = 0; u < LD; ++u) r[u] = 0u;
+            }
+#pragma unroll
+            for (int u = 0; u < LD; u += 2) {
+              float v0 = __uint_as_float(r[u]), v1 = __uint_as_float(r[u + 1]);
+              if constexpr (KIND == kProductDense) {
                 v0 = fmaf(alpha, v0, extra[u]);
                 v1 = fmaf(alpha, v1, extra[u + 1]);
               }
-              packed[(c + u) / 2] = to16(v0, f16) | (to16(v1, f16) << 16);
+              packed[(c + u) / 2] = pack_out(v0, v1, f16);
             }
           }
         }
@@ -719,12 +814,32 @@ __global__ void __launch_bounds__(kPThreads, 1)
           // the accumulator is free before any store
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(tempty(acc), 0));
+          if (lane == 0) arrive_relaxed_cluster(ptx::map_to_rank(tempty(acc), 0));
           acc ^= 1;
           if (acc == 0) acc_phase ^= 1u;
         }
         const int64_t j = static_cast<int64_t>(t.j0) + col_begin;
-        if (paired) {
+        if (KIND == kProductGroups && p.staged) {
+#pragma unroll
+          for (int c = 0; c < COLS; c += 32) {
+            if (c < ncols) {
+              if (lane == 0) tma_store_read_done();
+              __syncwarp();
+#pragma unroll
+              for (int u = 0; u < 32; u += 2) {
+                const uint32_t v = swap_pair(packed[(c + u) / 2], lane);
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage_at + (u + (lane & 1)) * 64 +
+                                                             (lane & ~1) * 2),
+                             "r"(v)
+                             : "memory");
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0 && i < p.M)
+                tma_store_3d<false>(&tm_out, stage_at, i, t.j0 + col_begin + c, t.z);
+            }
+          }
+        } else if (paired) {
           uint16_t* dst = out + (j + (lane & 1)) * p.ld_out + (i & ~1);
 #pragma unroll
           for (int c = 0; c < COLS; c += 2) {
@@ -755,6 +870,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
   }
 
+  if (C::STAGED && warp >= 3 && lane == 0) tma_store_done();
   ptx::tc_fence_before();
   __syncthreads();
   // no signal, copy or MMA read crosses between the two CTAs after this

@@ -48,6 +48,28 @@ bool tmap3(CUtensorMap* m, const void* base, int32_t type, int64_t inner, int64_
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map of a result [z][rows][cols] for bulk copies out of shared memory; false
+// where its address or strides are no multiples of 16 bytes.
+bool staged_out(CUtensorMap* m, void* out, int32_t type, int64_t cols, int64_t rows, int64_t z,
+                int64_t ld, int64_t zs) {
+  const int64_t bytes = type == BEAM_DTYPE_F32 ? 4 : 2;
+  if (z <= 1) zs = ld * rows;
+  if ((reinterpret_cast<uintptr_t>(out) & 15u) || ld * bytes % 16 || zs * bytes % 16) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(z)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * bytes),
+                           static_cast<cuuint64_t>(zs * bytes)};
+  cuuint32_t box[3] = {32, type == BEAM_DTYPE_F32 ? 16u : 32u, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUtensorMapDataType t = type == BEAM_DTYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : type == BEAM_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return beam::host::g_encode(m, t, 3, out, dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                              CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 beam_status_t device_ready(beam::host::DevInfo* dev) {
   if (!beam::host::device_info(dev)) return BEAM_ERR_CUDA;
   if (!dev->supported) return BEAM_ERR_UNSUPPORTED;
@@ -163,7 +185,7 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   if (pack_b) b.pack_into(static_cast<uint8_t*>(ws) + at_b, s);
   CUtensorMap ta, tb;
   if (!tmap3(&ta, a.base, g.dtype, a.inner, a.outer, a.z, a.ld, a.zs, a_mn ? 64 : 128) ||
-      !tmap3(&tb, b.base, g.dtype, b.inner, b.outer, b.z, b.ld, b.zs, b_mn ? 64 : nt / 2))
+      !tmap3(&tb, b.base, g.dtype, b.inner, b.outer, b.z, b.ld, b.zs, b_mn ? 64 : beam::product_box_rows(nt)))
     return BEAM_ERR_CUDA;
   ProductArgs p = {};
   p.M = static_cast<int32_t>(M);
@@ -183,7 +205,10 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   p.alpha = 1.f;
   p.status = static_cast<uint32_t*>(ws);
   p.wait_limit_ns = beam::host::wait_limit_ns();
-  return launched(beam::launch_pair_product(kind, nt, a_mn, b_mn, ta, tb, p, false, s));
+  CUtensorMap to = {};
+  p.staged = staged_out(&to, out, g.out_dtype, M, N, kind == beam::kProductGroups ? g.n_groups : 1,
+                        ld_out, z_out);
+  return launched(beam::launch_pair_product(kind, nt, a_mn, b_mn, ta, tb, to, p, false, s));
 }
 
 // ------------------------------------------------------ orthogonalised update
@@ -432,13 +457,13 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
   for (int i = 0; i < 2; ++i) {
     const int64_t z = i == 0 && split ? 2 * batch : batch;
     if (!tmap3(&ga[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? 128 : 64) ||
-        !tmap3(&gb[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? nt_gram / 2 : 64) ||
-        !tmap3(&sx[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? 64 : nt_step / 2))
+        !tmap3(&gb[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? beam::product_box_rows(nt_gram) : 64) ||
+        !tmap3(&sx[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? 64 : beam::product_box_rows(nt_step)))
       return BEAM_ERR_CUDA;
   }
   if (!tmap3(&pa, gram, F16, m, m, batch, L.ldm, m * L.ldm, 128) ||
-      !tmap3(&pb, gram, F16, m, m, batch, L.ldm, m * L.ldm, nt_poly / 2) ||
-      !tmap3(&sp, poly, F16, m, m, batch, L.ldm, m * L.ldm, wide ? nt_step / 2 : 128))
+      !tmap3(&pb, gram, F16, m, m, batch, L.ldm, m * L.ldm, beam::product_box_rows(nt_poly)) ||
+      !tmap3(&sp, poly, F16, m, m, batch, L.ldm, m * L.ldm, wide ? beam::product_box_rows(nt_step) : 128))
     return BEAM_ERR_CUDA;
 
   ProductArgs base = {};
@@ -448,6 +473,7 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
   base.out_type = F16;
   base.status = static_cast<uint32_t*>(workspace);
   base.wait_limit_ns = beam::host::wait_limit_ns();
+  const CUtensorMap none = {};
   for (int t = 0; t < d->steps; ++t) {
     const bool last = t + 1 == d->steps;
     const int cur = t & 1;
@@ -462,7 +488,7 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
     g.alpha = t == 0 ? 1.f : kScaleGram / (kScaleX * kScaleX);
     g.alpha_z = t == 0 ? n.alpha_gram : nullptr;
     cudaError_t e = beam::launch_pair_product(beam::kProductDense, nt_gram, !wide, !wide, ga[cur],
-                                              gb[cur], g, true, s);
+                                              gb[cur], none, g, true, s);
     if (e != cudaSuccess) return BEAM_ERR_CUDA;
 
     ProductArgs q = base;  // P = a I + b A + c A A
@@ -477,7 +503,7 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
     q.beta = kScalePoly * d->b / kScaleGram;
     q.diag = kScalePoly * d->a;
     q.add = gram;
-    e = beam::launch_pair_product(beam::kProductDense, nt_poly, false, false, pa, pb, q, true, s);
+    e = beam::launch_pair_product(beam::kProductDense, nt_poly, false, false, pa, pb, none, q, true, s);
     if (e != cudaSuccess) return BEAM_ERR_CUDA;
 
     ProductArgs u = base;  // X <- P X (wide) or X P (tall)
@@ -496,10 +522,10 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
     const float out_scale = last ? 1.f : kScaleX;
     u.alpha = t == 0 ? 1.f : out_scale / (kScalePoly * kScaleX);
     u.alpha_z = t == 0 ? n.alpha_step : nullptr;
-    e = wide ? beam::launch_pair_product(beam::kProductDense, nt_step, true, false, sx[cur], sp, u,
-                                         true, s)
+    e = wide ? beam::launch_pair_product(beam::kProductDense, nt_step, true, false, sx[cur], sp, none,
+                                         u, true, s)
              : beam::launch_pair_product(beam::kProductDense, nt_step, false, false, sp, sx[cur],
-                                         u, true, s);
+                                         none, u, true, s);
     if (e != cudaSuccess) return BEAM_ERR_CUDA;
   }
   return BEAM_OK;
