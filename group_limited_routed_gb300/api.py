@@ -7,7 +7,9 @@ fallback: without the compiled library every entry point raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -107,6 +109,8 @@ def library_path() -> str:
 def lib():
     """Load libbeam_moe.so; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -753,38 +757,95 @@ def _type(dtype, name: str, allowed) -> int:
 _HALVES = (torch.bfloat16, torch.float16)
 
 
-def _rows2d(t: torch.Tensor, name: str, dtype=None, width=None) -> int:
-    """Check a CUDA matrix with contiguous rows; returns its row stride."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+# The checks of a call depend on shapes, strides, types and devices alone, so
+# their outcome (the C description, the output's shape) is kept by those: a
+# step that repeats its shapes pays a dictionary look-up.  Pointers, streams
+# and contents are looked at in every call.
+_plans = functools.lru_cache(maxsize=1024)
+
+
+def _meta(t, name: str) -> tuple:
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or (width is not None and t.shape[1] != width):
+    return t.shape, t.stride(), t.dtype, t.device
+
+
+def _row_stride(meta, name: str, dtype=None, rows=None, width=None, device=None) -> int:
+    """Check a CUDA matrix with contiguous rows; returns its row stride."""
+    shape, stride, dt, dev = meta
+    if dev.type != "cuda":
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if device is not None and dev != device:
+        raise ValueError(f"{name} must be on {device}, got {dev}")
+    if dtype is not None and dt != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {dt}")
+    if len(shape) != 2 or (width is not None and shape[1] != width):
         raise ValueError(f"{name} must be a matrix"
                          + (f" with {width} columns" if width is not None else "")
-                         + f", got shape {tuple(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows, got strides {t.stride()}")
-    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
-    if ld < t.shape[1]:
-        raise ValueError(f"{name} must not have overlapping rows, got strides {t.stride()}")
+                         + f", got shape {tuple(shape)}")
+    if rows is not None and shape[0] != rows:
+        raise ValueError(f"{name} must have {rows} rows, got {shape[0]}")
+    if shape[1] > 1 and stride[1] != 1:
+        raise ValueError(f"{name} must have contiguous rows, got strides {stride}")
+    ld = stride[0] if shape[0] > 1 else shape[1]
+    if ld < shape[1]:
+        raise ValueError(f"{name} must not have overlapping rows, got strides {stride}")
     return ld
 
 
-def _same_device(first: torch.Tensor, **others) -> None:
-    for name, t in others.items():
-        if isinstance(t, torch.Tensor) and t.device != first.device:
-            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+def _vector(meta, name: str, dtype, device, length=None) -> None:
+    shape, stride, dt, dev = meta
+    if dev.type != "cuda":
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if dt != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {dt}")
+    if dev != device:
+        raise ValueError(f"{name} must be on {device}, got {dev}")
+    if len(shape) != 1 or (length is not None and shape[0] != length):
+        raise ValueError(f"{name} must be a vector"
+                         + (f" of {length}" if length is not None else "")
+                         + f", got shape {tuple(shape)}")
+    if shape[0] > 1 and stride[0] != 1:
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _offsets(offsets, n_groups=None) -> int:
-    ptr = _dev(offsets, torch.int32, "offsets")
-    if offsets.dim() != 1 or offsets.numel() < 2:
-        raise ValueError("offsets must be a vector of at least 2 boundaries, "
-                         f"got shape {tuple(offsets.shape)}")
-    if n_groups is not None and offsets.numel() != n_groups + 1:
-        raise ValueError(f"offsets must hold {n_groups + 1} boundaries, got {offsets.numel()}")
-    return ptr
+def _dense(meta, name: str, dtype, shape, device) -> None:
+    """Check a given output: this shape and type, contiguous."""
+    got, stride, dt, dev = meta
+    if dev != device:
+        raise ValueError(f"{name} must be on {device}, got {dev}")
+    if dt != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {dt}")
+    if tuple(got) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(got)}")
+    step = 1
+    for n, s in zip(reversed(got), reversed(stride)):
+        if n > 1 and s != step:
+            raise ValueError(f"{name} must be contiguous")
+        step *= n
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _current(device):
+    """A context in which `device` is current (it usually is)."""
+    return _HERE_ALREADY if device.index == torch.cuda.current_device() \
+        else torch.cuda.device(device)
+
+
+def _raw_stream(stream, index: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _temporary(t: torch.Tensor, stream) -> torch.Tensor:
+    """Memory this module allocated for a call on a stream that is not the
+    current one: the allocator must not hand it out before that work is done."""
+    if isinstance(stream, torch.cuda.Stream):
+        t.record_stream(stream)
+    return t
 
 
 def _grouped_desc(rows, E, N, K, dtype, out_dtype, x_ld, y_ld, w_strides) -> _Grouped:
@@ -794,15 +855,18 @@ def _grouped_desc(rows, E, N, K, dtype, out_dtype, x_ld, y_ld, w_strides) -> _Gr
                     _type(out_dtype, "out_dtype", (dtype, torch.float32)), x_ld, y_ld, *w_strides)
 
 
-def _w_strides(w, dtype) -> tuple:
-    if not isinstance(w, torch.Tensor) or not w.is_cuda:
+def _w_strides(meta, dtype, device) -> tuple:
+    shape, stride, dt, dev = meta
+    if dev.type != "cuda":
         raise TypeError("w must be a CUDA tensor")
-    if w.dtype != dtype:
-        raise TypeError(f"w must be {dtype}, got {w.dtype}")
-    if w.dim() != 3 or w.numel() == 0:
-        raise ValueError(f"w must be [groups, N, K], got shape {tuple(w.shape)}")
-    E, N, K = w.shape
-    e, n, k = w.stride()
+    if dt != dtype:
+        raise TypeError(f"w must be {dtype}, got {dt}")
+    if dev != device:
+        raise ValueError(f"w must be on {device}, got {dev}")
+    if len(shape) != 3 or 0 in shape:
+        raise ValueError(f"w must be [groups, N, K], got shape {tuple(shape)}")
+    E, N, K = shape
+    e, n, k = stride
     if K == 1 and n != 1:
         k = 1
     if N == 1 and k != 1:
@@ -812,53 +876,62 @@ def _w_strides(w, dtype) -> tuple:
     elif n == 1 and (K == 1 or k >= N):
         k = N if K == 1 else k
     else:
-        raise ValueError(f"w must be contiguous along N or K, got strides {w.stride()}")
+        raise ValueError(f"w must be contiguous along N or K, got strides {stride}")
     return (e if E > 1 else N * K), n, k
 
 
-def grouped_matmul_workspace_size(rows: int, n_groups: int, N: int, K: int,
-                                  dtype=torch.bfloat16, unaligned: bool = False) -> int:
-    """Workspace bytes of the grouped products on contiguous operands (with
-    ``unaligned``, of views whose base or strides are not 16-byte multiples)."""
-    d = _grouped_desc(rows, n_groups, N, K, dtype, dtype, K, N, (N * K, K, 1))
+def _grouped_size(d: _Grouped, unaligned: bool) -> int:
     n = lib().beam_moe_grouped_matmul_workspace_size(ctypes.byref(d), int(unaligned))
     if n == 0:
         raise BeamError(1, "beam_moe_grouped_matmul_workspace_size")
     return int(n)
 
 
-def _op_ws(ws, device, size) -> "OpWorkspace":
-    return OpWorkspace(size(), device) if ws is None else ws
+def grouped_matmul_workspace_size(rows: int, n_groups: int, N: int, K: int,
+                                  dtype=torch.bfloat16, unaligned: bool = False) -> int:
+    """Workspace bytes of the grouped products on contiguous operands (with
+    ``unaligned``, of views whose base or strides are not 16-byte multiples)."""
+    return _grouped_size(_grouped_desc(rows, n_groups, N, K, dtype, dtype, K, N,
+                                       (N * K, K, 1)), unaligned)
 
 
-def _grouped_ws(ws, d, device, *operands):
-    def size():
-        odd = any(t.data_ptr() % 16 for t in operands)
-        n = lib().beam_moe_grouped_matmul_workspace_size(ctypes.byref(d), int(odd))
-        if n == 0:
-            raise BeamError(1, "beam_moe_grouped_matmul_workspace_size")
-        return n
-    return _op_ws(ws, device, size)
+def _grouped_ws(d, a, b, stream) -> OpWorkspace:
+    """A workspace for one call, when the caller keeps none."""
+    ws = OpWorkspace(_grouped_size(d, bool(a.data_ptr() % 16 or b.data_ptr() % 16)), a.device)
+    _temporary(ws.buf, stream)
+    return ws
 
 
-def _grouped_rows(a, a_name, w, offsets, out, out_dtype, ws, transpose):
-    """y = x W^T or, with ``transpose``, dx = dy W, group by group."""
-    strides = _w_strides(w, a.dtype if isinstance(a, torch.Tensor) else None)
-    E, N, K = w.shape
+@_plans
+def _rows_plan(transpose, a, w, off, out, out_dtype):
+    """(description, its reference, output shape and type, device)."""
+    name = "dy" if transpose else "x"
+    device = a[3]
+    _row_stride(a, name)
+    strides = _w_strides(w, a[2], device)
+    E, N, K = w[0]
     width_in, width_out = (N, K) if transpose else (K, N)
-    ld = _rows2d(a, a_name, width=width_in)
-    _same_device(a, w=w, offsets=offsets, out=out)
-    dt = out_dtype if out_dtype is not None else out.dtype if out is not None else a.dtype
-    off = _offsets(offsets, E)
-    if out is None:
-        out = torch.empty(a.shape[0], width_out, dtype=dt, device=a.device)
-    out_ld = _rows2d(out, "out", dt, width_out)
-    if out.shape[0] != a.shape[0]:
-        raise ValueError(f"out must have {a.shape[0]} rows, got {out.shape[0]}")
+    ld = _row_stride(a, name, width=width_in)
+    _vector(off, "offsets", torch.int32, device, E + 1)
+    dt = out_dtype if out_dtype is not None else out[2] if out is not None else a[2]
+    rows = a[0][0]
+    out_ld = width_out if out is None else _row_stride(out, "out", dt, rows, width_out, device)
     x_ld, y_ld = (out_ld, ld) if transpose else (ld, out_ld)
-    d = _grouped_desc(a.shape[0], E, N, K, a.dtype, dt, x_ld, y_ld, strides)
-    ws = _grouped_ws(ws, d, a.device, a, w)
-    return d, off, out, ws
+    d = _grouped_desc(rows, E, N, K, a[2], dt, x_ld, y_ld, strides)
+    return d, ctypes.byref(d), (rows, width_out), dt, device
+
+
+def _rows_call(transpose, a, w, offsets, out, out_dtype, ws, stream):
+    d, ref, shape, dt, device = _rows_plan(
+        transpose, _meta(a, "dy" if transpose else "x"), _meta(w, "w"), _meta(offsets, "offsets"),
+        None if out is None else _meta(out, "out"), out_dtype)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=device)
+        if stream is not None:
+            _temporary(out, stream)
+    if ws is None:
+        ws = _grouped_ws(d, a, w, stream)
+    return ref, out, ws, device
 
 
 def grouped_matmul(x, w, offsets, out=None, out_dtype=None, ws: OpWorkspace | None = None,
@@ -869,10 +942,11 @@ def grouped_matmul(x, w, offsets, out=None, out_dtype=None, ws: OpWorkspace | No
     x [rows, K] and w [E, N, K] are BF16 or F16 (w contiguous along N or K, so
     ``w.transpose(1, 2)`` of a [E, K, N] tensor is read in place), offsets
     int32 [E + 1].  y [rows, N] has x's type or FP32."""
-    d, off, y, ws = _grouped_rows(x, "x", w, offsets, out, out_dtype, ws, False)
-    with torch.cuda.device(x.device):
-        _check(lib().beam_moe_grouped_matmul(ctypes.byref(d), x.data_ptr(), w.data_ptr(), off,
-                                             y.data_ptr(), ws.ptr, ws.nbytes, _stream(stream)),
+    ref, y, ws, dev = _rows_call(False, x, w, offsets, out, out_dtype, ws, stream)
+    with _current(dev):
+        _check(lib().beam_moe_grouped_matmul(ref, x.data_ptr(), w.data_ptr(), offsets.data_ptr(),
+                                             y.data_ptr(), ws.ptr, ws.nbytes,
+                                             _raw_stream(stream, dev.index)),
                "beam_moe_grouped_matmul")
     return y
 
@@ -880,12 +954,33 @@ def grouped_matmul(x, w, offsets, out=None, out_dtype=None, ws: OpWorkspace | No
 def grouped_matmul_dx(dy, w, offsets, out=None, out_dtype=None, ws: OpWorkspace | None = None,
                       stream=None):
     """The input gradient of ``grouped_matmul``: dx[r] = W[e]^T dy[r]."""
-    d, off, dx, ws = _grouped_rows(dy, "dy", w, offsets, out, out_dtype, ws, True)
-    with torch.cuda.device(dy.device):
-        _check(lib().beam_moe_grouped_matmul_dx(ctypes.byref(d), dy.data_ptr(), w.data_ptr(), off,
-                                                dx.data_ptr(), ws.ptr, ws.nbytes,
-                                                _stream(stream)), "beam_moe_grouped_matmul_dx")
+    ref, dx, ws, dev = _rows_call(True, dy, w, offsets, out, out_dtype, ws, stream)
+    with _current(dev):
+        _check(lib().beam_moe_grouped_matmul_dx(ref, dy.data_ptr(), w.data_ptr(),
+                                                offsets.data_ptr(), dx.data_ptr(), ws.ptr,
+                                                ws.nbytes, _raw_stream(stream, dev.index)),
+               "beam_moe_grouped_matmul_dx")
     return dx
+
+
+@_plans
+def _dw_plan(dy, x, off, out, accumulate, out_dtype):
+    device = dy[3]
+    y_ld = _row_stride(dy, "dy")
+    x_ld = _row_stride(x, "x", dy[2], dy[0][0], device=device)
+    _vector(off, "offsets", torch.int32, device)
+    if off[0][0] < 2:
+        raise ValueError(f"offsets must hold at least 2 boundaries, got {off[0][0]}")
+    E, N, K = off[0][0] - 1, dy[0][1], x[0][1]
+    dt = out_dtype if out_dtype is not None else out[2] if out is not None else dy[2]
+    if accumulate and (out is None or dt != torch.float32):
+        raise ValueError("accumulate needs an FP32 out to add to")
+    # W takes no part: described so that it needs no aligned copy
+    k8 = (K + 7) // 8 * 8
+    d = _grouped_desc(dy[0][0], E, N, K, dy[2], dt, x_ld, y_ld, (k8 * N, k8, 1))
+    if out is not None:
+        _dense(out, "out", dt, (E, N, K), device)
+    return d, ctypes.byref(d), (E, N, K), dt, device
 
 
 def grouped_matmul_dw(dy, x, offsets, out=None, accumulate: bool = False, out_dtype=None,
@@ -893,71 +988,58 @@ def grouped_matmul_dw(dy, x, offsets, out=None, accumulate: bool = False, out_dt
     """The weight gradient of ``grouped_matmul``: dW[e] = sum over the rows of
     group e of dy[r] x[r]^T, [E, N, K] in the operands' type or FP32; zero for
     a group without rows.  ``accumulate`` adds to ``out`` (FP32)."""
-    y_ld = _rows2d(dy, "dy")
-    x_ld = _rows2d(x, "x", dy.dtype)
-    if x.shape[0] != dy.shape[0]:
-        raise ValueError(f"x and dy must have the same rows, got {x.shape[0]} and {dy.shape[0]}")
-    _same_device(dy, x=x, offsets=offsets, out=out)
-    off = _offsets(offsets)
-    E, N, K = offsets.numel() - 1, dy.shape[1], x.shape[1]
-    dt = out_dtype if out_dtype is not None else out.dtype if out is not None else dy.dtype
-    if accumulate and (out is None or dt != torch.float32):
-        raise ValueError("accumulate needs an FP32 out to add to")
-    d = _grouped_desc(x.shape[0], E, N, K, dy.dtype, dt, x_ld, y_ld, (N * K, K, 1))
+    d, ref, shape, dt, dev = _dw_plan(_meta(dy, "dy"), _meta(x, "x"), _meta(offsets, "offsets"),
+                                      None if out is None else _meta(out, "out"),
+                                      bool(accumulate), out_dtype)
     if out is None:
-        out = torch.empty(E, N, K, dtype=dt, device=dy.device)
-    if tuple(out.shape) != (E, N, K):
-        raise ValueError(f"out must be {(E, N, K)}, got {tuple(out.shape)}")
-    dst = _dev(out, dt, "out")
+        out = torch.empty(shape, dtype=dt, device=dev)
+        if stream is not None:
+            _temporary(out, stream)
     if ws is None:
-        # W takes no part: describe one that needs no copy
-        d.w_stride_n, d.w_stride_e = (K + 7) // 8 * 8, (K + 7) // 8 * 8 * N
-    ws = _grouped_ws(ws, d, dy.device, dy, x)
-    with torch.cuda.device(dy.device):
-        _check(lib().beam_moe_grouped_matmul_dw(ctypes.byref(d), dy.data_ptr(), x.data_ptr(), off,
-                                                int(accumulate), dst, ws.ptr, ws.nbytes,
-                                                _stream(stream)), "beam_moe_grouped_matmul_dw")
+        ws = _grouped_ws(d, dy, x, stream)
+    with _current(dev):
+        _check(lib().beam_moe_grouped_matmul_dw(ref, dy.data_ptr(), x.data_ptr(),
+                                                offsets.data_ptr(), int(accumulate),
+                                                out.data_ptr(), ws.ptr, ws.nbytes,
+                                                _raw_stream(stream, dev.index)),
+               "beam_moe_grouped_matmul_dw")
     return out
 
 
-def _row_weight(row_weight, rows: int):
-    if row_weight is None:
-        return None
-    ptr = _dev(row_weight, torch.float32, "row_weight")
-    if tuple(row_weight.shape) != (rows,):
-        raise ValueError(f"row_weight must be [{rows}], got {tuple(row_weight.shape)}")
-    return ptr
+@_plans
+def _gate_plan(gate, up, row_weight, dh, outs):
+    """(description's reference, row strides of dh and the outputs, device)."""
+    device, dt = gate[3], gate[2]
+    g_ld = _row_stride(gate, "gate")
+    rows, F = gate[0]
+    u_ld = _row_stride(up, "up", dt, rows, F, device)
+    if row_weight is not None:
+        _vector(row_weight, "row_weight", torch.float32, device, rows)
+    dh_ld = 0 if dh is None else _row_stride(dh, "dh", dt, rows, F, device)
+    lds = tuple(F if o is None else _row_stride(o, "out", dt, rows, F, device) for o in outs)
+    d = _Gate(rows, F, _type(dt, "gate", _HALVES), g_ld, u_ld)
+    return d, ctypes.byref(d), dh_ld, lds, device
 
 
-def _gate_desc(gate, up):
-    g_ld = _rows2d(gate, "gate")
-    u_ld = _rows2d(up, "up", gate.dtype, gate.shape[1])
-    if up.shape[0] != gate.shape[0]:
-        raise ValueError(f"gate and up must have the same rows, got {gate.shape[0]} "
-                         f"and {up.shape[0]}")
-    return _Gate(gate.shape[0], gate.shape[1], _type(gate.dtype, "gate", _HALVES), g_ld, u_ld)
-
-
-def _like(out, like, name):
-    if out is None:
-        out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    ld = _rows2d(out, name, like.dtype, like.shape[1])
-    if out.shape[0] != like.shape[0]:
-        raise ValueError(f"{name} must have {like.shape[0]} rows, got {out.shape[0]}")
-    _same_device(like, **{name: out})
-    return out, ld
+def _like(t, stream):
+    out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    if stream is not None:
+        _temporary(out, stream)
+    return out
 
 
 def swiglu(gate, up, row_weight=None, out=None, stream=None):
     """h = row_weight[r] * silu(gate) * up (BF16 or F16 [rows, F], row strides
     free; FP32 inside, rounded once).  Without row_weight the factor is 1."""
-    d = _gate_desc(gate, up)
-    _same_device(gate, up=up, row_weight=row_weight)
-    h, h_ld = _like(out, gate, "out")
-    w = _row_weight(row_weight, gate.shape[0])
-    with torch.cuda.device(gate.device):
-        _check(lib().beam_moe_swiglu(ctypes.byref(d), gate.data_ptr(), up.data_ptr(), w,
-                                     h.data_ptr(), h_ld, _stream(stream)), "beam_moe_swiglu")
+    _, ref, _, (h_ld,), dev = _gate_plan(
+        _meta(gate, "gate"), _meta(up, "up"),
+        None if row_weight is None else _meta(row_weight, "row_weight"), None,
+        (None if out is None else _meta(out, "out"),))
+    h = _like(gate, stream) if out is None else out
+    w = None if row_weight is None else row_weight.data_ptr()
+    with _current(dev):
+        _check(lib().beam_moe_swiglu(ref, gate.data_ptr(), up.data_ptr(), w, h.data_ptr(), h_ld,
+                                     _raw_stream(stream, dev.index)), "beam_moe_swiglu")
     return h
 
 
@@ -965,20 +1047,20 @@ def swiglu_grad(dh, gate, up, row_weight=None, out=None, stream=None):
     """The gradient of ``swiglu``: (dgate, dup) and, with row_weight, its own
     gradient (FP32 [rows]).  ``out``: (dgate, dup) to write to; they may be
     gate and up themselves."""
-    d = _gate_desc(gate, up)
-    dh_ld = _rows2d(dh, "dh", gate.dtype, gate.shape[1])
-    if dh.shape[0] != gate.shape[0]:
-        raise ValueError(f"dh must have {gate.shape[0]} rows, got {dh.shape[0]}")
-    _same_device(gate, up=up, dh=dh, row_weight=row_weight)
-    dg, dg_ld = _like(None if out is None else out[0], gate, "dgate")
-    du, du_ld = _like(None if out is None else out[1], gate, "dup")
-    w = _row_weight(row_weight, gate.shape[0])
-    dw = None if w is None else torch.empty(gate.shape[0], dtype=torch.float32, device=gate.device)
-    with torch.cuda.device(gate.device):
-        _check(lib().beam_moe_swiglu_grad(ctypes.byref(d), dh.data_ptr(), dh_ld, gate.data_ptr(),
+    _, ref, dh_ld, (dg_ld, du_ld), dev = _gate_plan(
+        _meta(gate, "gate"), _meta(up, "up"),
+        None if row_weight is None else _meta(row_weight, "row_weight"), _meta(dh, "dh"),
+        (None, None) if out is None else (_meta(out[0], "out"), _meta(out[1], "out")))
+    dg, du = (_like(gate, stream), _like(gate, stream)) if out is None else out
+    w = dw = None
+    if row_weight is not None:
+        w = row_weight.data_ptr()
+        dw = _like(row_weight, stream)
+    with _current(dev):
+        _check(lib().beam_moe_swiglu_grad(ref, dh.data_ptr(), dh_ld, gate.data_ptr(),
                                           up.data_ptr(), w, dg.data_ptr(), dg_ld, du.data_ptr(),
                                           du_ld, None if dw is None else dw.data_ptr(),
-                                          _stream(stream)), "beam_moe_swiglu_grad")
+                                          _raw_stream(stream, dev.index)), "beam_moe_swiglu_grad")
     return (dg, du) if dw is None else (dg, du, dw)
 
 
@@ -991,6 +1073,37 @@ def orthogonalize_workspace_size(batch: int, rows: int, cols: int, dtype=torch.f
     return int(n)
 
 
+@_plans
+def _ortho_plan(m, steps, coeffs, eps, out, out_dtype):
+    shape, stride, dt, device = m
+    if device.type != "cuda":
+        raise TypeError("m must be a CUDA tensor")
+    if len(shape) < 2:
+        raise ValueError(f"m must be a matrix or a stack of them, got shape {tuple(shape)}")
+    if len(coeffs) != 3:
+        raise ValueError(f"coeffs must be (a, b, c), got {len(coeffs)} values")
+    kind = _type(dt, "m", _HALVES + (torch.float32,))
+    odt = out_dtype if out_dtype is not None else out[2] if out is not None else \
+        dt if dt in _HALVES else torch.bfloat16
+    out_kind = _type(odt, "out_dtype", _HALVES)
+    if out is not None:
+        _dense(out, "out", odt, shape, device)
+    if 0 in shape:
+        return None, None, tuple(shape), odt, device
+    batch = 1
+    for n in shape[:-2]:
+        batch *= n
+    R, C = shape[-2:]
+    if len(shape) > 3:
+        # several leading axes: one if their strides nest, else a copy
+        probe = torch.empty_strided(shape, stride, dtype=dt, device="meta").reshape(batch, R, C)
+        strides = probe.stride()
+    else:
+        strides = ((0,) if len(shape) == 2 else ()) + tuple(stride)
+    d = _Ortho(batch, R, C, kind, out_kind, steps, *coeffs, eps, *strides)
+    return d, ctypes.byref(d), tuple(shape), odt, device
+
+
 def orthogonalize(m, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: float = 1e-7,
                   out=None, out_dtype=None, ws: OpWorkspace | None = None, stream=None):
     """The update m [..., R, C] orthogonalised matrix by matrix: X = M / (|M|_F
@@ -1000,29 +1113,25 @@ def orthogonalize(m, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: floa
     m is BF16, F16 or FP32 with any strides; the result is BF16 or F16
     (``out_dtype``; m's own 16-bit type, BF16 for FP32) and accurate to about
     2e-3 of its norm."""
-    if not isinstance(m, torch.Tensor) or not m.is_cuda:
-        raise TypeError("m must be a CUDA tensor")
-    if m.dim() < 2:
-        raise ValueError(f"m must be a matrix or a stack of them, got shape {tuple(m.shape)}")
-    kind = _type(m.dtype, "m", _HALVES + (torch.float32,))
-    dt = out_dtype if out_dtype is not None else out.dtype if out is not None else \
-        m.dtype if m.dtype in _HALVES else torch.bfloat16
-    out_kind = _type(dt, "out_dtype", _HALVES)
-    R, C = m.shape[-2:]
-    stack = m if m.dim() == 3 else m.reshape(-1, R, C) if m.numel() else m.new_empty(0, R, C)
-    batch = stack.shape[0]
+    d, ref, shape, dt, dev = _ortho_plan(
+        _meta(m, "m"), int(steps), tuple(float(v) for v in coeffs), float(eps),
+        None if out is None else _meta(out, "out"), out_dtype)
     if out is None:
-        out = torch.empty(m.shape, dtype=dt, device=m.device)
-    if out.shape != m.shape:
-        raise ValueError(f"out must be {tuple(m.shape)}, got {tuple(out.shape)}")
-    _same_device(m, out=out)
-    dst = _dev(out, dt, "out")
-    if m.numel() == 0:
+        out = torch.empty(shape, dtype=dt, device=dev)
+        if stream is not None:
+            _temporary(out, stream)
+    if d is None:
         return out
-    d = _Ortho(batch, R, C, kind, out_kind, int(steps), *(float(v) for v in coeffs), float(eps),
-               *stack.stride())
-    ws = _op_ws(ws, m.device, lambda: orthogonalize_workspace_size(batch, R, C, m.dtype))
-    with torch.cuda.device(m.device):
-        _check(lib().beam_moe_orthogonalize(ctypes.byref(d), stack.data_ptr(), dst, ws.ptr,
-                                            ws.nbytes, _stream(stream)), "beam_moe_orthogonalize")
+    stack = m
+    if m.dim() > 3:
+        stack = m.reshape(d.batch, d.rows, d.cols)
+        if stack.data_ptr() != m.data_ptr() and stream is not None:
+            _temporary(stack, stream)
+    if ws is None:
+        ws = OpWorkspace(orthogonalize_workspace_size(d.batch, d.rows, d.cols, m.dtype), dev)
+        _temporary(ws.buf, stream)
+    with _current(dev):
+        _check(lib().beam_moe_orthogonalize(ref, stack.data_ptr(), out.data_ptr(), ws.ptr,
+                                            ws.nbytes, _raw_stream(stream, dev.index)),
+               "beam_moe_orthogonalize")
     return out
