@@ -670,8 +670,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     constexpr int GROUPS = kPEpiWarps / 4;
     constexpr int COLS = NT / GROUPS < 16 ? 16 : NT / GROUPS;  // rows j per warp
     const int col_begin = ((warp - 3) >> 2) * COLS;
-    // TMEM columns per load; the affine epilogue needs the registers itself
-    constexpr int LD = COLS < 32 || KIND == kProductDense ? 16 : 32;
+    // TMEM columns per load
+    constexpr int LD = COLS < 32 ? 16 : 32;
     const uint32_t stage_at = ring + C::STAGING + (warp - 3) * 2048;
     const bool f16 = p.out_type == kF16;
     // two columns per store where every address of it is 4-byte aligned
@@ -767,6 +767,23 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
       } else {
         const bool live = t.k_blocks > 0;
+        uint32_t packed[COLS / 2];  // rows (2c, 2c + 1) of this lane's column
+        const bool with_add = KIND == kProductDense && p.add;
+        if (with_add) {
+          // the addend, fetched while the tile's MMAs run: two columns and
+          // one row per lane (rows are padded to even lengths), then swapped
+          // to one column and two rows as the results will be
+          const uint16_t* src = p.add + zbase +
+                                (static_cast<int64_t>(t.j0) + col_begin + (lane & 1)) * p.ld_out +
+                                (i & ~1);
+#pragma unroll
+          for (int c = 0; c < COLS; c += 2)
+            packed[c / 2] = (i & ~1) < p.M && c + (lane & 1) < ncols
+                                ? *reinterpret_cast<const uint32_t*>(src + c * p.ld_out)
+                                : 0u;
+#pragma unroll
+          for (int c = 0; c < COLS; c += 2) packed[c / 2] = swap_pair(packed[c / 2], lane);
+        }
         if (live) {
           if (!W.wait(tfull(acc), acc_phase)) break;
           ptx::tc_fence_after();
@@ -775,24 +792,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
         float alpha = p.alpha;
         if (KIND == kProductDense && p.alpha_z) alpha *= p.alpha_z[t.z];
         uint16_t* out = static_cast<uint16_t*>(p.out) + zbase;
-        const uint16_t* add = KIND == kProductDense && p.add ? p.add + zbase : nullptr;
-        uint32_t packed[COLS / 2];  // rows (2c, 2c + 1) of this lane's column
+        const int on_diag = i - t.j0 - col_begin;
 #pragma unroll
         for (int c = 0; c < COLS; c += LD) {
           if (c < ncols) {
             uint32_t r[LD];
-            float extra[KIND == kProductDense ? LD : 1];
             if (live) tmem_ld(tq + c, r);
-            if constexpr (KIND == kProductDense) {
-#pragma unroll
-              for (int u = 0; u < LD; ++u) {
-                const int j = t.j0 + col_begin + c + u;
-                extra[u] = (add && i < p.M && c + u < ncols)
-                               ? p.beta * __half2float(__ushort_as_half(add[static_cast<int64_t>(j) * p.ld_out + i]))
-                               : 0.f;
-                if (j == i) extra[u] += p.diag;
-              }
-            }
             if (live) {
               ptx::tmem_wait_ld();
             } else {
@@ -803,8 +808,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int u = 0; u < LD; u += 2) {
               float v0 = __uint_as_float(r[u]), v1 = __uint_as_float(r[u + 1]);
               if constexpr (KIND == kProductDense) {
-                v0 = fmaf(alpha, v0, extra[u]);
-                v1 = fmaf(alpha, v1, extra[u + 1]);
+                v0 *= alpha;
+                v1 *= alpha;
+                if (with_add) {
+                  const __half2 a =
+                      *reinterpret_cast<const __half2*>(&packed[(c + u) / 2]);
+                  v0 = fmaf(p.beta, __low2float(a), v0);
+                  v1 = fmaf(p.beta, __high2float(a), v1);
+                }
+                // on the diagonal (i == j)
+                if (c + u == on_diag) v0 += p.diag;
+                if (c + u + 1 == on_diag) v1 += p.diag;
               }
               packed[(c + u) / 2] = pack_out(v0, v1, f16);
             }

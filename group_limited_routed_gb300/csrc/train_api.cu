@@ -101,7 +101,6 @@ struct Operand {
     p.src = static_cast<const uint16_t*>(base);
     p.sz = zs;
     p.sr = ld;
-    p.sc = 1;
     p.zs = z;
     p.rows = outer;
     p.cols = static_cast<int32_t>(inner);
@@ -219,7 +218,7 @@ constexpr float kScaleX = 1024.f, kScaleGram = 1024.f, kScalePoly = 256.f;
 
 struct OrthoLayout {
   int64_t m, ld, ldm;   // smaller extent, row strides of X and of the m x m products
-  size_t amax, sumsq, alpha_gram, alpha_step, x0, x1, gram, poly, total;
+  size_t amax, sum_exp, sumsq, alpha_gram, alpha_step, x0, x1, gram, poly, total;
 };
 
 bool ortho_layout(int32_t batch, int32_t rows, int32_t cols, int32_t dtype, OrthoLayout* L) {
@@ -238,6 +237,7 @@ bool ortho_layout(int32_t batch, int32_t rows, int32_t cols, int32_t dtype, Orth
   const size_t x = static_cast<size_t>(batch) * rows * L->ld * 2;
   const size_t mm = static_cast<size_t>(batch) * L->m * L->ldm * 2;
   L->amax = take(static_cast<size_t>(batch) * beam::kNormBlocks * 4);
+  L->sum_exp = take(static_cast<size_t>(batch) * beam::kNormBlocks * 4);
   L->sumsq = take(static_cast<size_t>(batch) * beam::kNormBlocks * 4);
   L->alpha_gram = take(static_cast<size_t>(batch) * 4);
   L->alpha_step = take(static_cast<size_t>(batch) * 4);
@@ -430,8 +430,9 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
   n.cols = d->cols;
   n.type = d->dtype;
   n.blocks = static_cast<int32_t>(
-      std::min<int64_t>(beam::kNormBlocks, (R * C + 2047) / 2048));
+      std::min<int64_t>(beam::kNormBlocks, (R * ((C + 7) / 8) + 255) / 256));
   n.amax = at<uint32_t>(workspace, L.amax);
+  n.sum_exp = at<int32_t>(workspace, L.sum_exp);
   n.sumsq = at<float>(workspace, L.sumsq);
   n.hi = x[0];
   n.lo = split ? x[0] + batch * R * L.ld : nullptr;

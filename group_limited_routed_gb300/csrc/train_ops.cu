@@ -36,22 +36,47 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 
 // ------------------------------------------------------------ aligned copies
-// One thread per 8 elements of the destination: the store is one 16-byte
-// word; the source is read element by element, as its alignment allows no
-// more.  Memory bound (2 bytes read, 2 written per element).
+// A warp takes a row, a lane 8 elements of the destination at a time: the
+// store is one 16-byte word.  The source row starts anywhere (element
+// aligned), so it is read in 4-byte words from the 4-byte boundary at or
+// before it -- five words hold the eight elements -- and shifted by one
+// element where it starts on an odd one.  Memory bound: 2 bytes read, 2
+// written per element.
 __global__ void __launch_bounds__(256) pack_kernel(const PackArgs p) {
-  const int64_t words = p.zs * p.rows * (p.ld / 8);
-  for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < words;
-       at += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t row = at / (p.ld / 8);
-    const int c = static_cast<int>(at - row * (p.ld / 8)) * 8;
+  const int64_t rows = p.zs * p.rows;
+  const int lane = threadIdx.x & 31;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < rows;
+       row += static_cast<int64_t>(gridDim.x) * 8) {
     const int64_t z = row / p.rows;
     const uint16_t* src = p.src + z * p.sz + (row - z * p.rows) * p.sr;
-    uint32_t v[8];
+    const bool odd = (reinterpret_cast<uintptr_t>(src) & 2u) != 0;
+    // words[k] holds elements 2k - odd and 2k + 1 - odd of the row
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(src - (odd ? 1 : 0));
+    const int whole = (p.cols + (odd ? 1 : 0)) / 2;  // words wholly at or before the row's end
+    uint16_t* dst = p.dst + row * p.ld;
+    for (int c = lane * 8; c < p.ld; c += 256) {
+      uint32_t w[5];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = c + u < p.cols ? src[(c + u) * p.sc] : 0u;
-    *reinterpret_cast<uint4*>(p.dst + row * p.ld + c) =
-        make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+      for (int k = 0; k < 5; ++k) {
+        const int at = c / 2 + k;
+        // the first word of an odd row begins one element before it, the
+        // last word may end one after it: those are read by the element
+        w[k] = 0u;
+        if (at < whole && !(odd && at == 0)) {
+          w[k] = words[at];
+        } else {
+          const int e = 2 * at - (odd ? 1 : 0);
+          if (e >= 0 && e < p.cols) w[k] = src[e];
+          if (e + 1 >= 0 && e + 1 < p.cols) w[k] |= static_cast<uint32_t>(src[e + 1]) << 16;
+        }
+      }
+      uint4 v;
+      v.x = odd ? __funnelshift_r(w[0], w[1], 16) : w[0];
+      v.y = odd ? __funnelshift_r(w[1], w[2], 16) : w[1];
+      v.z = odd ? __funnelshift_r(w[2], w[3], 16) : w[2];
+      v.w = odd ? __funnelshift_r(w[3], w[4], 16) : w[3];
+      *reinterpret_cast<uint4*>(dst + c) = v;
+    }
   }
 }
 
@@ -225,86 +250,168 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* s) {
   return m;
 }
 
-template <int TYPE>
+// Eight consecutive elements of a row (those at or past its end are 0).
+template <int TYPE, bool VEC>
+__device__ __forceinline__ void load_row8(const NormArgs& p, int64_t base, int c, float (&v)[8]) {
+  if constexpr (VEC && TYPE == kF32) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p.src) + base + c);
+    const float4 a = q[0];
+    const float4 b = c + 4 < p.cols ? q[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else if constexpr (VEC) {
+    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.src) + base + c);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = from16<TYPE == kF16>(w[k] & 0xffffu);
+      v[2 * k + 1] = from16<TYPE == kF16>(w[k] >> 16);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      v[k] = c + k < p.cols ? element<TYPE>(p.src, base + (c + k) * p.sc) : 0.f;
+  }
+}
+
+// Sum of squares over any range of magnitudes: sum * 2^(2 exp), where exp is
+// the exponent of the largest element met so far (its bits' exponent field).
+struct ScaledSum {
+  int exp = 0;
+  float sum = 0.f;
+
+  static __device__ __forceinline__ float pow2(int k) {  // 2^k, 0 below the normal range
+    return k < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+  }
+  __device__ __forceinline__ void add(int e, float s) {
+    if (e > exp) {
+      sum *= pow2(max(2 * (exp - e), -200));
+      exp = e;
+    }
+    sum = fmaf(s, pow2(max(2 * (e - exp), -200)), sum);
+  }
+};
+
+// First pass: each block's largest magnitude and sum of squares, in one read.
+template <int TYPE, bool VEC>
 __global__ void __launch_bounds__(256) amax_kernel(const NormArgs p) {
   __shared__ uint32_t s[8];
+  __shared__ int se[8];
+  __shared__ float sf[8];
   const int z = blockIdx.y;
-  const int64_t n = static_cast<int64_t>(p.rows) * p.cols;
+  const uint32_t per_row = (p.cols + 7) / 8;
+  const uint32_t n = static_cast<uint32_t>(p.rows) * per_row;  // below 2^29
   uint32_t m = 0;
-  for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < n;
-       at += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t r = at / p.cols;
-    const float v = element<TYPE>(p.src, z * p.sz + r * p.sr + (at - r * p.cols) * p.sc);
-    // as integers, so that a NaN is larger than every number
-    m = max(m, __float_as_uint(v) & 0x7fffffffu);
+  ScaledSum acc;
+  for (uint32_t at = blockIdx.x * 256 + threadIdx.x; at < n; at += gridDim.x * 256) {
+    const uint32_t r = at / per_row;
+    float v[8];
+    load_row8<TYPE, VEC>(p, z * p.sz + r * p.sr, static_cast<int>(at - r * per_row) * 8, v);
+    uint32_t top = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      // as integers, so that a NaN is larger than every number
+      top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
+    m = max(m, top);
+    if (top == 0 || top >= 0x7f800000u) continue;  // not finite: the maximum tells
+    // squares of the elements times 2^(127 - e), which brings the largest
+    // near 1 (subnormals count from the smallest normal exponent; the largest
+    // exponent's power of two would be subnormal)
+    const int e = min(max(static_cast<int>(top >> 23), 1), 253);
+    const float k1 = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+    float sq = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sq = fmaf(v[k] * k1, v[k] * k1, sq);
+    acc.add(e, sq);
   }
   m = block_max(m, s);
-  if (threadIdx.x == 0) p.amax[z * kNormBlocks + blockIdx.x] = m;
-}
-
-template <int TYPE>
-__global__ void __launch_bounds__(256) scale_kernel(const NormArgs p) {
-  __shared__ uint32_t s[8];
-  __shared__ float f[8];
-  const int z = blockIdx.y;
-  const float k = range_scale(block_max(
-      threadIdx.x < p.blocks ? p.amax[z * kNormBlocks + threadIdx.x] : 0u, s));
-  const int64_t n = static_cast<int64_t>(p.rows) * p.cols;
-  float sum = 0.f;
-  for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < n;
-       at += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t r = at / p.cols;
-    const int64_t c = at - r * p.cols;
-    const float v = element<TYPE>(p.src, z * p.sz + r * p.sr + c * p.sc) * k;
-    const __half h = __float2half_rn(v);
-    const int64_t dst = (static_cast<int64_t>(z) * p.rows + r) * p.ld + c;
-    p.hi[dst] = __half_as_ushort(h);
-    if (p.lo) p.lo[dst] = __half_as_ushort(__float2half_rn(v - __half2float(h)));
-    sum = fmaf(v, v, sum);
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-  if (threadIdx.x % 32 == 0) f[threadIdx.x / 32] = sum;
+  for (int o = 16; o > 0; o >>= 1) {
+    const int e = __shfl_xor_sync(kAll, acc.exp, o);
+    const float f = __shfl_xor_sync(kAll, acc.sum, o);
+    acc.add(e, f);
+  }
+  if (threadIdx.x % 32 == 0) {
+    se[threadIdx.x / 32] = acc.exp;
+    sf[threadIdx.x / 32] = acc.sum;
+  }
   __syncthreads();
   if (threadIdx.x == 0) {
-    sum = 0.f;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) sum += f[q];
-    p.sumsq[z * kNormBlocks + blockIdx.x] = sum;
+    for (int k = 1; k < 8; ++k) acc.add(se[k], sf[k]);
+    p.amax[z * kNormBlocks + blockIdx.x] = m;
+    p.sum_exp[z * kNormBlocks + blockIdx.x] = acc.exp;
+    p.sumsq[z * kNormBlocks + blockIdx.x] = acc.sum;
   }
 }
 
-// Per matrix: X = s * (scaled copy) with s = 1 / (norm + eps), the norm and
+// Second pass: the scaled F16 copy.  One block of each matrix also turns the
+// sums into the factors of X = s * copy, s = 1 / (norm + eps), the norm and
 // eps both in the copy's scale.
-__global__ void __launch_bounds__(256) norm_kernel(const NormArgs p) {
+template <int TYPE, bool VEC>
+__global__ void __launch_bounds__(256) scale_kernel(const NormArgs p) {
   __shared__ uint32_t s[8];
-  const int z = blockIdx.x;
-  const float k = range_scale(block_max(
-      threadIdx.x < p.blocks ? p.amax[z * kNormBlocks + threadIdx.x] : 0u, s));
-  if (threadIdx.x == 0) {
-    float sum = 0.f;
-    for (int q = 0; q < p.blocks; ++q) sum += p.sumsq[z * kNormBlocks + q];
-    const float inv = 1.f / (sqrtf(sum) + p.eps * k);
+  const int z = blockIdx.y;
+  const uint32_t amax = block_max(
+      threadIdx.x < p.blocks ? p.amax[z * kNormBlocks + threadIdx.x] : 0u, s);
+  const float k = range_scale(amax);
+  const uint32_t per_row = (p.cols + 7) / 8;
+  const uint32_t n = static_cast<uint32_t>(p.rows) * per_row;
+  for (uint32_t at = blockIdx.x * 256 + threadIdx.x; at < n; at += gridDim.x * 256) {
+    const uint32_t r = at / per_row;
+    const int c = static_cast<int>(at - r * per_row) * 8;
+    float v[8];
+    load_row8<TYPE, VEC>(p, z * p.sz + r * p.sr, c, v);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float a = v[2 * q] * k, b = v[2 * q + 1] * k;
+      hi[q] = pack16<true>(a, b);
+      lo[q] = pack16<true>(a - from16<true>(hi[q] & 0xffffu), b - from16<true>(hi[q] >> 16));
+    }
+    // rows of the copy are padded: whole words stay inside
+    const int64_t dst = (static_cast<int64_t>(z) * p.rows + r) * p.ld + c;
+    *reinterpret_cast<uint4*>(p.hi + dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if (p.lo) *reinterpret_cast<uint4*>(p.lo + dst) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    ScaledSum acc;
+    for (int q = 0; q < p.blocks; ++q)
+      acc.add(p.sum_exp[z * kNormBlocks + q], p.sumsq[z * kNormBlocks + q]);
+    // the sum is in units of 2^(2 (exp - 127)); the copy's scale is k
+    const float norm = sqrtf(acc.sum) * (__uint_as_float(static_cast<uint32_t>(acc.exp) << 23) * k);
+    const float inv = amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
+                                          : 1.f / (norm + p.eps * k);
     // an all-zero matrix with eps = 0 stays 0 / 0
     p.alpha_gram[z] = p.scale_gram * inv * inv;
     p.alpha_step[z] = p.scale_step * inv;
   }
 }
 
-template <int TYPE>
+template <int TYPE, bool VEC>
 cudaError_t norm_impl(const NormArgs& p, cudaStream_t s) {
   const dim3 grid(p.blocks, p.batch);
-  amax_kernel<TYPE><<<grid, 256, 0, s>>>(p);
-  scale_kernel<TYPE><<<grid, 256, 0, s>>>(p);
-  norm_kernel<<<p.batch, 256, 0, s>>>(p);
+  amax_kernel<TYPE, VEC><<<grid, 256, 0, s>>>(p);
+  scale_kernel<TYPE, VEC><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError();
+}
+
+// Rows of 16-byte words: contiguous, aligned, and no word crosses a row's end
+// (an odd number of FP32 quarters is handled by the loader).
+bool norm_aligned(const NormArgs& p) {
+  const int64_t word = p.type == kF32 ? 4 : 8;
+  return p.sc == 1 && (reinterpret_cast<uintptr_t>(p.src) & 15) == 0 && p.cols % word == 0 &&
+         p.sr % word == 0 && p.sz % word == 0;
+}
+
+template <int TYPE>
+cudaError_t norm_typed(const NormArgs& p, cudaStream_t s) {
+  return norm_aligned(p) ? norm_impl<TYPE, true>(p, s) : norm_impl<TYPE, false>(p, s);
 }
 
 }  // namespace
 
 void launch_pack(const PackArgs& p, cudaStream_t s) {
-  const int64_t words = p.zs * p.rows * (p.ld / 8);
-  const int64_t blocks = std::min<int64_t>((words + 255) / 256, 1 << 20);
+  const int64_t blocks = std::min<int64_t>((p.zs * p.rows + 7) / 8, 1 << 20);
   if (blocks > 0) pack_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(p);
 }
 
@@ -343,9 +450,9 @@ void launch_gate_grad(const GateArgs& p, int num_sms, cudaStream_t s) {
 
 cudaError_t launch_norm(const NormArgs& p, cudaStream_t s) {
   switch (p.type) {
-    case kBf16: return norm_impl<kBf16>(p, s);
-    case kF16: return norm_impl<kF16>(p, s);
-    case kF32: return norm_impl<kF32>(p, s);
+    case kBf16: return norm_typed<kBf16>(p, s);
+    case kF16: return norm_typed<kF16>(p, s);
+    case kF32: return norm_typed<kF32>(p, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -8,12 +8,12 @@
 namespace beam {
 
 // ------------------------------------------------------------ aligned copies
-// 16-bit elements src[z * sz + r * sr + c * sc], r < rows, c < cols, to
+// 16-bit elements src[z * sz + r * sr + c], r < rows, c < cols, to
 // dst[(z * rows + r) * ld + c] (ld a multiple of 8, at least cols; the
 // padding is zeroed).
 struct PackArgs {
   const uint16_t* src;
-  int64_t sz, sr, sc;
+  int64_t sz, sr;
   int64_t zs, rows;
   int32_t cols, ld;
   uint16_t* dst;
@@ -39,7 +39,7 @@ void launch_gate(const GateArgs& p, int num_sms, cudaStream_t s);
 void launch_gate_grad(const GateArgs& p, int num_sms, cudaStream_t s);
 
 // ------------------------------------------------------ orthogonalised update
-constexpr int kNormBlocks = 64;  // partial sums per matrix, at most
+constexpr int kNormBlocks = 256;  // partial sums per matrix, at most
 
 struct NormArgs {
   const void* src;         // kBf16, kF16 or kF32, src[z * sz + r * sr + c * sc]
@@ -48,7 +48,8 @@ struct NormArgs {
   int32_t type;
   int32_t blocks;          // partial sums per matrix (<= kNormBlocks)
   uint32_t* amax;          // [batch, kNormBlocks] bits of the largest magnitudes
-  float* sumsq;            // [batch, kNormBlocks]
+  int32_t* sum_exp;        // [batch, kNormBlocks] sums of squares: exponents ...
+  float* sumsq;            // [batch, kNormBlocks] ... and values
   uint16_t* hi;            // F16 [batch, rows, ld]: the update times a power of two
   uint16_t* lo;            // F16, what hi leaves of a 32-bit update; or nullptr
   int64_t ld;
@@ -56,7 +57,7 @@ struct NormArgs {
   float* alpha_step;       // [batch] scale_step / norm
   float scale_gram, scale_step, eps;
 };
-// Three launches: magnitudes, scaled F16 copy with its sum of squares, norms.
+// Two launches: magnitudes with sums of squares, the scaled F16 copy with the norms.
 cudaError_t launch_norm(const NormArgs& p, cudaStream_t s);
 
 }  // namespace beam
