@@ -24,11 +24,11 @@ int resident_clusters_once(const cudaLaunchConfig_t& cfg) {
   return cached[dev];
 }
 
-template <int NT, bool A_MN, bool B_MN, int KIND, bool WIDE>
+template <int NT, bool A_MN, bool B_MN, int KIND, bool WIDE, bool DUAL = false>
 cudaError_t launch_impl(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out,
                         const ProductArgs& p, int64_t max_tiles, bool dependent, cudaStream_t s) {
-  using C = ProductCfg<NT, KIND, WIDE>;
-  constexpr auto kern = pair_product_kernel<NT, A_MN, B_MN, KIND, WIDE>;
+  using C = ProductCfg<NT, KIND, WIDE, DUAL>;
+  constexpr auto kern = pair_product_kernel<NT, A_MN, B_MN, KIND, WIDE, DUAL>;
   const cudaError_t err = smem_limit_once<kern>(static_cast<int>(C::SMEM_BYTES));
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr[2];
@@ -86,7 +86,7 @@ cudaError_t launch_pair_product(int kind, int nt, bool a_mn, bool b_mn, const CU
   if (kind == kProductGroups && a_mn && b_mn && nt == 256)
     return p.out_type == kF32
                ? launch_impl<256, true, true, kProductGroups, true>(a, b, out, p, tiles, dependent, s)
-               : launch_impl<256, true, true, kProductGroups, false>(a, b, out, p, tiles, dependent, s);
+               : launch_impl<256, true, true, kProductGroups, false, true>(a, b, out, p, tiles, dependent, s);
   if (kind == kProductDense && p.out_type != kF32) {
     if (!a_mn && !b_mn && nt == 256)
       return launch_impl<256, false, false, kProductDense, false>(a, b, out, p, tiles, dependent, s);

@@ -61,7 +61,7 @@ constexpr uint32_t kPABytes = 128 * 128;       // one CTA's A per stage
 constexpr int kPEpiWarps = 16;
 constexpr int kPThreads = 96 + 32 * kPEpiWarps;
 constexpr uint32_t kPRing = 216 * 1024;
-constexpr int kWideBlocks = 4;                 // k blocks per accumulator chain, FP32 outputs
+constexpr int kWideBlocks = 8;                 // k blocks per accumulator chain, FP32 outputs
 constexpr uint64_t kPPeerDrainNs = 1000000ull; // see the producer's teardown
 constexpr uint32_t kAtom = 64 * 128;           // MN-major atom: 64 k rows of 64 elements
 
@@ -69,16 +69,19 @@ constexpr uint32_t kAtom = 64 * 128;           // MN-major atom: 64 k rows of 64
 // FP32 columns, or 32 rows of 16-bit ones) and one bulk copy writes them.
 constexpr uint32_t kStaging = kPEpiWarps * 2048;
 
-template <int NT, int KIND, bool WIDE>
+template <int NT, int KIND, bool WIDE, bool DUAL>
 struct ProductCfg {
   static constexpr bool STAGED = KIND == kProductGroups || WIDE;
-  static constexpr uint32_t B_BYTES = NT / 2 * 128;
-  static constexpr uint32_t STAGE = kPABytes + B_BYTES;
-  static constexpr int S_RAW = static_cast<int>((kPRing - (STAGED ? kStaging : 0)) / STAGE);
+  static constexpr uint32_t B_BYTES = NT / 2 * 128;  // one block of rows
+  static constexpr uint32_t STAGE = kPABytes + (DUAL ? 2 : 1) * B_BYTES;
+  static constexpr int S_RAW = static_cast<int>((kPRing + (DUAL ? 8192 : 0) - (STAGED ? kStaging : 0)) / STAGE);
   static constexpr int S = S_RAW > 12 ? 12 : S_RAW;
   static constexpr uint32_t TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
   static constexpr uint32_t NUM_BARS = 4 * S + 5;
-  static constexpr uint32_t MISC = 16 + 4 * (2 * (kProductMaxGroups + 1) + 2);
+  // group boundaries and first tiles in shared memory (kProductGroups reads
+  // the boundaries where they are)
+  static constexpr uint32_t MISC =
+      16 + (KIND == kProductRows ? 4 * (2 * (kProductMaxGroups + 1) + 2) : 0);
   static constexpr uint32_t STAGING = S * STAGE;  // offset
   static constexpr uint32_t BARS = STAGING + (STAGED ? kStaging : 0);
   static constexpr uint32_t SMEM_BYTES = 1024 + BARS + NUM_BARS * 8 + MISC;
@@ -127,8 +130,32 @@ __device__ __forceinline__ void arrive_relaxed_cluster(uint32_t cluster_bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
 }
-__device__ __forceinline__ void fence_acquire_cluster() {
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+// Waiter::wait for a barrier whose arrivals release at cluster scope.
+__device__ __forceinline__ bool wait_cluster(const Waiter& w, uint32_t bar, uint32_t parity) {
+  auto done = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (done()) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  for (uint32_t n = 1;; ++n) {
+    if (done()) return true;
+    if ((n & 63u) == 0) {
+      if (*w.abort_flag) return false;
+      if (ptx::globaltimer() - t0 > w.limit_ns) {
+        *w.abort_flag = 1;
+        latch_status(w.status, kStatusTimeout);
+        return false;
+      }
+    }
+  }
 }
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -140,6 +167,7 @@ struct ProductTile {
   int j0;        // first row (kProductRows: of all rows)
   int nvalid;    // rows of the tile
   int n_mma;     // rounded up to the MMA's step
+  int nvalid2;   // rows of a second block behind the first (0: none)
   int k_blocks;  // 64-wide k blocks
   int k0;        // kProductGroups: first row of the group
   int k_count;   // kProductGroups: rows of the group
@@ -155,7 +183,7 @@ __device__ __forceinline__ int small_div(int a, int b) {
 // One role's walk over this pair's tiles: tile, tile + num_pairs, ...  With a
 // few k blocks per tile (kProductGroups) finding the next tile must cost less
 // than a block, so positions advance by addition where they can.
-template <int NT, int KIND>
+template <int NT, int KIND, bool DUAL>
 struct ProductWalk {
   const ProductArgs& p;
   const int32_t* s_off;
@@ -164,12 +192,15 @@ struct ProductWalk {
   int mt, nt;       // tiles along i and j
   int group = 0;    // kProductRows: group of the last tile
   int z = 0, i = 0, j = 0, dz = 0, di = 0, dj = 0;
+  int known_z = -1, k_first = 0, k_rows = 0;   // kProductGroups: that group's rows
+
+  static constexpr int kSpan = DUAL ? 2 * NT : NT;  // rows of a tile
 
   __device__ ProductWalk(const ProductArgs& args, const int32_t* off, const int32_t* start,
                          int first, int stride, int tiles)
       : p(args), s_off(off), s_start(start), tile(first), step(stride), total(tiles) {
     mt = (p.M + kProductTileM - 1) / kProductTileM;
-    nt = (p.N + NT - 1) / NT;
+    nt = (p.N + kSpan - 1) / kSpan;
     if constexpr (KIND == kProductGroups) {
       // i fastest: neighbouring pairs write neighbouring pieces of the same rows
       z = first / (mt * nt);
@@ -225,15 +256,23 @@ struct ProductWalk {
       t.i0 = block_i * kProductTileM;
       t.j0 = s_off[group] + b * per;
       t.nvalid = min(per, cnt - b * per);
+      t.nvalid2 = 0;
       t.k_blocks = p.k_blocks;
       t.k0 = t.k_count = 0;
     } else if constexpr (KIND == kProductGroups) {
       t.z = z;
       t.i0 = i * kProductTileM;
-      t.j0 = j * NT;
+      t.j0 = j * kSpan;
       t.nvalid = min(NT, p.N - t.j0);
-      t.k0 = s_off[z];
-      t.k_count = s_off[z + 1] - t.k0;
+      t.nvalid2 = DUAL ? max(0, min(NT, p.N - t.j0 - NT)) : 0;
+      if (z != known_z) {
+        // made safe to index with: inside the rows, not backwards
+        known_z = z;
+        k_first = min(max(p.offsets[z], 0), p.rows);
+        k_rows = max(0, min(p.offsets[z + 1], p.rows) - k_first);
+      }
+      t.k0 = k_first;
+      t.k_count = k_rows;
       t.k_blocks = (t.k_count + kPBK - 1) / kPBK;
     } else {
       int bi, bj;
@@ -258,6 +297,7 @@ struct ProductWalk {
       t.i0 = bi * kProductTileM;
       t.j0 = bj * NT;
       t.nvalid = min(NT, p.N - t.j0);
+      t.nvalid2 = 0;
       t.k_blocks = p.k_blocks;
       t.k0 = t.k_count = 0;
     }
@@ -269,10 +309,11 @@ struct ProductWalk {
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[16]) { ptx::tmem_ld16(at, r); }
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[32]) { ptx::tmem_ld32(at, r); }
 
-template <int NT, int KIND>
+template <int NT, int KIND, bool DUAL>
 __device__ __forceinline__ int product_tiles(const ProductArgs& p, const int32_t* s_start) {
+  constexpr int kSpan = DUAL ? 2 * NT : NT;
   const int mt = (p.M + kProductTileM - 1) / kProductTileM;
-  const int nt = (p.N + NT - 1) / NT;
+  const int nt = (p.N + kSpan - 1) / kSpan;
   if constexpr (KIND == kProductRows) {
     return s_start[p.groups];
   } else if (KIND == kProductDense && p.symmetric) {
@@ -327,12 +368,13 @@ __device__ __forceinline__ uint32_t swap_pair(uint32_t mine, int lane) {
   return (lane & 1) ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
 }
 
-template <int NT, bool A_MN, bool B_MN, int KIND, bool WIDE>
+template <int NT, bool A_MN, bool B_MN, int KIND, bool WIDE, bool DUAL>
 __global__ void __launch_bounds__(kPThreads, 1)
     pair_product_kernel(const __grid_constant__ CUtensorMap tm_a,
                         const __grid_constant__ CUtensorMap tm_b,
                         const __grid_constant__ CUtensorMap tm_out, const ProductArgs p) {
-  using C = ProductCfg<NT, KIND, WIDE>;
+  using C = ProductCfg<NT, KIND, WIDE, DUAL>;
+  using Walk = ProductWalk<NT, KIND, DUAL>;
   constexpr bool RAGGED_K = KIND == kProductGroups;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = ptx::smem_addr(smem_raw);
@@ -388,7 +430,16 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  if constexpr (KIND != kProductDense) {
+  if constexpr (KIND == kProductGroups) {
+    // boundaries that decrease or leave the rows are reported (the walk
+    // clamps them)
+    for (int e = threadIdx.x; e <= p.groups; e += kPThreads) {
+      const int v = p.offsets[e];
+      if (v < 0 || v > p.rows || (e > 0 && p.offsets[e - 1] > v))
+        latch_status(p.status, kStatusDeviceCheck);
+    }
+  }
+  if constexpr (KIND == kProductRows) {
     // group boundaries, made safe to index with: monotonic and inside the
     // rows.  What had to be changed is reported, not followed.
     for (int e = threadIdx.x; e <= p.groups; e += kPThreads) {
@@ -417,23 +468,21 @@ __global__ void __launch_bounds__(kPThreads, 1)
         top = __shfl_sync(0xffffffffu, v, 31);
       }
       __syncwarp();
-      if constexpr (KIND == kProductRows) {
-        const int mt = (p.M + kProductTileM - 1) / kProductTileM;
-        for (int base = 0; base < p.groups; base += 32) {
-          const int e = base + lane;
-          const int cnt = e < p.groups ? s_off[e + 1] - s_off[e] : 0;
-          const int v = mt * ((cnt + NT - 1) / NT);
-          int incl = v;
+      const int mt = (p.M + kProductTileM - 1) / kProductTileM;
+      for (int base = 0; base < p.groups; base += 32) {
+        const int e = base + lane;
+        const int cnt = e < p.groups ? s_off[e + 1] - s_off[e] : 0;
+        const int v = mt * ((cnt + NT - 1) / NT);
+        int incl = v;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int n = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += n;
-          }
-          if (e < p.groups) s_start[e] = running + incl - v;
-          running += __shfl_sync(0xffffffffu, incl, 31);
+        for (int o = 1; o < 32; o <<= 1) {
+          const int n = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += n;
         }
-        if (lane == 0) s_start[p.groups] = running;
+        if (e < p.groups) s_start[e] = running + incl - v;
+        running += __shfl_sync(0xffffffffu, incl, 31);
       }
+      if (lane == 0) s_start[p.groups] = running;
     }
   }
   ptx::tc_fence_before();
@@ -441,7 +490,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int num_tiles = product_tiles<NT, KIND>(p, s_start);
+  const int num_tiles = product_tiles<NT, KIND, DUAL>(p, s_start);
   const Waiter W{abort_flag, p.status, p.wait_limit_ns};
 
   if (warp == 0) {
@@ -455,7 +504,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (ProductWalk<NT, KIND> walk(p, s_off, s_start, pair, num_pairs, num_tiles);
+      for (Walk walk(p, s_off, s_start, pair, num_pairs, num_tiles);
            ok && !walk.done(); walk.next()) {
         const ProductTile t = walk.get();
         const int i = t.i0 + static_cast<int>(rank) * 128;
@@ -463,7 +512,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
         // k-contiguous B comes in boxes of BOX rows, as many as the tile has
         constexpr int BOX = NT / 2 < kProductBoxRows ? NT / 2 : kProductBoxRows;
         const int boxes = (t.n_mma / 2 + BOX - 1) / BOX;
-        const uint32_t bytes = kPABytes + (B_MN ? C::B_BYTES : boxes * BOX * 128u);
+        const int n2 = (t.nvalid2 + 15) & ~15;
+        const int j2 = t.j0 + t.nvalid + static_cast<int>(rank) * (n2 / 2);
+        const uint32_t bytes =
+            kPABytes + (B_MN ? (n2 ? 2 : 1) * C::B_BYTES : boxes * BOX * 128u);
         for (int kb = 0; kb < t.k_blocks; ++kb) {
           if (!W.wait(empty(stage), phase ^ 1u)) {
             ok = false;
@@ -507,6 +559,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
               for (int c = 0; c < NT / 128; ++c)
                 tma_load_3d_pair(sb + c * kAtom, &tm_b, bar, j + c * 64, k, zb, pol);
+              if (DUAL && n2) {
+#pragma unroll
+                for (int c = 0; c < NT / 128; ++c)
+                  tma_load_3d_pair(sb + C::B_BYTES + c * kAtom, &tm_b, bar, j2 + c * 64, k, zb,
+                                   pol);
+              }
             } else {
 #pragma unroll
               for (int c = 0; c < NT / 2 / BOX; ++c)
@@ -562,7 +620,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       uint32_t acc_phase = 0;
       uint32_t cleared_parity = 0;  // bit s: phase of cleared(s)
       bool ok = true;
-      ProductWalk<NT, KIND> walk(p, s_off, s_start, pair, num_pairs, num_tiles);
+      Walk walk(p, s_off, s_start, pair, num_pairs, num_tiles);
       ProductTile ahead;
       if (!walk.done()) ahead = walk.get();
       while (ok && !walk.done()) {
@@ -573,6 +631,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           continue;
         }
         const uint32_t idesc = idesc_m | (static_cast<uint32_t>(t.n_mma >> 3) << 17);
+        const uint32_t idesc2 =
+            idesc_m | (static_cast<uint32_t>(((t.nvalid2 + 15) & ~15) >> 3) << 17);
         uint32_t d0 = 0;
         for (int kb = 0; kb < t.k_blocks; ++kb) {
           const bool fresh = kb == 0 || (WIDE && kb % kWideBlocks == 0);
@@ -582,6 +642,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
               break;
             }
             d0 = tmem_base + acc * NT;
+            // a second block takes the other buffer, one use later
+            if (DUAL && t.nvalid2 > 0 &&
+                !W.wait(tempty(acc ^ 1), (acc == 1 ? acc_phase ^ 1u : acc_phase) ^ 1u)) {
+              ok = false;
+              break;
+            }
           }
           if (!W.wait(full(stage), phase)) {
             ok = false;
@@ -589,13 +655,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           const bool ragged = RAGGED_K && (kb + 1) * kPBK > t.k_count;
           if (ragged) {
-            if (!W.wait(cleared(stage), cleared_parity >> stage & 1u)) {
+            // also written by the peer's threads: acquired at cluster scope
+            if (!wait_cluster(W, cleared(stage), cleared_parity >> stage & 1u)) {
               ok = false;
               break;
             }
             cleared_parity ^= 1u << stage;
-            // the block was also written by the peer's threads
-            fence_acquire_cluster();
           }
           ptx::tc_fence_after();
           const bool last = kb + 1 == t.k_blocks || (WIDE && (kb + 1) % kWideBlocks == 0);
@@ -608,8 +673,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
               if (!RAGGED_K || kk < steps)
                 ptx::mma_bf16_pair(d0, ad + kk * A_STEP, bd + kk * B_STEP, idesc,
                                    (fresh && kk == 0) ? 0u : 1u);
-            ptx::mma_commit_pair_both(empty(stage));
             if (last) ptx::mma_commit_pair_both(tfull(acc));
+            if (DUAL && t.nvalid2 > 0) {
+              // the same A against the second block
+              const uint32_t d1 = tmem_base + (acc ^ 1) * NT;
+#pragma unroll
+              for (int kk = 0; kk < kPBK / 16; ++kk)
+                if (!RAGGED_K || kk < steps)
+                  ptx::mma_bf16_pair(d1, ad + kk * A_STEP, bd + (C::B_BYTES >> 4) + kk * B_STEP,
+                                     idesc2, (fresh && kk == 0) ? 0u : 1u);
+              if (last) ptx::mma_commit_pair_both(tfull(acc ^ 1));
+            }
+            ptx::mma_commit_pair_both(empty(stage));
           }
           __syncwarp();
           if (kb == 0) {
@@ -622,8 +697,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
             phase ^= 1u;
           }
           if (last) {
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1u;
+            if (DUAL && t.nvalid2 > 0) {
+              acc_phase ^= 1u;  // both buffers used: acc comes round to itself
+            } else {
+              acc ^= 1;
+              if (acc == 0) acc_phase ^= 1u;
+            }
           }
         }
       }
@@ -638,7 +717,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if constexpr (RAGGED_K) {
       int stage = 0;
       uint32_t parity = 0;  // bit s: phase of landed(s)
-      for (ProductWalk<NT, KIND> walk(p, s_off, s_start, pair, num_pairs, num_tiles);
+      for (Walk walk(p, s_off, s_start, pair, num_pairs, num_tiles);
            !walk.done(); walk.next()) {
         const ProductTile t = walk.get();
         stage = (stage + t.k_blocks) % C::S;
@@ -650,7 +729,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int last = (tail + 15) & ~15;
         const uint32_t base = ring + s * C::STAGE;
         // rows [tail, last) of every 64-element atom of both operands
-        constexpr int ATOMS = 2 + NT / 128;
+        constexpr int ATOMS = 2 + (DUAL ? 2 : 1) * (NT / 128);
         const int n = (last - tail) * ATOMS * 8;
         for (int q = lane; q < n; q += 32) {
           const int row = tail + q / (ATOMS * 8);
@@ -696,12 +775,46 @@ __global__ void __launch_bounds__(kPThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     bool ok = true;
-    for (ProductWalk<NT, KIND> walk(p, s_off, s_start, pair, num_pairs, num_tiles);
+    for (Walk walk(p, s_off, s_start, pair, num_pairs, num_tiles);
          ok && !walk.done(); walk.next()) {
-      const ProductTile t = walk.get();
+      ProductTile t = walk.get();
       const int i = t.i0 + static_cast<int>(rank) * 128 + q * 32 + lane;
       const int64_t zbase = KIND == kProductRows ? 0 : static_cast<int64_t>(t.z) * p.z_out;
-      const int ncols = min(t.nvalid - col_begin, COLS);  // <= 0: nothing for this warp
+      int ncols = min(t.nvalid - col_begin, COLS);  // <= 0: nothing for this warp
+      if (WIDE && KIND == kProductGroups && p.staged && t.k_blocks > 0 &&
+          t.k_blocks <= kWideBlocks) {
+        // one chain: straight from TMEM to the staged pieces
+        if (!W.wait(tfull(acc), acc_phase)) break;
+        ptx::tc_fence_after();
+        const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NT + col_begin;
+#pragma unroll 1
+        for (int c = 0; c < COLS; c += 16) {
+          if (c >= ncols) break;
+          uint32_t r[16];
+          ptx::tmem_ld16(tq + c, r);
+          if (lane == 0) tma_store_read_done();
+          ptx::tmem_wait_ld();
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < 16; ++u)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage_at + u * 128 + lane * 4), "r"(r[u])
+                         : "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && i < p.M) {
+            if (p.accumulate)
+              tma_store_3d<true>(&tm_out, stage_at, i, t.j0 + col_begin + c, t.z);
+            else
+              tma_store_3d<false>(&tm_out, stage_at, i, t.j0 + col_begin + c, t.z);
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_relaxed_cluster(ptx::map_to_rank(tempty(acc), 0));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+        continue;
+      }
       if constexpr (WIDE) {
         float sum[COLS];
 #pragma unroll
@@ -766,119 +879,130 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
         }
       } else {
-        const bool live = t.k_blocks > 0;
-        uint32_t packed[COLS / 2];  // rows (2c, 2c + 1) of this lane's column
-        const bool with_add = KIND == kProductDense && p.add;
-        if (with_add) {
-          // the addend, fetched while the tile's MMAs run: two columns and
-          // one row per lane (rows are padded to even lengths), then swapped
-          // to one column and two rows as the results will be
-          const uint16_t* src = p.add + zbase +
-                                (static_cast<int64_t>(t.j0) + col_begin + (lane & 1)) * p.ld_out +
-                                (i & ~1);
+        for (;;) {
+          const bool live = t.k_blocks > 0;
+          uint32_t packed[COLS / 2];  // rows (2c, 2c + 1) of this lane's column
+          const bool with_add = KIND == kProductDense && p.add;
+          if (with_add) {
+            // the addend, fetched while the tile's MMAs run: two columns and
+            // one row per lane (rows are padded to even lengths), then swapped
+            // to one column and two rows as the results will be
+            const uint16_t* src = p.add + zbase +
+                                  (static_cast<int64_t>(t.j0) + col_begin + (lane & 1)) * p.ld_out +
+                                  (i & ~1);
 #pragma unroll
-          for (int c = 0; c < COLS; c += 2)
-            packed[c / 2] = (i & ~1) < p.M && c + (lane & 1) < ncols
-                                ? *reinterpret_cast<const uint32_t*>(src + c * p.ld_out)
-                                : 0u;
+            for (int c = 0; c < COLS; c += 2)
+              packed[c / 2] = (i & ~1) < p.M && c + (lane & 1) < ncols
+                                  ? *reinterpret_cast<const uint32_t*>(src + c * p.ld_out)
+                                  : 0u;
 #pragma unroll
-          for (int c = 0; c < COLS; c += 2) packed[c / 2] = swap_pair(packed[c / 2], lane);
-        }
-        if (live) {
-          if (!W.wait(tfull(acc), acc_phase)) break;
-          ptx::tc_fence_after();
-        }
-        const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NT + col_begin;
-        float alpha = p.alpha;
-        if (KIND == kProductDense && p.alpha_z) alpha *= p.alpha_z[t.z];
-        uint16_t* out = static_cast<uint16_t*>(p.out) + zbase;
-        const int on_diag = i - t.j0 - col_begin;
-#pragma unroll
-        for (int c = 0; c < COLS; c += LD) {
-          if (c < ncols) {
-            uint32_t r[LD];
-            if (live) tmem_ld(tq + c, r);
-            if (live) {
-              ptx::tmem_wait_ld();
-            } else {
-#pragma unroll
-              for (int u = 0; u < LD; ++u) r[u] = 0u;
-            }
-#pragma unroll
-            for (int u = 0; u < LD; u += 2) {
-              float v0 = __uint_as_float(r[u]), v1 = __uint_as_float(r[u + 1]);
-              if constexpr (KIND == kProductDense) {
-                v0 *= alpha;
-                v1 *= alpha;
-                if (with_add) {
-                  const __half2 a =
-                      *reinterpret_cast<const __half2*>(&packed[(c + u) / 2]);
-                  v0 = fmaf(p.beta, __low2float(a), v0);
-                  v1 = fmaf(p.beta, __high2float(a), v1);
-                }
-                // on the diagonal (i == j)
-                if (c + u == on_diag) v0 += p.diag;
-                if (c + u + 1 == on_diag) v1 += p.diag;
-              }
-              packed[(c + u) / 2] = pack_out(v0, v1, f16);
-            }
+            for (int c = 0; c < COLS; c += 2) packed[c / 2] = swap_pair(packed[c / 2], lane);
           }
-        }
-        if (live) {
-          // the accumulator is free before any store
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_relaxed_cluster(ptx::map_to_rank(tempty(acc), 0));
-          acc ^= 1;
-          if (acc == 0) acc_phase ^= 1u;
-        }
-        const int64_t j = static_cast<int64_t>(t.j0) + col_begin;
-        if (KIND == kProductGroups && p.staged) {
+          if (live) {
+            if (!W.wait(tfull(acc), acc_phase)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+          }
+          const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NT + col_begin;
+          float alpha = p.alpha;
+          if (KIND == kProductDense && p.alpha_z) alpha *= p.alpha_z[t.z];
+          uint16_t* out = static_cast<uint16_t*>(p.out) + zbase;
+          const int on_diag = i - t.j0 - col_begin;
 #pragma unroll
-          for (int c = 0; c < COLS; c += 32) {
+          for (int c = 0; c < COLS; c += LD) {
             if (c < ncols) {
-              if (lane == 0) tma_store_read_done();
-              __syncwarp();
+              uint32_t r[LD];
+              if (live) tmem_ld(tq + c, r);
+              if (live) {
+                ptx::tmem_wait_ld();
+              } else {
 #pragma unroll
-              for (int u = 0; u < 32; u += 2) {
-                const uint32_t v = swap_pair(packed[(c + u) / 2], lane);
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage_at + (u + (lane & 1)) * 64 +
-                                                             (lane & ~1) * 2),
-                             "r"(v)
-                             : "memory");
+                for (int u = 0; u < LD; ++u) r[u] = 0u;
               }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0 && i < p.M)
-                tma_store_3d<false>(&tm_out, stage_at, i, t.j0 + col_begin + c, t.z);
+#pragma unroll
+              for (int u = 0; u < LD; u += 2) {
+                float v0 = __uint_as_float(r[u]), v1 = __uint_as_float(r[u + 1]);
+                if constexpr (KIND == kProductDense) {
+                  v0 *= alpha;
+                  v1 *= alpha;
+                  if (with_add) {
+                    const __half2 a =
+                        *reinterpret_cast<const __half2*>(&packed[(c + u) / 2]);
+                    v0 = fmaf(p.beta, __low2float(a), v0);
+                    v1 = fmaf(p.beta, __high2float(a), v1);
+                  }
+                  // on the diagonal (i == j)
+                  if (c + u == on_diag) v0 += p.diag;
+                  if (c + u + 1 == on_diag) v1 += p.diag;
+                }
+                packed[(c + u) / 2] = pack_out(v0, v1, f16);
+              }
             }
           }
-        } else if (paired) {
-          uint16_t* dst = out + (j + (lane & 1)) * p.ld_out + (i & ~1);
-#pragma unroll
-          for (int c = 0; c < COLS; c += 2) {
-            if (c < ncols) {  // the same on every lane of the warp
-              const uint32_t v = swap_pair(packed[c / 2], lane);
-              if (i < p.M && c + (lane & 1) < ncols)
-                *reinterpret_cast<uint32_t*>(dst + c * p.ld_out) = v;
-            }
+          if (live) {
+            // the accumulator is free before any store
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_relaxed_cluster(ptx::map_to_rank(tempty(acc), 0));
+            acc ^= 1;
+            if (acc == 0) acc_phase ^= 1u;
           }
-        } else if (i < p.M) {
-          uint16_t* dst = out + j * p.ld_out + i;
+          const int64_t j = static_cast<int64_t>(t.j0) + col_begin;
+          if (KIND == kProductGroups && p.staged) {
 #pragma unroll
-          for (int c = 0; c < COLS; ++c)
-            if (c < ncols)
-              dst[c * p.ld_out] = static_cast<uint16_t>(packed[c / 2] >> (16 * (c & 1)));
-        }
-        if (KIND == kProductDense && p.symmetric && t.j0 >= t.i0 + kProductTileM && i < p.M) {
-          // the mirror image: row i, columns j (16 at a time; rows are padded
-          // to multiples of 16 elements)
-          uint16_t* dst = out + static_cast<int64_t>(i) * p.ld_out + j;
+            for (int c = 0; c < COLS; c += 32) {
+              if (c < ncols) {
+                if (lane == 0) tma_store_read_done();
+                __syncwarp();
 #pragma unroll
-          for (int c = 0; c < COLS; c += 8)
-            if (c < ncols)
-              *reinterpret_cast<uint4*>(dst + c) = make_uint4(packed[c / 2], packed[c / 2 + 1],
-                                                              packed[c / 2 + 2], packed[c / 2 + 3]);
+                for (int u = 0; u < 32; u += 2) {
+                  const uint32_t v = swap_pair(packed[(c + u) / 2], lane);
+                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage_at + (u + (lane & 1)) * 64 +
+                                                               (lane & ~1) * 2),
+                               "r"(v)
+                               : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && i < p.M)
+                  tma_store_3d<false>(&tm_out, stage_at, i, t.j0 + col_begin + c, t.z);
+              }
+            }
+          } else if (paired) {
+            uint16_t* dst = out + (j + (lane & 1)) * p.ld_out + (i & ~1);
+#pragma unroll
+            for (int c = 0; c < COLS; c += 2) {
+              if (c < ncols) {  // the same on every lane of the warp
+                const uint32_t v = swap_pair(packed[c / 2], lane);
+                if (i < p.M && c + (lane & 1) < ncols)
+                  *reinterpret_cast<uint32_t*>(dst + c * p.ld_out) = v;
+              }
+            }
+          } else if (i < p.M) {
+            uint16_t* dst = out + j * p.ld_out + i;
+#pragma unroll
+            for (int c = 0; c < COLS; ++c)
+              if (c < ncols)
+                dst[c * p.ld_out] = static_cast<uint16_t>(packed[c / 2] >> (16 * (c & 1)));
+          }
+          if (KIND == kProductDense && p.symmetric && t.j0 >= t.i0 + kProductTileM && i < p.M) {
+            // the mirror image: row i, columns j (16 at a time; rows are padded
+            // to multiples of 16 elements)
+            uint16_t* dst = out + static_cast<int64_t>(i) * p.ld_out + j;
+#pragma unroll
+            for (int c = 0; c < COLS; c += 8)
+              if (c < ncols)
+                *reinterpret_cast<uint4*>(dst + c) = make_uint4(packed[c / 2], packed[c / 2 + 1],
+                                                                packed[c / 2 + 2], packed[c / 2 + 3]);
+          }
+          if (!DUAL || t.nvalid2 == 0) break;
+          // the tile's second block
+          t.j0 += t.nvalid;
+          t.nvalid = t.nvalid2;
+          t.nvalid2 = 0;
+          ncols = min(t.nvalid - col_begin, COLS);
         }
       }
     }

@@ -3,7 +3,7 @@ products with both gradients, the gated activation with its gradient, the
 orthogonalised update.
 
 Bounds.  A product's FP32 sum truncates once per tensor-core step of 16 k; a
-16-bit result takes one chain over all of k, an FP32 result chains of 256 k
+16-bit result takes one chain over all of k, an FP32 result short chains
 that are then added.  With S = sum |a||b| that is at most S * 2^-23 per step
 (and per addition); 16-bit results add half a step of the result.  The
 activation's exponential and divide are good to 2^-18 here (arguments within
@@ -141,7 +141,7 @@ def test_every_row_tile_over_many_groups(pkg, rows):
 
 
 def test_long_sums_in_32_bits(pkg):
-    """FP32 results over a long k stay at FP32 accuracy (chains of 256)."""
+    """FP32 results over a long k stay at FP32 accuracy (short chains, added in FP32)."""
     g = gen(5)
     off = bounds([130, 20])
     x, w = randn(g, 150, 8192), randn(g, 2, 64, 8192)
