@@ -1,0 +1,479 @@
+// The orthogonalised update of matrices whose smaller extent m is at most 128,
+// all steps in one launch.
+//
+// Taken product by product such an update is a chain of 15 launches of a few
+// microseconds, each with next to no work.  Here a cluster of up to 8 CTAs
+// holds one matrix X [m, n] (n the larger extent; a tall matrix is held
+// transposed) in shared memory for all steps, each CTA a slice of columns:
+//
+//   A = X X^T       each CTA the product of its slice (tcgen05, M = 128); the
+//                   partial sums are added in FP32 over the cluster in rank
+//                   order, each CTA one part of A, and shared out as F16
+//   P = aI + bA + cA^2    every CTA for itself
+//   X <- P X        each CTA its own slice, in place
+//
+// One layout serves both uses of X: tiles of 128 rows by 64 columns, 128-byte
+// rows with the 128-byte swizzle.  Read with rows as M or N and columns as k
+// it is a K-major operand (A = X X^T), with columns as N and rows as k an
+// MN-major one (P X).
+//
+// F16 operands with the scales and the FP32 second part of the first step as
+// in beam_moe_orthogonalize.  Latency bound: per step two cluster barriers,
+// three tensor-core products of under a microsecond and their epilogues.
+#include "ortho_small.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "gemm_common.cuh"
+#include "launch_once.cuh"
+#include "ortho_scale.cuh"
+#include "pair_product.cuh"
+#include "ptx.cuh"
+
+namespace beam {
+namespace {
+
+using gemm::Waiter;
+
+constexpr int kThreads = 256;
+constexpr uint32_t kTile = 128 * 128;          // 128 rows of 64 F16 columns
+constexpr int kSliceMax = 320;                 // columns per CTA (256 for FP32 input)
+constexpr uint32_t kOffG = kSliceMax / 64 * kTile;
+constexpr uint32_t kOffP = kOffG + 2 * kTile;
+constexpr uint32_t kOffPart = kOffP + 2 * kTile;  // FP32 [128 columns][128 rows]; later X's low parts
+constexpr uint32_t kPartBytes = 128 * 128 * 4;
+constexpr uint32_t kOffMisc = kOffPart + kPartBytes;
+constexpr uint32_t kSmem = 1024 + kOffMisc + 256;
+constexpr uint32_t kTmemStep = 128;            // TMEM column of P X
+static_assert(kSmem <= 227 * 1024, "shared memory budget");
+
+struct Share {           // what the CTAs of a cluster tell one another
+  uint32_t amax;
+  int32_t exp;
+  float sum;
+};
+
+// Byte offset of the 16-byte word of row r that holds columns 8w .. 8w + 7 of
+// the tiles at `base`.
+__device__ __forceinline__ uint32_t word_at(int r, int w) {
+  return static_cast<uint32_t>(w >> 3) * kTile + static_cast<uint32_t>(r) * 128 +
+         (static_cast<uint32_t>((w & 7) ^ (r & 7)) << 4);
+}
+
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
+  // 64-column tiles kTile apart, groups of 8 rows (k) 1024 bytes apart
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(kTile >> 4) << 16) |
+         (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) |
+         (static_cast<uint64_t>(2u) << 61);
+}
+
+__device__ __forceinline__ float4 load_peer4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_peer2(uint32_t cluster_addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(cluster_addr), "r"(a), "r"(b)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t load_peer(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Eight elements (r, 8w ..) of this CTA's slice; 0 outside the matrix.
+template <int TYPE>
+__device__ __forceinline__ void load8(const OrthoSmallArgs& p, int64_t base, int col0, int ncols,
+                                      int r, int w, float (&v)[8]) {
+  const int64_t at = base + r * p.sr + (col0 + static_cast<int64_t>(w) * 8) * p.sc;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    v[k] = w * 8 + k < ncols ? element<TYPE>(p.src, at + k * p.sc) : 0.f;
+}
+
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSmallArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t x_at = raw + pad, g_at = x_at + kOffG, p_at = x_at + kOffP,
+                 part_at = x_at + kOffPart;
+  uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + kOffMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 16);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + kOffMisc + 20);
+  Share* share = reinterpret_cast<Share*>(smem + kOffMisc + 32);
+  Share* warp_share = reinterpret_cast<Share*>(smem + kOffMisc + 64);  // 8 warps
+  const uint32_t bar = ptx::smem_addr(bar_mem);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cs = p.cluster;
+  const uint32_t rank = cs > 1 ? ptx::cluster_rank() : 0u;
+  const int z = blockIdx.x / cs;
+  const int m16 = (p.m + 15) & ~15;
+  const int col0 = static_cast<int>(rank) * p.slice;
+  const int ncols = max(0, min(p.slice, p.n - col0));
+  const int64_t src = z * p.sz;
+  // threads walk words of 8 columns in the order that neighbours in memory
+  // are neighbours in the warp
+  const bool along_n = p.sc <= p.sr;
+  const int words = p.slice / 8;
+  const int items = m16 * words;
+  auto item = [&](int at, int& r, int& w) {
+    if (along_n) {
+      r = at / words;
+      w = at - r * words;
+    } else {
+      w = at / m16;
+      r = at - w * m16;
+    }
+  };
+
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(bar, 1);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 0) {
+    ptx::tmem_alloc(ptx::smem_addr(tmem_slot), 512);
+    ptx::tmem_relinquish();
+  }
+
+  // ------------------------------------------- magnitudes and the norm
+  uint32_t top = 0;
+  ScaledSum acc;
+  for (int at = threadIdx.x; at < items; at += kThreads) {
+    int r, w;
+    item(at, r, w);
+    if (r >= p.m) continue;
+    float v[8];
+    load8<TYPE>(p, src, col0, ncols, r, w, v);
+    acc.add8(v, top);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int e = __shfl_xor_sync(0xffffffffu, acc.exp, o);
+    const float f = __shfl_xor_sync(0xffffffffu, acc.sum, o);
+    acc.add(e, f);
+  }
+  if (lane == 0) warp_share[warp] = Share{top, acc.exp, acc.sum};
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (threadIdx.x == 0) {
+    Share s = warp_share[0];
+    ScaledSum t{s.exp, s.sum};
+    for (int k = 1; k < kThreads / 32; ++k) {
+      s.amax = max(s.amax, warp_share[k].amax);
+      t.add(warp_share[k].exp, warp_share[k].sum);
+    }
+    *share = Share{s.amax, t.exp, t.sum};
+  }
+  if (cs > 1)
+    ptx::cluster_sync();
+  else
+    __syncthreads();
+  ScaledSum total;
+  uint32_t amax = 0;
+  for (int q = 0; q < cs; ++q) {
+    const uint32_t at = cs > 1 ? ptx::map_to_rank(ptx::smem_addr(share), q) : ptx::smem_addr(share);
+    amax = max(amax, load_peer(at));
+    total.add(static_cast<int>(load_peer(at + 4)), __uint_as_float(load_peer(at + 8)));
+  }
+  const float k0 = range_scale(amax);
+  const float inv = inverse_norm(amax, total, k0, p.eps);
+
+  // ------------------------------------------- the scaled F16 copy
+  auto fill = [&](uint32_t dst, bool low) {
+    for (int at = threadIdx.x; at < items; at += kThreads) {
+      int r, w;
+      item(at, r, w);
+      float v[8];
+      if (r < p.m) {
+        load8<TYPE>(p, src, col0, ncols, r, w, v);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = 0.f;
+      }
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float a = v[2 * k] * k0, b = v[2 * k + 1] * k0;
+        o[k] = half2_bits(a, b);
+        if (low) {
+          const __half2 h = *reinterpret_cast<const __half2*>(&o[k]);
+          o[k] = half2_bits(a - __low2float(h), b - __high2float(h));
+        }
+      }
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + word_at(r, w)),
+                   "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                   : "memory");
+    }
+  };
+  fill(x_at, false);
+
+  const Waiter W{abort_flag, p.status, p.wait_limit_ns};
+  uint32_t phase = 0;
+  constexpr uint32_t kF16Idesc = (1u << 4) | ((128u >> 4) << 24);  // F16 A and B, FP32 D, M = 128
+  const uint32_t idesc_m16 = kF16Idesc | (static_cast<uint32_t>(m16 >> 3) << 17);
+  // writes of shared memory -> the tensor core's reads
+  auto publish = [&] {
+    asm volatile("fence.proxy.async;" ::: "memory");
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+  };
+  auto finish = [&] {  // all MMAs of the phase have completed
+    W.wait(bar, phase);
+    phase ^= 1u;
+    ptx::tc_fence_after();
+  };
+  const int quarter = warp & 3, half = warp >> 2;
+  const int row = quarter * 32 + lane;  // TMEM lane
+  const uint32_t tq = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  const bool vector_out = p.ocol == 1 && p.orow % 8 == 0 && p.oz % 8 == 0 &&
+                          (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+
+  for (int t = 0; t < p.steps; ++t) {
+    const bool last = t + 1 == p.steps;
+    // ----------------------------------------------------- A = X X^T
+    publish();
+    if (warp == 0) {
+      if (lane == 0) {
+        for (int k = 0; k < p.slice / 16; ++k) {
+          const uint32_t at = x_at + static_cast<uint32_t>(k >> 2) * kTile + (k & 3) * 32;
+          ptx::mma_bf16(tmem, ptx::sdesc_sw128(at), ptx::sdesc_sw128(at), idesc_m16, k ? 1u : 0u);
+        }
+        ptx::mma_commit(bar);
+      }
+      __syncwarp();
+    }
+    finish();
+    const float gram_scale = t == 0 ? kScaleGram * inv * inv : kScaleGram / (kScaleX * kScaleX);
+    // partial sums, one column of 128 rows after another (A is symmetric:
+    // column c is also row c)
+    for (int c = half * 64; c < min(m16, half * 64 + 64); c += 16) {
+      uint32_t r[16];
+      ptx::tmem_ld16(tq + c, r);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int u = 0; u < 16; ++u)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(part_at + ((c + u) * 128 + row) * 4), "r"(r[u])
+                     : "memory");
+    }
+    ptx::tc_fence_before();
+    if (cs > 1)
+      ptx::cluster_sync();
+    else
+      __syncthreads();
+    ptx::tc_fence_after();
+    // this CTA's share of A: words of 4 rows of columns c = rank, rank + cs, ...
+    const int quads = m16 / 4;
+    const int mine = (m16 - static_cast<int>(rank) + cs - 1) / cs;
+    for (int at = threadIdx.x; at < mine * quads; at += kThreads) {
+      const int c = static_cast<int>(rank) + at / quads * cs;
+      const int r4 = at % quads * 4;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int q = 0; q < cs; ++q) {
+        const uint32_t from = part_at + (c * 128 + r4) * 4;
+        const float4 v = load_peer4(cs > 1 ? ptx::map_to_rank(from, q) : from);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      }
+      const uint32_t lo = half2_bits(s.x * gram_scale, s.y * gram_scale);
+      const uint32_t hi = half2_bits(s.z * gram_scale, s.w * gram_scale);
+      const uint32_t to = g_at + word_at(c, r4 >> 3) + (r4 & 4) * 2;
+      for (int q = 0; q < cs; ++q) store_peer2(cs > 1 ? ptx::map_to_rank(to, q) : to, lo, hi);
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");
+    if (cs > 1) ptx::cluster_sync();
+    // ----------------------------------------------------- P = aI + bA + cA^2
+    publish();
+    if (warp == 0) {
+      if (lane == 0) {
+        for (int k = 0; k < m16 / 16; ++k) {
+          const uint32_t at = g_at + static_cast<uint32_t>(k >> 2) * kTile + (k & 3) * 32;
+          ptx::mma_bf16(tmem, ptx::sdesc_sw128(at), ptx::sdesc_sw128(at), idesc_m16, k ? 1u : 0u);
+        }
+        ptx::mma_commit(bar);
+      }
+      __syncwarp();
+    }
+    // the low parts of a 32-bit update, for the first P X
+    const bool low = TYPE == kF32 && t == 0;
+    if (low) fill(part_at, true);
+    finish();
+    {
+      const float ca = kScalePoly * p.c / (kScaleGram * kScaleGram);
+      const float cb = kScalePoly * p.b / kScaleGram;
+      const float cd = kScalePoly * p.a;
+      for (int c = half * 64; c < min(m16, half * 64 + 64); c += 16) {
+        uint32_t r[16];
+        ptx::tmem_ld16(tq + c, r);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t at = word_at(row, (c >> 3) + w);
+          uint32_t g[4], o[4];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(g[0]), "=r"(g[1]), "=r"(g[2]), "=r"(g[3])
+                       : "r"(g_at + at)
+                       : "memory");
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const __half2 h = *reinterpret_cast<const __half2*>(&g[k]);
+            const int col = c + w * 8 + 2 * k;
+            float a = fmaf(cb, __low2float(h), ca * __uint_as_float(r[w * 8 + 2 * k]));
+            float b = fmaf(cb, __high2float(h), ca * __uint_as_float(r[w * 8 + 2 * k + 1]));
+            if (col == row) a += cd;
+            if (col + 1 == row) b += cd;
+            o[k] = half2_bits(a, b);
+          }
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_at + at), "r"(o[0]),
+                       "r"(o[1]), "r"(o[2]), "r"(o[3])
+                       : "memory");
+        }
+      }
+    }
+    // ----------------------------------------------------- X <- P X
+    publish();
+    if (warp == 0) {
+      if (lane == 0) {
+        for (int n0 = 0; n0 < p.slice; n0 += 256) {
+          const uint32_t nn = static_cast<uint32_t>(min(256, p.slice - n0));
+          const uint32_t idesc = kF16Idesc | (1u << 16) | ((nn >> 3) << 17);  // B MN-major
+          for (int pass = 0; pass < (low ? 2 : 1); ++pass) {
+            const uint32_t xb = (pass ? part_at : x_at) + static_cast<uint32_t>(n0 / 64) * kTile;
+            for (int k = 0; k < m16 / 16; ++k) {
+              const uint32_t at = p_at + static_cast<uint32_t>(k >> 2) * kTile + (k & 3) * 32;
+              ptx::mma_bf16(tmem + kTmemStep + n0, ptx::sdesc_sw128(at), desc_mn(xb + k * 2048),
+                            idesc, (pass | k) ? 1u : 0u);
+            }
+          }
+        }
+        ptx::mma_commit(bar);
+      }
+      __syncwarp();
+    }
+    finish();
+    const float x_scale = (last ? 1.f : kScaleX) / kScalePoly * (t == 0 ? inv : 1.f / kScaleX);
+    for (int c = half * 16; c < p.slice; c += 32) {
+      uint32_t r[16];
+      ptx::tmem_ld16(tq + kTmemStep + c, r);
+      ptx::tmem_wait_ld();
+      float v[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) v[u] = __uint_as_float(r[u]) * x_scale;
+      if (!last) {
+        if (row < m16) {
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             x_at + word_at(row, (c >> 3) + w)),
+                         "r"(half2_bits(v[w * 8], v[w * 8 + 1])),
+                         "r"(half2_bits(v[w * 8 + 2], v[w * 8 + 3])),
+                         "r"(half2_bits(v[w * 8 + 4], v[w * 8 + 5])),
+                         "r"(half2_bits(v[w * 8 + 6], v[w * 8 + 7]))
+                         : "memory");
+        }
+      } else if (row < p.m) {
+        uint16_t* out = static_cast<uint16_t*>(p.out) + z * p.oz + row * p.orow +
+                        (col0 + c) * p.ocol;
+        uint32_t o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (p.out_type == kF16) {
+            o[k] = half2_bits(v[2 * k], v[2 * k + 1]);
+          } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+            o[k] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+        if (vector_out && c + 16 <= ncols) {
+          reinterpret_cast<uint4*>(out)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+          reinterpret_cast<uint4*>(out)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+        } else {
+#pragma unroll
+          for (int u = 0; u < 16; ++u)
+            if (c + u < ncols)
+              out[u * p.ocol] = static_cast<uint16_t>(o[u / 2] >> (16 * (u & 1)));
+        }
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  // no CTA leaves while a peer may still read its shared memory
+  if (cs > 1)
+    ptx::cluster_sync();
+  else
+    __syncthreads();
+  if (warp == 0) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int TYPE>
+cudaError_t launch_typed(const OrthoSmallArgs& p, int32_t batch, cudaStream_t s) {
+  constexpr auto kern = ortho_small_kernel<TYPE>;
+  const cudaError_t err = smem_limit_once<kern>(static_cast<int>(kSmem));
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(batch * p.cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+}  // namespace
+
+bool ortho_small_shape(int32_t batch, int32_t m, int32_t n, int32_t type, int num_sms,
+                       int32_t* cluster, int32_t* slice) {
+  if (m > kOrthoSmallM) return false;
+  const int32_t most = type == kF32 ? 256 : kSliceMax;
+  const int32_t least = (n + most - 1) / most;  // CTAs
+  if (least > kOrthoSmallCluster) return false;
+  // more CTAs than needed while the stack leaves SMs free and a slice has
+  // more than 64 columns
+  int32_t c = least;
+  while (c < kOrthoSmallCluster && batch * (c + 1) <= num_sms && (n + c - 1) / c > 64) ++c;
+  *cluster = c;
+  *slice = ((n + c - 1) / c + 63) / 64 * 64;
+  // whole slices of 64 may need fewer CTAs than c
+  *cluster = (n + *slice - 1) / *slice;
+  return true;
+}
+
+cudaError_t launch_ortho_small(const OrthoSmallArgs& p, int32_t batch, cudaStream_t s) {
+  switch (p.type) {
+    case kBf16: return launch_typed<kBf16>(p, batch, s);
+    case kF16: return launch_typed<kF16>(p, batch, s);
+    case kF32: return launch_typed<kF32>(p, batch, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace beam

@@ -1,0 +1,34 @@
+// The orthogonalised update of small matrices in one launch (ortho_small.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace beam {
+
+struct OrthoSmallArgs {
+  const void* src;             // kBf16, kF16 or kF32
+  int64_t sz, sr, sc;          // elements between matrices, along m and along n
+  int32_t m, n;                // smaller and larger extent
+  int32_t type;
+  int32_t steps;
+  float a, b, c, eps;
+  void* out;                   // out[z * oz + r * orow + col * ocol], r < m, col < n
+  int64_t oz, orow, ocol;
+  int32_t out_type;            // kBf16 or kF16
+  int32_t cluster;             // CTAs per matrix
+  int32_t slice;               // columns n per CTA, a multiple of 64
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+};
+
+constexpr int kOrthoSmallM = 128;        // smaller extent, at most
+constexpr int kOrthoSmallCluster = 8;    // CTAs per matrix, at most
+
+// Columns per CTA and CTAs per matrix for a stack; false: too large.
+bool ortho_small_shape(int32_t batch, int32_t m, int32_t n, int32_t type, int num_sms,
+                       int32_t* cluster, int32_t* slice);
+cudaError_t launch_ortho_small(const OrthoSmallArgs& p, int32_t batch, cudaStream_t s);
+
+}  // namespace beam

@@ -12,6 +12,8 @@
 #include "../../include/beam_moe.h"
 #include "common.cuh"
 #include "host.cuh"
+#include "ortho_scale.cuh"
+#include "ortho_small.cuh"
 #include "pair_product.cuh"
 #include "train_ops.cuh"
 
@@ -211,10 +213,9 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
 }
 
 // ------------------------------------------------------ orthogonalised update
-// F16 scales of the three intermediates (powers of two; see the kernel's
-// note in beam_moe_orthogonalize): singular values stay near or below one,
-// so elements stay below these and the small ones keep their bits.
-constexpr float kScaleX = 1024.f, kScaleGram = 1024.f, kScalePoly = 256.f;
+using beam::kScaleGram;
+using beam::kScalePoly;
+using beam::kScaleX;
 
 struct OrthoLayout {
   int64_t m, ld, ldm;   // smaller extent, row strides of X and of the m x m products
@@ -415,6 +416,33 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
 
   const int64_t batch = d->batch, R = d->rows, C = d->cols, m = L.m;
   const bool wide = R <= C;
+  int32_t cluster, slice;
+  if (beam::ortho_small_shape(d->batch, static_cast<int32_t>(m), std::max(d->rows, d->cols),
+                              d->dtype, dev.sms, &cluster, &slice)) {
+    beam::OrthoSmallArgs o = {};
+    o.src = src;
+    o.sz = d->stride_batch;
+    o.sr = wide ? d->stride_row : d->stride_col;
+    o.sc = wide ? d->stride_col : d->stride_row;
+    o.m = static_cast<int32_t>(m);
+    o.n = std::max(d->rows, d->cols);
+    o.type = d->dtype;
+    o.steps = d->steps;
+    o.a = d->a;
+    o.b = d->b;
+    o.c = d->c;
+    o.eps = d->eps;
+    o.out = out;
+    o.oz = R * C;
+    o.orow = wide ? C : 1;
+    o.ocol = wide ? 1 : C;
+    o.out_type = d->out_dtype;
+    o.cluster = cluster;
+    o.slice = slice;
+    o.status = static_cast<uint32_t*>(workspace);
+    o.wait_limit_ns = beam::host::wait_limit_ns();
+    return launched(beam::launch_ortho_small(o, d->batch, s));
+  }
   const bool split = d->dtype == BEAM_DTYPE_F32;
   uint16_t* x[2] = {at<uint16_t>(workspace, L.x0), at<uint16_t>(workspace, L.x1)};
   uint16_t* gram = at<uint16_t>(workspace, L.gram);

@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "launch_once.cuh"
+#include "ortho_scale.cuh"
 #include "pair_product.cuh"
 #include "ptx.cuh"
 
@@ -17,12 +18,6 @@ namespace beam {
 namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
-
-template <bool F16>
-__device__ __forceinline__ float from16(uint32_t bits) {
-  return F16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(bits)))
-             : __uint_as_float(bits << 16);
-}
 
 template <bool F16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
@@ -220,25 +215,6 @@ bool gate_aligned(const GateArgs& p, bool grad) {
 }
 
 // ------------------------------------------------------ orthogonalised update
-template <int TYPE>
-__device__ __forceinline__ float element(const void* src, int64_t at) {
-  if constexpr (TYPE == kF32)
-    return static_cast<const float*>(src)[at];
-  else
-    return from16<TYPE == kF16>(static_cast<const uint16_t*>(src)[at]);
-}
-
-// The power of two that brings the largest magnitude into [2^13, 2^14): F16
-// then keeps every bit of a 16-bit update down to 2^-27 of its largest
-// element, and no product or norm over- or underflows.  Zero, infinite and
-// NaN maxima take 1 (and then give zeros, or NaN throughout).
-__device__ __forceinline__ float range_scale(uint32_t amax_bits) {
-  const int e = static_cast<int>(amax_bits >> 23);
-  if (amax_bits == 0 || e == 255) return 1.f;
-  const int k = min(13 + 127 - e, 120);
-  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-}
-
 __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
@@ -274,24 +250,6 @@ __device__ __forceinline__ void load_row8(const NormArgs& p, int64_t base, int c
   }
 }
 
-// Sum of squares over any range of magnitudes: sum * 2^(2 exp), where exp is
-// the exponent of the largest element met so far (its bits' exponent field).
-struct ScaledSum {
-  int exp = 0;
-  float sum = 0.f;
-
-  static __device__ __forceinline__ float pow2(int k) {  // 2^k, 0 below the normal range
-    return k < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-  }
-  __device__ __forceinline__ void add(int e, float s) {
-    if (e > exp) {
-      sum *= pow2(max(2 * (exp - e), -200));
-      exp = e;
-    }
-    sum = fmaf(s, pow2(max(2 * (e - exp), -200)), sum);
-  }
-};
-
 // First pass: each block's largest magnitude and sum of squares, in one read.
 template <int TYPE, bool VEC>
 __global__ void __launch_bounds__(256) amax_kernel(const NormArgs p) {
@@ -307,22 +265,7 @@ __global__ void __launch_bounds__(256) amax_kernel(const NormArgs p) {
     const uint32_t r = at / per_row;
     float v[8];
     load_row8<TYPE, VEC>(p, z * p.sz + r * p.sr, static_cast<int>(at - r * per_row) * 8, v);
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      // as integers, so that a NaN is larger than every number
-      top = max(top, __float_as_uint(v[k]) & 0x7fffffffu);
-    m = max(m, top);
-    if (top == 0 || top >= 0x7f800000u) continue;  // not finite: the maximum tells
-    // squares of the elements times 2^(127 - e), which brings the largest
-    // near 1 (subnormals count from the smallest normal exponent; the largest
-    // exponent's power of two would be subnormal)
-    const int e = min(max(static_cast<int>(top >> 23), 1), 253);
-    const float k1 = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-    float sq = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) sq = fmaf(v[k] * k1, v[k] * k1, sq);
-    acc.add(e, sq);
+    acc.add8(v, m);
   }
   m = block_max(m, s);
 #pragma unroll
@@ -377,11 +320,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormArgs p) {
     ScaledSum acc;
     for (int q = 0; q < p.blocks; ++q)
       acc.add(p.sum_exp[z * kNormBlocks + q], p.sumsq[z * kNormBlocks + q]);
-    // the sum is in units of 2^(2 (exp - 127)); the copy's scale is k
-    const float norm = sqrtf(acc.sum) * (__uint_as_float(static_cast<uint32_t>(acc.exp) << 23) * k);
-    const float inv = amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u)
-                                          : 1.f / (norm + p.eps * k);
-    // an all-zero matrix with eps = 0 stays 0 / 0
+    const float inv = inverse_norm(amax, acc, k, p.eps);
     p.alpha_gram[z] = p.scale_gram * inv * inv;
     p.alpha_step[z] = p.scale_step * inv;
   }
