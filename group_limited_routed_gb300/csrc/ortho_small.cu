@@ -39,7 +39,8 @@ namespace {
 
 using gemm::Waiter;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
+constexpr int kWarpCols = 128 / (kThreads / 128);  // columns of A and P per warp
 constexpr uint32_t kTile = 128 * 128;          // 128 rows of 64 F16 columns
 constexpr int kSliceMax = 320;                 // columns per CTA (256 for FP32 input)
 constexpr uint32_t kOffG = kSliceMax / 64 * kTile;
@@ -47,15 +48,9 @@ constexpr uint32_t kOffP = kOffG + 2 * kTile;
 constexpr uint32_t kOffPart = kOffP + 2 * kTile;  // FP32 [128 columns][128 rows]; later X's low parts
 constexpr uint32_t kPartBytes = 128 * 128 * 4;
 constexpr uint32_t kOffMisc = kOffPart + kPartBytes;
-constexpr uint32_t kSmem = 1024 + kOffMisc + 256;
+constexpr uint32_t kSmem = 1024 + kOffMisc + 32 + kThreads / 32 * 4 + 128 * 4;
 constexpr uint32_t kTmemStep = 128;            // TMEM column of P X
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
-
-struct Share {           // what the CTAs of a cluster tell one another
-  uint32_t amax;
-  int32_t exp;
-  float sum;
-};
 
 // Byte offset of the 16-byte word of row r that holds columns 8w .. 8w + 7 of
 // the tiles at `base`.
@@ -94,29 +89,59 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Eight elements (r, 8w ..) of this CTA's slice; 0 outside the matrix.
+// Eight elements (r, 8w ..) of this CTA's slice, as loaded (0 outside the
+// matrix): held in registers between the norm and the scaled copy.
 template <int TYPE>
-__device__ __forceinline__ void load8(const OrthoSmallArgs& p, int64_t base, int col0, int ncols,
-                                      int r, int w, float (&v)[8]) {
-  const int64_t at = base + r * p.sr + (col0 + static_cast<int64_t>(w) * 8) * p.sc;
+struct Raw8 {
+  uint32_t w[TYPE == kF32 ? 8 : 4];
+
+  __device__ __forceinline__ void load(const OrthoSmallArgs& p, int64_t base, int col0, int ncols,
+                                       int r, int word, bool vector) {
+    const int64_t at = base + r * p.sr + (col0 + static_cast<int64_t>(word) * 8) * p.sc;
+    const int left = r < p.m ? ncols - word * 8 : 0;
+    if constexpr (TYPE == kF32) {
+      const float* q = static_cast<const float*>(p.src) + at;
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    v[k] = w * 8 + k < ncols ? element<TYPE>(p.src, at + k * p.sc) : 0.f;
-}
+      for (int k = 0; k < 8; ++k) w[k] = k < left ? __float_as_uint(q[k * p.sc]) : 0u;
+    } else {
+      const uint16_t* q = static_cast<const uint16_t*>(p.src) + at;
+      if (vector && left >= 8) {
+        const uint4 v = *reinterpret_cast<const uint4*>(q);
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          w[k] = 2 * k < left ? q[2 * k * p.sc] : 0u;
+          if (2 * k + 1 < left) w[k] |= static_cast<uint32_t>(q[(2 * k + 1) * p.sc]) << 16;
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void floats(float (&v)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if constexpr (TYPE == kF32)
+        v[k] = __uint_as_float(w[k]);
+      else
+        v[k] = from16<TYPE == kF16>(w[k / 2] >> (16 * (k & 1)) & 0xffffu);
+    }
+  }
+};
 
 template <int TYPE>
 __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSmallArgs p) {
   extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = ptx::smem_addr(smem_raw);
-  const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+  const uint32_t raw_addr = ptx::smem_addr(smem_raw);
+  const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
-  const uint32_t x_at = raw + pad, g_at = x_at + kOffG, p_at = x_at + kOffP,
+  const uint32_t x_at = raw_addr + pad, g_at = x_at + kOffG, p_at = x_at + kOffP,
                  part_at = x_at + kOffPart;
   uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + kOffMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 16);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + kOffMisc + 20);
-  Share* share = reinterpret_cast<Share*>(smem + kOffMisc + 32);
-  Share* warp_share = reinterpret_cast<Share*>(smem + kOffMisc + 64);  // 8 warps
+  uint32_t* share = reinterpret_cast<uint32_t*>(smem + kOffMisc + 24);  // this CTA's maximum
+  uint32_t* warp_max = reinterpret_cast<uint32_t*>(smem + kOffMisc + 32);
+  float* squares = reinterpret_cast<float*>(smem + kOffMisc + 32 + kThreads / 32 * 4);  // [128]
   const uint32_t bar = ptx::smem_addr(bar_mem);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -152,68 +177,65 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
     ptx::tmem_relinquish();
   }
 
-  // ------------------------------------------- magnitudes and the norm
+  // ------------------------------------------- the largest magnitude
+  constexpr int kItems = 128 * (TYPE == kF32 ? 256 : kSliceMax) / 8 / kThreads;
+  const bool vector_in = TYPE != kF32 && p.sc == 1 && p.sr % 8 == 0 && p.sz % 8 == 0 &&
+                         (reinterpret_cast<uintptr_t>(p.src) & 15) == 0;
+  Raw8<TYPE> raw[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    int r = 128, w = 0;
+    const int at = threadIdx.x + k * kThreads;
+    if (at < items) item(at, r, w);
+    raw[k].load(p, src, col0, ncols, r, w, vector_in);
+  }
   uint32_t top = 0;
-  ScaledSum acc;
-  for (int at = threadIdx.x; at < items; at += kThreads) {
-    int r, w;
-    item(at, r, w);
-    if (r >= p.m) continue;
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
     float v[8];
-    load8<TYPE>(p, src, col0, ncols, r, w, v);
-    acc.add8(v, top);
+    raw[k].floats(v);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      // as integers, so that a NaN is larger than every number
+      top = max(top, __float_as_uint(v[u]) & 0x7fffffffu);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int e = __shfl_xor_sync(0xffffffffu, acc.exp, o);
-    const float f = __shfl_xor_sync(0xffffffffu, acc.sum, o);
-    acc.add(e, f);
-  }
-  if (lane == 0) warp_share[warp] = Share{top, acc.exp, acc.sum};
+  for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) warp_max[warp] = top;
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (threadIdx.x == 0) {
-    Share s = warp_share[0];
-    ScaledSum t{s.exp, s.sum};
-    for (int k = 1; k < kThreads / 32; ++k) {
-      s.amax = max(s.amax, warp_share[k].amax);
-      t.add(warp_share[k].exp, warp_share[k].sum);
-    }
-    *share = Share{s.amax, t.exp, t.sum};
+    for (int k = 0; k < kThreads / 32; ++k) top = max(top, warp_max[k]);
+    *share = top;
   }
   if (cs > 1)
     ptx::cluster_sync();
   else
     __syncthreads();
-  ScaledSum total;
   uint32_t amax = 0;
   for (int q = 0; q < cs; ++q) {
-    const uint32_t at = cs > 1 ? ptx::map_to_rank(ptx::smem_addr(share), q) : ptx::smem_addr(share);
-    amax = max(amax, load_peer(at));
-    total.add(static_cast<int>(load_peer(at + 4)), __uint_as_float(load_peer(at + 8)));
+    const uint32_t at = ptx::smem_addr(share);
+    amax = max(amax, load_peer(cs > 1 ? ptx::map_to_rank(at, q) : at));
   }
   const float k0 = range_scale(amax);
-  const float inv = inverse_norm(amax, total, k0, p.eps);
+  float inv = 0.f;  // X = inv * copy: from the first A's trace
 
   // ------------------------------------------- the scaled F16 copy
   auto fill = [&](uint32_t dst, bool low) {
-    for (int at = threadIdx.x; at < items; at += kThreads) {
+#pragma unroll
+    for (int it = 0; it < kItems; ++it) {
+      const int at = threadIdx.x + it * kThreads;
+      if (at >= items) break;
       int r, w;
       item(at, r, w);
       float v[8];
-      if (r < p.m) {
-        load8<TYPE>(p, src, col0, ncols, r, w, v);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = 0.f;
-      }
+      raw[it].floats(v);
       uint32_t o[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        float a = v[2 * k] * k0, b = v[2 * k + 1] * k0;
+        const float a = v[2 * k] * k0, b = v[2 * k + 1] * k0;
         o[k] = half2_bits(a, b);
         if (low) {
           const __half2 h = *reinterpret_cast<const __half2*>(&o[k]);
@@ -228,6 +250,8 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
   fill(x_at, false);
 
   const Waiter W{abort_flag, p.status, p.wait_limit_ns};
+  // warp 0 walks the products as a whole, one lane of it issues
+  const bool elected = ptx::elect_one();
   uint32_t phase = 0;
   constexpr uint32_t kF16Idesc = (1u << 4) | ((128u >> 4) << 24);  // F16 A and B, FP32 D, M = 128
   const uint32_t idesc_m16 = kF16Idesc | (static_cast<uint32_t>(m16 >> 3) << 17);
@@ -243,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
     phase ^= 1u;
     ptx::tc_fence_after();
   };
-  const int quarter = warp & 3, half = warp >> 2;
+  const int quarter = warp & 3, part = warp >> 2;
   const int row = quarter * 32 + lane;  // TMEM lane
   const uint32_t tq = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   const bool vector_out = p.ocol == 1 && p.orow % 8 == 0 && p.oz % 8 == 0 &&
@@ -254,20 +278,18 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
     // ----------------------------------------------------- A = X X^T
     publish();
     if (warp == 0) {
-      if (lane == 0) {
-        for (int k = 0; k < p.slice / 16; ++k) {
-          const uint32_t at = x_at + static_cast<uint32_t>(k >> 2) * kTile + (k & 3) * 32;
+      for (int k = 0; k < p.slice / 16; ++k) {
+        const uint32_t at = x_at + static_cast<uint32_t>(k >> 2) * kTile + (k & 3) * 32;
+        if (elected)
           ptx::mma_bf16(tmem, ptx::sdesc_sw128(at), ptx::sdesc_sw128(at), idesc_m16, k ? 1u : 0u);
-        }
-        ptx::mma_commit(bar);
       }
+      if (elected) ptx::mma_commit(bar);
       __syncwarp();
     }
     finish();
-    const float gram_scale = t == 0 ? kScaleGram * inv * inv : kScaleGram / (kScaleX * kScaleX);
     // partial sums, one column of 128 rows after another (A is symmetric:
     // column c is also row c)
-    for (int c = half * 64; c < min(m16, half * 64 + 64); c += 16) {
+    for (int c = part * kWarpCols; c < min(m16, (part + 1) * kWarpCols); c += 16) {
       uint32_t r[16];
       ptx::tmem_ld16(tq + c, r);
       ptx::tmem_wait_ld();
@@ -282,6 +304,26 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
     else
       __syncthreads();
     ptx::tc_fence_after();
+    if (t == 0) {
+      // the squared norm is the trace of the copy's A: FP32 sums in an order
+      // that no memory layout of the update changes
+      if (threadIdx.x < 128) {
+        float d = 0.f;
+        if (threadIdx.x < static_cast<unsigned>(m16)) {
+          const uint32_t from = part_at + threadIdx.x * (128 + 1) * 4;
+          for (int q = 0; q < cs; ++q)
+            d += __uint_as_float(load_peer(cs > 1 ? ptx::map_to_rank(from, q) : from));
+        }
+        squares[threadIdx.x] = d;
+      }
+      __syncthreads();
+      float sum = 0.f;
+      for (int k = lane; k < 128; k += 32) sum += squares[k];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      inv = amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : 1.f / (sqrtf(sum) + p.eps * k0);
+    }
+    const float gram_scale = t == 0 ? kScaleGram * inv * inv : kScaleGram / (kScaleX * kScaleX);
     // this CTA's share of A: words of 4 rows of columns c = rank, rank + cs, ...
     const int quads = m16 / 4;
     const int mine = (m16 - static_cast<int>(rank) + cs - 1) / cs;
@@ -304,13 +346,12 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
     // ----------------------------------------------------- P = aI + bA + cA^2
     publish();
     if (warp == 0) {
-      if (lane == 0) {
-        for (int k = 0; k < m16 / 16; ++k) {
-          const uint32_t at = g_at + static_cast<uint32_t>(k >> 2) * kTile + (k & 3) * 32;
+      for (int k = 0; k < m16 / 16; ++k) {
+        const uint32_t at = g_at + static_cast<uint32_t>(k >> 2) * kTile + (k & 3) * 32;
+        if (elected)
           ptx::mma_bf16(tmem, ptx::sdesc_sw128(at), ptx::sdesc_sw128(at), idesc_m16, k ? 1u : 0u);
-        }
-        ptx::mma_commit(bar);
       }
+      if (elected) ptx::mma_commit(bar);
       __syncwarp();
     }
     // the low parts of a 32-bit update, for the first P X
@@ -321,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
       const float ca = kScalePoly * p.c / (kScaleGram * kScaleGram);
       const float cb = kScalePoly * p.b / kScaleGram;
       const float cd = kScalePoly * p.a;
-      for (int c = half * 64; c < min(m16, half * 64 + 64); c += 16) {
+      for (int c = part * kWarpCols; c < min(m16, (part + 1) * kWarpCols); c += 16) {
         uint32_t r[16];
         ptx::tmem_ld16(tq + c, r);
         ptx::tmem_wait_ld();
@@ -352,26 +393,25 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
     // ----------------------------------------------------- X <- P X
     publish();
     if (warp == 0) {
-      if (lane == 0) {
-        for (int n0 = 0; n0 < p.slice; n0 += 256) {
-          const uint32_t nn = static_cast<uint32_t>(min(256, p.slice - n0));
-          const uint32_t idesc = kF16Idesc | (1u << 16) | ((nn >> 3) << 17);  // B MN-major
-          for (int pass = 0; pass < (low ? 2 : 1); ++pass) {
-            const uint32_t xb = (pass ? part_at : x_at) + static_cast<uint32_t>(n0 / 64) * kTile;
-            for (int k = 0; k < m16 / 16; ++k) {
-              const uint32_t at = p_at + static_cast<uint32_t>(k >> 2) * kTile + (k & 3) * 32;
+      for (int n0 = 0; n0 < p.slice; n0 += 256) {
+        const uint32_t nn = static_cast<uint32_t>(min(256, p.slice - n0));
+        const uint32_t idesc = kF16Idesc | (1u << 16) | ((nn >> 3) << 17);  // B MN-major
+        for (int pass = 0; pass < (low ? 2 : 1); ++pass) {
+          const uint32_t xb = (pass ? part_at : x_at) + static_cast<uint32_t>(n0 / 64) * kTile;
+          for (int k = 0; k < m16 / 16; ++k) {
+            const uint32_t at = p_at + static_cast<uint32_t>(k >> 2) * kTile + (k & 3) * 32;
+            if (elected)
               ptx::mma_bf16(tmem + kTmemStep + n0, ptx::sdesc_sw128(at), desc_mn(xb + k * 2048),
                             idesc, (pass | k) ? 1u : 0u);
-            }
           }
         }
-        ptx::mma_commit(bar);
       }
+      if (elected) ptx::mma_commit(bar);
       __syncwarp();
     }
     finish();
     const float x_scale = (last ? 1.f : kScaleX) / kScalePoly * (t == 0 ? inv : 1.f / kScaleX);
-    for (int c = half * 16; c < p.slice; c += 32) {
+    for (int c = part * 16; c < p.slice; c += kThreads / 128 * 16) {
       uint32_t r[16];
       ptx::tmem_ld16(tq + kTmemStep + c, r);
       ptx::tmem_wait_ld();

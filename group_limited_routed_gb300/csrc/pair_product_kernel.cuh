@@ -116,13 +116,6 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
   return d;
 }
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok));
-  return ok != 0;
-}
 // Arrive on either CTA's barrier without a release.  It frees TMEM columns
 // whose loads have completed (tcgen05.wait::ld): no memory is handed over,
 // and a release would wait for the warp's earlier global stores.
@@ -499,7 +492,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // one elected lane arms the barriers and issues the copies.
     {
       const uint64_t pol = ptx::policy_evict_normal();
-      const bool elected = elect_one();
+      const bool elected = ptx::elect_one();
       uint32_t used = 0, parities = 0;  // bit s: stage s was filled, its last phase
       int stage = 0;
       uint32_t phase = 0;
@@ -613,7 +606,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const uint64_t b_desc0 =
           B_MN ? sdesc_mn_sw128(ring + kPABytes) : ptx::sdesc_sw128(ring + kPABytes);
       constexpr uint32_t A_STEP = (A_MN ? 2048 : 32) >> 4, B_STEP = (B_MN ? 2048 : 32) >> 4;
-      const bool elected = elect_one();
+      const bool elected = ptx::elect_one();
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
