@@ -177,6 +177,10 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
     ptx::tmem_relinquish();
   }
 
+  // the kernel before this one on the stream has written all it writes
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+
   // ------------------------------------------- the largest magnitude
   constexpr int kItems = 128 * (TYPE == kF32 ? 256 : kSliceMax) / 8 / kThreads;
   const bool vector_in = TYPE != kF32 && p.sc == 1 && p.sr % 8 == 0 && p.sz % 8 == 0 &&
@@ -473,18 +477,20 @@ cudaError_t launch_typed(const OrthoSmallArgs& p, int32_t batch, cudaStream_t s)
   constexpr auto kern = ortho_small_kernel<TYPE>;
   const cudaError_t err = smem_limit_once<kern>(static_cast<int>(kSmem));
   if (err != cudaSuccess) return err;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(p.cluster);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = kProgrammaticLaunch;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(batch * p.cluster));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 

@@ -26,7 +26,7 @@ int resident_clusters_once(const cudaLaunchConfig_t& cfg) {
 
 template <int NT, bool A_MN, bool B_MN, int KIND, bool WIDE, bool DUAL = false>
 cudaError_t launch_impl(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out,
-                        const ProductArgs& p, int64_t max_tiles, bool dependent, cudaStream_t s) {
+                        const ProductArgs& p, int64_t max_tiles, cudaStream_t s) {
   using C = ProductCfg<NT, KIND, WIDE, DUAL>;
   constexpr auto kern = pair_product_kernel<NT, A_MN, B_MN, KIND, WIDE, DUAL>;
   const cudaError_t err = smem_limit_once<kern>(static_cast<int>(C::SMEM_BYTES));
@@ -49,57 +49,56 @@ cudaError_t launch_impl(const CUtensorMap& a, const CUtensorMap& b, const CUtens
   if (resident <= 0) return cudaErrorUnknown;
   const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(resident, max_tiles));
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-  cfg.numAttrs = dependent ? 2 : 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, a, b, out, p);
 }
 
 template <int NT>
 cudaError_t launch_rows(bool a_mn, const CUtensorMap& a, const CUtensorMap& b,
-                        const CUtensorMap& out, const ProductArgs& p, int64_t tiles, bool dep,
-                        cudaStream_t s) {
+                        const CUtensorMap& out, const ProductArgs& p, int64_t tiles, cudaStream_t s) {
   const bool wide = p.out_type == kF32;
   if (a_mn)
-    return wide ? launch_impl<NT, true, false, kProductRows, true>(a, b, out, p, tiles, dep, s)
-                : launch_impl<NT, true, false, kProductRows, false>(a, b, out, p, tiles, dep, s);
-  return wide ? launch_impl<NT, false, false, kProductRows, true>(a, b, out, p, tiles, dep, s)
-              : launch_impl<NT, false, false, kProductRows, false>(a, b, out, p, tiles, dep, s);
+    return wide ? launch_impl<NT, true, false, kProductRows, true>(a, b, out, p, tiles, s)
+                : launch_impl<NT, true, false, kProductRows, false>(a, b, out, p, tiles, s);
+  return wide ? launch_impl<NT, false, false, kProductRows, true>(a, b, out, p, tiles, s)
+              : launch_impl<NT, false, false, kProductRows, false>(a, b, out, p, tiles, s);
 }
 
 }  // namespace
 
 cudaError_t launch_pair_product(int kind, int nt, bool a_mn, bool b_mn, const CUtensorMap& a,
                                 const CUtensorMap& b, const CUtensorMap& out,
-                                const ProductArgs& p, bool dependent, cudaStream_t s) {
+                                const ProductArgs& p, cudaStream_t s) {
   const int64_t mt = (p.M + kProductTileM - 1) / kProductTileM;
   if (kind == kProductRows && !b_mn) {
     // at most one ragged block more than rows / nt per group that has rows
     const int64_t tiles = mt * (p.rows / nt + std::min(p.groups, p.rows));
     switch (nt) {
-      case 32: return launch_rows<32>(a_mn, a, b, out, p, tiles, dependent, s);
-      case 64: return launch_rows<64>(a_mn, a, b, out, p, tiles, dependent, s);
-      case 128: return launch_rows<128>(a_mn, a, b, out, p, tiles, dependent, s);
-      case 256: return launch_rows<256>(a_mn, a, b, out, p, tiles, dependent, s);
+      case 32: return launch_rows<32>(a_mn, a, b, out, p, tiles, s);
+      case 64: return launch_rows<64>(a_mn, a, b, out, p, tiles, s);
+      case 128: return launch_rows<128>(a_mn, a, b, out, p, tiles, s);
+      case 256: return launch_rows<256>(a_mn, a, b, out, p, tiles, s);
     }
     return cudaErrorInvalidValue;
   }
   const int64_t tiles = mt * ((p.N + nt - 1) / nt) * p.groups;
   if (kind == kProductGroups && a_mn && b_mn && nt == 256)
     return p.out_type == kF32
-               ? launch_impl<256, true, true, kProductGroups, true>(a, b, out, p, tiles, dependent, s)
-               : launch_impl<256, true, true, kProductGroups, false, true>(a, b, out, p, tiles, dependent, s);
+               ? launch_impl<256, true, true, kProductGroups, true>(a, b, out, p, tiles, s)
+               : launch_impl<256, true, true, kProductGroups, false, true>(a, b, out, p, tiles, s);
   if (kind == kProductDense && p.out_type != kF32) {
     if (!a_mn && !b_mn && nt == 256)
-      return launch_impl<256, false, false, kProductDense, false>(a, b, out, p, tiles, dependent, s);
+      return launch_impl<256, false, false, kProductDense, false>(a, b, out, p, tiles, s);
     if (!a_mn && !b_mn && nt == 64)
-      return launch_impl<64, false, false, kProductDense, false>(a, b, out, p, tiles, dependent, s);
+      return launch_impl<64, false, false, kProductDense, false>(a, b, out, p, tiles, s);
     if (a_mn && !b_mn && nt == 256)
-      return launch_impl<256, true, false, kProductDense, false>(a, b, out, p, tiles, dependent, s);
+      return launch_impl<256, true, false, kProductDense, false>(a, b, out, p, tiles, s);
     if (a_mn && !b_mn && nt == 64)
-      return launch_impl<64, true, false, kProductDense, false>(a, b, out, p, tiles, dependent, s);
+      return launch_impl<64, true, false, kProductDense, false>(a, b, out, p, tiles, s);
     if (a_mn && b_mn && nt == 256)
-      return launch_impl<256, true, true, kProductDense, false>(a, b, out, p, tiles, dependent, s);
+      return launch_impl<256, true, true, kProductDense, false>(a, b, out, p, tiles, s);
     if (a_mn && b_mn && nt == 128)
-      return launch_impl<128, true, true, kProductDense, false>(a, b, out, p, tiles, dependent, s);
+      return launch_impl<128, true, true, kProductDense, false>(a, b, out, p, tiles, s);
   }
   return cudaErrorInvalidValue;
 }

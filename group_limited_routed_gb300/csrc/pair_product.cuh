@@ -65,6 +65,6 @@ inline int product_box_rows(int nt) { return nt / 2 < kProductBoxRows ? nt / 2 :
 // without swizzle, boxes 32 x 16 (FP32) or 32 x 32 (16-bit).
 cudaError_t launch_pair_product(int kind, int nt, bool a_mn, bool b_mn, const CUtensorMap& a,
                                 const CUtensorMap& b, const CUtensorMap& out,
-                                const ProductArgs& p, bool dependent, cudaStream_t s);
+                                const ProductArgs& p, cudaStream_t s);
 
 }  // namespace beam

@@ -98,7 +98,7 @@ struct Operand {
   size_t packed_bytes() const {
     return align_up(static_cast<size_t>(z) * outer * round_up(inner, 8) * 2);
   }
-  void pack_into(void* dst, cudaStream_t s) {
+  cudaError_t pack_into(void* dst, cudaStream_t s) {
     beam::PackArgs p;
     p.src = static_cast<const uint16_t*>(base);
     p.sz = zs;
@@ -108,10 +108,11 @@ struct Operand {
     p.cols = static_cast<int32_t>(inner);
     p.ld = static_cast<int32_t>(round_up(inner, 8));
     p.dst = static_cast<uint16_t*>(dst);
-    beam::launch_pack(p, s);
+    const cudaError_t e = beam::launch_pack(p, s);
     base = dst;
     ld = p.ld;
     zs = ld * outer;
+    return e;
   }
 };
 
@@ -182,8 +183,10 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   const beam_status_t st = device_ready(&dev);
   if (st != BEAM_OK) return st;
   if (!beam::host::encoder()) return BEAM_ERR_CUDA;
-  if (pack_a) a.pack_into(static_cast<uint8_t*>(ws) + at_a, s);
-  if (pack_b) b.pack_into(static_cast<uint8_t*>(ws) + at_b, s);
+  if (pack_a && a.pack_into(static_cast<uint8_t*>(ws) + at_a, s) != cudaSuccess)
+    return BEAM_ERR_CUDA;
+  if (pack_b && b.pack_into(static_cast<uint8_t*>(ws) + at_b, s) != cudaSuccess)
+    return BEAM_ERR_CUDA;
   CUtensorMap ta, tb;
   if (!tmap3(&ta, a.base, g.dtype, a.inner, a.outer, a.z, a.ld, a.zs, a_mn ? 64 : 128) ||
       !tmap3(&tb, b.base, g.dtype, b.inner, b.outer, b.z, b.ld, b.zs, b_mn ? 64 : beam::product_box_rows(nt)))
@@ -209,7 +212,7 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   CUtensorMap to = {};
   p.staged = staged_out(&to, out, g.out_dtype, M, N, kind == beam::kProductGroups ? g.n_groups : 1,
                         ld_out, z_out);
-  return launched(beam::launch_pair_product(kind, nt, a_mn, b_mn, ta, tb, to, p, false, s));
+  return launched(beam::launch_pair_product(kind, nt, a_mn, b_mn, ta, tb, to, p, s));
 }
 
 // ------------------------------------------------------ orthogonalised update
@@ -341,8 +344,7 @@ beam_status_t beam_moe_swiglu(const beam_moe_gate_t* d, const void* gate, const 
   p.rows = d->rows;
   p.F = d->F;
   p.type = d->dtype;
-  beam::launch_gate(p, dev.sms, static_cast<cudaStream_t>(stream));
-  return launched(cudaGetLastError());
+  return launched(beam::launch_gate(p, dev.sms, static_cast<cudaStream_t>(stream)));
 }
 
 beam_status_t beam_moe_swiglu_grad(const beam_moe_gate_t* d, const void* dh, int64_t dh_ld,
@@ -376,8 +378,7 @@ beam_status_t beam_moe_swiglu_grad(const beam_moe_gate_t* d, const void* dh, int
   p.rows = d->rows;
   p.F = d->F;
   p.type = d->dtype;
-  beam::launch_gate_grad(p, dev.sms, s);
-  return launched(cudaGetLastError());
+  return launched(beam::launch_gate_grad(p, dev.sms, s));
 }
 
 size_t beam_moe_orthogonalize_workspace_size(int32_t batch, int32_t rows, int32_t cols,
@@ -517,7 +518,7 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
     g.alpha = t == 0 ? 1.f : kScaleGram / (kScaleX * kScaleX);
     g.alpha_z = t == 0 ? n.alpha_gram : nullptr;
     cudaError_t e = beam::launch_pair_product(beam::kProductDense, nt_gram, !wide, !wide, ga[cur],
-                                              gb[cur], none, g, true, s);
+                                              gb[cur], none, g, s);
     if (e != cudaSuccess) return BEAM_ERR_CUDA;
 
     ProductArgs q = base;  // P = a I + b A + c A A
@@ -532,7 +533,7 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
     q.beta = kScalePoly * d->b / kScaleGram;
     q.diag = kScalePoly * d->a;
     q.add = gram;
-    e = beam::launch_pair_product(beam::kProductDense, nt_poly, false, false, pa, pb, none, q, true, s);
+    e = beam::launch_pair_product(beam::kProductDense, nt_poly, false, false, pa, pb, none, q, s);
     if (e != cudaSuccess) return BEAM_ERR_CUDA;
 
     ProductArgs u = base;  // X <- P X (wide) or X P (tall)
@@ -552,9 +553,9 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
     u.alpha = t == 0 ? 1.f : out_scale / (kScalePoly * kScaleX);
     u.alpha_z = t == 0 ? n.alpha_step : nullptr;
     e = wide ? beam::launch_pair_product(beam::kProductDense, nt_step, true, false, sx[cur], sp, none,
-                                         u, true, s)
+                                         u, s)
              : beam::launch_pair_product(beam::kProductDense, nt_step, false, false, sp, sx[cur],
-                                         none, u, true, s);
+                                         none, u, s);
     if (e != cudaSuccess) return BEAM_ERR_CUDA;
   }
   return BEAM_OK;

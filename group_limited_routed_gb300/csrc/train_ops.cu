@@ -38,6 +38,8 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // element where it starts on an odd one.  Memory bound: 2 bytes read, 2
 // written per element.
 __global__ void __launch_bounds__(256) pack_kernel(const PackArgs p) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
   const int64_t rows = p.zs * p.rows;
   const int lane = threadIdx.x & 31;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < rows;
@@ -107,6 +109,8 @@ __device__ __forceinline__ void store8(uint16_t* p, int n, const uint32_t (&v)[4
 
 template <bool F16, bool VEC>
 __global__ void __launch_bounds__(256) gate_kernel(const GateArgs p) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
   const int per_row = (p.F + 7) / 8;
   const int64_t n = p.rows * per_row;
   for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < n;
@@ -138,6 +142,8 @@ __global__ void __launch_bounds__(256) gate_kernel(const GateArgs p) {
 // warp when the rows alone fill the GPU, else the whole block.
 template <bool F16, bool VEC, int TPR>
 __global__ void __launch_bounds__(256) gate_grad_kernel(const GateArgs p) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
   constexpr int ROWS = 256 / TPR;
   __shared__ float part[8];
   const int t = threadIdx.x % TPR;
@@ -253,6 +259,8 @@ __device__ __forceinline__ void load_row8(const NormArgs& p, int64_t base, int c
 // First pass: each block's largest magnitude and sum of squares, in one read.
 template <int TYPE, bool VEC>
 __global__ void __launch_bounds__(256) amax_kernel(const NormArgs p) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
   __shared__ uint32_t s[8];
   __shared__ int se[8];
   __shared__ float sf[8];
@@ -292,6 +300,8 @@ __global__ void __launch_bounds__(256) amax_kernel(const NormArgs p) {
 // eps both in the copy's scale.
 template <int TYPE, bool VEC>
 __global__ void __launch_bounds__(256) scale_kernel(const NormArgs p) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
   __shared__ uint32_t s[8];
   const int z = blockIdx.y;
   const uint32_t amax = block_max(
@@ -329,9 +339,9 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormArgs p) {
 template <int TYPE, bool VEC>
 cudaError_t norm_impl(const NormArgs& p, cudaStream_t s) {
   const dim3 grid(p.blocks, p.batch);
-  amax_kernel<TYPE, VEC><<<grid, 256, 0, s>>>(p);
-  scale_kernel<TYPE, VEC><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  const cudaError_t e = launch_dependent(amax_kernel<TYPE, VEC>, grid, dim3(256), 0, s, p);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(scale_kernel<TYPE, VEC>, grid, dim3(256), 0, s, p);
 }
 
 // Rows of 16-byte words: contiguous, aligned, and no word crosses a row's end
@@ -349,42 +359,44 @@ cudaError_t norm_typed(const NormArgs& p, cudaStream_t s) {
 
 }  // namespace
 
-void launch_pack(const PackArgs& p, cudaStream_t s) {
+cudaError_t launch_pack(const PackArgs& p, cudaStream_t s) {
   const int64_t blocks = std::min<int64_t>((p.zs * p.rows + 7) / 8, 1 << 20);
-  if (blocks > 0) pack_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(p);
+  if (blocks == 0) return cudaSuccess;
+  return launch_dependent(pack_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, p);
 }
 
-void launch_gate(const GateArgs& p, int num_sms, cudaStream_t s) {
+cudaError_t launch_gate(const GateArgs& p, int num_sms, cudaStream_t s) {
   const int64_t n = p.rows * ((p.F + 7) / 8);
-  const unsigned blocks =
-      static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, static_cast<int64_t>(num_sms) * 32));
+  const dim3 grid(static_cast<unsigned>(
+      std::min<int64_t>((n + 255) / 256, static_cast<int64_t>(num_sms) * 32)));
   const bool vec = gate_aligned(p, false);
   if (p.type == kF16)
-    vec ? gate_kernel<true, true><<<blocks, 256, 0, s>>>(p)
-        : gate_kernel<true, false><<<blocks, 256, 0, s>>>(p);
-  else
-    vec ? gate_kernel<false, true><<<blocks, 256, 0, s>>>(p)
-        : gate_kernel<false, false><<<blocks, 256, 0, s>>>(p);
+    return vec ? launch_dependent(gate_kernel<true, true>, grid, dim3(256), 0, s, p)
+               : launch_dependent(gate_kernel<true, false>, grid, dim3(256), 0, s, p);
+  return vec ? launch_dependent(gate_kernel<false, true>, grid, dim3(256), 0, s, p)
+             : launch_dependent(gate_kernel<false, false>, grid, dim3(256), 0, s, p);
 }
 
 template <bool F16, bool VEC>
-static void gate_grad_impl(const GateArgs& p, int num_sms, cudaStream_t s) {
+static cudaError_t gate_grad_impl(const GateArgs& p, int num_sms, cudaStream_t s) {
   // a warp per row from as many rows as the GPU holds warps of this kernel
   // at once; below, a block per row shortens the row's chain of loads
   if (p.rows >= static_cast<int64_t>(num_sms) * 16) {
     const int64_t blocks = std::min<int64_t>((p.rows + 7) / 8, static_cast<int64_t>(num_sms) * 32);
-    gate_grad_kernel<F16, VEC, 32><<<static_cast<unsigned>(blocks), 256, 0, s>>>(p);
-  } else {
-    gate_grad_kernel<F16, VEC, 256><<<static_cast<unsigned>(p.rows), 256, 0, s>>>(p);
+    return launch_dependent(gate_grad_kernel<F16, VEC, 32>, dim3(static_cast<unsigned>(blocks)),
+                            dim3(256), 0, s, p);
   }
+  return launch_dependent(gate_grad_kernel<F16, VEC, 256>, dim3(static_cast<unsigned>(p.rows)),
+                          dim3(256), 0, s, p);
 }
 
-void launch_gate_grad(const GateArgs& p, int num_sms, cudaStream_t s) {
+cudaError_t launch_gate_grad(const GateArgs& p, int num_sms, cudaStream_t s) {
   const bool vec = gate_aligned(p, true);
   if (p.type == kF16)
-    vec ? gate_grad_impl<true, true>(p, num_sms, s) : gate_grad_impl<true, false>(p, num_sms, s);
-  else
-    vec ? gate_grad_impl<false, true>(p, num_sms, s) : gate_grad_impl<false, false>(p, num_sms, s);
+    return vec ? gate_grad_impl<true, true>(p, num_sms, s)
+               : gate_grad_impl<true, false>(p, num_sms, s);
+  return vec ? gate_grad_impl<false, true>(p, num_sms, s)
+             : gate_grad_impl<false, false>(p, num_sms, s);
 }
 
 cudaError_t launch_norm(const NormArgs& p, cudaStream_t s) {

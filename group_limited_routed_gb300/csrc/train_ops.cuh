@@ -1,4 +1,7 @@
 // Launchers of the training operators' memory-bound kernels (train_ops.cu).
+// Like all kernels of these operators they are launched with programmatic
+// stream serialization, the first of a call included: each waits for the
+// kernel before it on the stream before it touches memory.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -18,7 +21,7 @@ struct PackArgs {
   int32_t cols, ld;
   uint16_t* dst;
 };
-void launch_pack(const PackArgs& p, cudaStream_t s);
+cudaError_t launch_pack(const PackArgs& p, cudaStream_t s);
 
 // -------------------------------------------------------------- gated rows
 struct GateArgs {
@@ -35,8 +38,8 @@ struct GateArgs {
   int32_t F;
   int32_t type;            // kBf16 or kF16
 };
-void launch_gate(const GateArgs& p, int num_sms, cudaStream_t s);
-void launch_gate_grad(const GateArgs& p, int num_sms, cudaStream_t s);
+cudaError_t launch_gate(const GateArgs& p, int num_sms, cudaStream_t s);
+cudaError_t launch_gate_grad(const GateArgs& p, int num_sms, cudaStream_t s);
 
 // ------------------------------------------------------ orthogonalised update
 constexpr int kNormBlocks = 256;  // partial sums per matrix, at most
