@@ -98,7 +98,7 @@ struct Operand {
   size_t packed_bytes() const {
     return align_up(static_cast<size_t>(z) * outer * round_up(inner, 8) * 2);
   }
-  cudaError_t pack_into(void* dst, cudaStream_t s) {
+  cudaError_t pack_into(void* dst, const int32_t* offsets, cudaStream_t s) {
     beam::PackArgs p;
     p.src = static_cast<const uint16_t*>(base);
     p.sz = zs;
@@ -108,6 +108,7 @@ struct Operand {
     p.cols = static_cast<int32_t>(inner);
     p.ld = static_cast<int32_t>(round_up(inner, 8));
     p.dst = static_cast<uint16_t*>(dst);
+    p.offsets = z > 1 ? offsets : nullptr;  // a stack: one matrix per group
     const cudaError_t e = beam::launch_pack(p, s);
     base = dst;
     ld = p.ld;
@@ -183,9 +184,9 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   const beam_status_t st = device_ready(&dev);
   if (st != BEAM_OK) return st;
   if (!beam::host::encoder()) return BEAM_ERR_CUDA;
-  if (pack_a && a.pack_into(static_cast<uint8_t*>(ws) + at_a, s) != cudaSuccess)
+  if (pack_a && a.pack_into(static_cast<uint8_t*>(ws) + at_a, offsets, s) != cudaSuccess)
     return BEAM_ERR_CUDA;
-  if (pack_b && b.pack_into(static_cast<uint8_t*>(ws) + at_b, s) != cudaSuccess)
+  if (pack_b && b.pack_into(static_cast<uint8_t*>(ws) + at_b, offsets, s) != cudaSuccess)
     return BEAM_ERR_CUDA;
   CUtensorMap ta, tb;
   if (!tmap3(&ta, a.base, g.dtype, a.inner, a.outer, a.z, a.ld, a.zs, a_mn ? 64 : 128) ||
@@ -210,8 +211,10 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   p.status = static_cast<uint32_t*>(ws);
   p.wait_limit_ns = beam::host::wait_limit_ns();
   CUtensorMap to = {};
-  p.staged = staged_out(&to, out, g.out_dtype, M, N, kind == beam::kProductGroups ? g.n_groups : 1,
-                        ld_out, z_out);
+  // 16-bit rows leave straight from registers
+  if (kind == beam::kProductGroups || g.out_dtype == BEAM_DTYPE_F32)
+    p.staged = staged_out(&to, out, g.out_dtype, M, N,
+                          kind == beam::kProductGroups ? g.n_groups : 1, ld_out, z_out);
   return launched(beam::launch_pair_product(kind, nt, a_mn, b_mn, ta, tb, to, p, s));
 }
 
@@ -253,6 +256,12 @@ bool ortho_layout(int32_t batch, int32_t rows, int32_t cols, int32_t dtype, Orth
   L->total = off;
   return true;
 }
+
+// Time of a tile of 256 columns by nt rows, for choosing nt: per 64-wide k
+// block (the MMAs of 256 rows, else the loads of A and of the rows), and once
+// (start-up, epilogue).  Measured on stacks of products of m = 777 and 2560.
+double dense_block_us(int nt) { return nt == 64 ? 0.22 : nt == 128 ? 0.25 : 0.36; }
+double dense_tile_us(int nt) { return 4.0 + nt / 128.0; }
 
 template <typename T>
 T* at(void* ws, size_t off) {
@@ -473,14 +482,26 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
   n.eps = d->eps;
   if (beam::launch_norm(n, s) != cudaSuccess) return BEAM_ERR_CUDA;
 
-  // rows j per tile: narrow tiles where wide ones would leave SMs idle
-  const int64_t sms2 = dev.sms / 2;
-  auto tiles = [&](int64_t cols_, int64_t rows_, int nt) {
-    return batch * ((cols_ + 255) / 256) * ((rows_ + nt - 1) / nt);
+  const int64_t pairs = dev.sms / 2;
+  // the symmetric products compute the tiles with j >= i only
+  auto tiles = [&](int64_t cols, int64_t rows, int nt, bool symmetric) {
+    const int64_t mt = (cols + 255) / 256, rt = (rows + nt - 1) / nt;
+    return batch * (mt * rt - (symmetric ? 256 / nt * (mt * (mt - 1) / 2) : 0));
   };
-  const int nt_gram = tiles(m, m, 256) / 2 >= sms2 ? 256 : wide ? 64 : 128;
-  const int nt_poly = tiles(m, m, 256) / 2 >= sms2 ? 256 : 64;
-  const int nt_step = tiles(C, R, 256) >= sms2 ? 256 : 64;
+  auto tile_rows = [&](int64_t cols, int64_t rows, int64_t k, bool symmetric, int least) {
+    int best = 256;
+    double best_us = 1e30;
+    for (int nt = least; nt <= 256; nt *= 2) {
+      const double waves = static_cast<double>((tiles(cols, rows, nt, symmetric) + pairs - 1) / pairs);
+      const double us = waves * ((k + 63) / 64 * dense_block_us(nt) + dense_tile_us(nt));
+      if (us < best_us) best = nt, best_us = us;
+    }
+    return best;
+  };
+  // (MN-major rows come in atoms of 64: a pair's tile has at least 128)
+  const int nt_gram = tile_rows(m, m, std::max(R, C), true, wide ? 64 : 128);
+  const int nt_poly = tile_rows(m, m, m, true, 64);
+  const int nt_step = tile_rows(C, R, m, false, 64);
 
   const int32_t F16 = BEAM_DTYPE_F16;
   CUtensorMap ga[2], gb[2], pa, pb, sx[2], sp;  // gram, polynomial, step

@@ -31,47 +31,59 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 
 // ------------------------------------------------------------ aligned copies
-// A warp takes a row, a lane 8 elements of the destination at a time: the
-// store is one 16-byte word.  The source row starts anywhere (element
+// A warp takes 512 elements of a row of the destination, a lane 8 at a time:
+// the store is one 16-byte word.  The source row starts anywhere (element
 // aligned), so it is read in 4-byte words from the 4-byte boundary at or
 // before it -- five words hold the eight elements -- and shifted by one
-// element where it starts on an odd one.  Memory bound: 2 bytes read, 2
-// written per element.
+// element where it starts on an odd one.  Matrices of groups without rows are
+// left out.  Memory bound: 2 bytes read, 2 written per element.
+constexpr int kPackSpan = 512;
+
 __global__ void __launch_bounds__(256) pack_kernel(const PackArgs p) {
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
   const int64_t rows = p.zs * p.rows;
   const int lane = threadIdx.x & 31;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < rows;
-       row += static_cast<int64_t>(gridDim.x) * 8) {
+  const int spans = (p.ld + kPackSpan - 1) / kPackSpan;
+  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+       unit < rows * spans; unit += static_cast<int64_t>(gridDim.x) * 8) {
+    const int64_t row = unit / spans;
+    const int first = static_cast<int>(unit - row * spans) * kPackSpan;
     const int64_t z = row / p.rows;
+    if (p.offsets && p.offsets[z + 1] <= p.offsets[z]) continue;
     const uint16_t* src = p.src + z * p.sz + (row - z * p.rows) * p.sr;
     const bool odd = (reinterpret_cast<uintptr_t>(src) & 2u) != 0;
     // words[k] holds elements 2k - odd and 2k + 1 - odd of the row
     const uint32_t* words = reinterpret_cast<const uint32_t*>(src - (odd ? 1 : 0));
     const int whole = (p.cols + (odd ? 1 : 0)) / 2;  // words wholly at or before the row's end
     uint16_t* dst = p.dst + row * p.ld;
-    for (int c = lane * 8; c < p.ld; c += 256) {
-      uint32_t w[5];
+    uint32_t w[kPackSpan / 256][5];
+#pragma unroll
+    for (int h = 0; h < kPackSpan / 256; ++h) {
 #pragma unroll
       for (int k = 0; k < 5; ++k) {
-        const int at = c / 2 + k;
+        const int at = (first + h * 256) / 2 + lane * 4 + k;
         // the first word of an odd row begins one element before it, the
         // last word may end one after it: those are read by the element
-        w[k] = 0u;
+        w[h][k] = 0u;
         if (at < whole && !(odd && at == 0)) {
-          w[k] = words[at];
+          w[h][k] = words[at];
         } else {
           const int e = 2 * at - (odd ? 1 : 0);
-          if (e >= 0 && e < p.cols) w[k] = src[e];
-          if (e + 1 >= 0 && e + 1 < p.cols) w[k] |= static_cast<uint32_t>(src[e + 1]) << 16;
+          if (e >= 0 && e < p.cols) w[h][k] = src[e];
+          if (e + 1 >= 0 && e + 1 < p.cols) w[h][k] |= static_cast<uint32_t>(src[e + 1]) << 16;
         }
       }
+    }
+#pragma unroll
+    for (int h = 0; h < kPackSpan / 256; ++h) {
+      const int c = first + h * 256 + lane * 8;
+      if (c >= p.ld) continue;
       uint4 v;
-      v.x = odd ? __funnelshift_r(w[0], w[1], 16) : w[0];
-      v.y = odd ? __funnelshift_r(w[1], w[2], 16) : w[1];
-      v.z = odd ? __funnelshift_r(w[2], w[3], 16) : w[2];
-      v.w = odd ? __funnelshift_r(w[3], w[4], 16) : w[3];
+      v.x = odd ? __funnelshift_r(w[h][0], w[h][1], 16) : w[h][0];
+      v.y = odd ? __funnelshift_r(w[h][1], w[h][2], 16) : w[h][1];
+      v.z = odd ? __funnelshift_r(w[h][2], w[h][3], 16) : w[h][2];
+      v.w = odd ? __funnelshift_r(w[h][3], w[h][4], 16) : w[h][3];
       *reinterpret_cast<uint4*>(dst + c) = v;
     }
   }
@@ -360,7 +372,8 @@ cudaError_t norm_typed(const NormArgs& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_pack(const PackArgs& p, cudaStream_t s) {
-  const int64_t blocks = std::min<int64_t>((p.zs * p.rows + 7) / 8, 1 << 20);
+  const int64_t units = p.zs * p.rows * ((p.ld + kPackSpan - 1) / kPackSpan);
+  const int64_t blocks = std::min<int64_t>((units + 7) / 8, 1 << 20);
   if (blocks == 0) return cudaSuccess;
   return launch_dependent(pack_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, p);
 }

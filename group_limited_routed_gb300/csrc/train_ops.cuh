@@ -20,6 +20,7 @@ struct PackArgs {
   int64_t zs, rows;
   int32_t cols, ld;
   uint16_t* dst;
+  const int32_t* offsets;  // or nullptr: z with offsets[z + 1] <= offsets[z] are not copied
 };
 cudaError_t launch_pack(const PackArgs& p, cudaStream_t s);
 
