@@ -830,7 +830,7 @@ _HERE_ALREADY = contextlib.nullcontext()
 
 def _current(device):
     """A context in which `device` is current (it usually is)."""
-    return _HERE_ALREADY if device.index == torch.cuda.current_device() \
+    return _HERE_ALREADY if device.index == torch._C._cuda_getDevice() \
         else torch.cuda.device(device)
 
 
@@ -1022,7 +1022,7 @@ def _gate_plan(gate, up, row_weight, dh, outs):
 
 
 def _like(t, stream):
-    out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    out = torch.empty_like(t, memory_format=torch.contiguous_format)
     if stream is not None:
         _temporary(out, stream)
     return out

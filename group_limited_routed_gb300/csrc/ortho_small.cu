@@ -26,6 +26,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <mutex>
 
 #include "common.cuh"
 #include "gemm_common.cuh"
@@ -494,6 +495,49 @@ cudaError_t launch_typed(const OrthoSmallArgs& p, int32_t batch, cudaStream_t s)
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// Whether the device runs the kernel in clusters of 16 (asked once per device
+// and kernel).
+template <int TYPE>
+bool large_clusters_once() {
+  constexpr auto kern = ortho_small_kernel<TYPE>;
+  static std::mutex mu;
+  static int known[kMaxDevices] = {};  // 0: not asked, 1: no, 2: yes
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  std::lock_guard<std::mutex> lock(mu);
+  if (known[dev] == 0) {
+    int n = 0;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kOrthoSmallCluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kOrthoSmallCluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const bool ok =
+        smem_limit_once<kern>(static_cast<int>(kSmem)) == cudaSuccess &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+            cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess && n > 0;
+    if (!ok) cudaGetLastError();  // a refusal is an answer, not an error of the call
+    known[dev] = ok ? 2 : 1;
+  }
+  return known[dev] == 2;
+}
+
+bool large_clusters(int32_t type) {
+  switch (type) {
+    case kBf16: return large_clusters_once<kBf16>();
+    case kF16: return large_clusters_once<kF16>();
+    case kF32: return large_clusters_once<kF32>();
+  }
+  return false;
+}
+
 }  // namespace
 
 bool ortho_small_shape(int32_t batch, int32_t m, int32_t n, int32_t type, int num_sms,
@@ -502,10 +546,12 @@ bool ortho_small_shape(int32_t batch, int32_t m, int32_t n, int32_t type, int nu
   const int32_t most = type == kF32 ? 256 : kSliceMax;
   const int32_t least = (n + most - 1) / most;  // CTAs
   if (least > kOrthoSmallCluster) return false;
+  // clusters of more than 8 CTAs depend on the device
+  if (least > 8 && !large_clusters(type)) return false;
   // more CTAs than needed while the stack leaves SMs free and a slice has
   // more than 64 columns
   int32_t c = least;
-  while (c < kOrthoSmallCluster && batch * (c + 1) <= num_sms && (n + c - 1) / c > 64) ++c;
+  while (c < 8 && batch * (c + 1) <= num_sms && (n + c - 1) / c > 64) ++c;
   *cluster = c;
   *slice = ((n + c - 1) / c + 63) / 64 * 64;
   // whole slices of 64 may need fewer CTAs than c

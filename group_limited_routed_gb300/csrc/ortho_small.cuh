@@ -24,7 +24,7 @@ struct OrthoSmallArgs {
 };
 
 constexpr int kOrthoSmallM = 128;        // smaller extent, at most
-constexpr int kOrthoSmallCluster = 8;    // CTAs per matrix, at most
+constexpr int kOrthoSmallCluster = 16;   // CTAs per matrix, at most (over 8 only where needed)
 
 // Columns per CTA and CTAs per matrix for a stack; false: too large.
 bool ortho_small_shape(int32_t batch, int32_t m, int32_t n, int32_t type, int num_sms,

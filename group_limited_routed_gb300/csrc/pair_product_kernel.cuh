@@ -71,7 +71,7 @@ constexpr uint32_t kStaging = kPEpiWarps * 2048;
 
 template <int NT, int KIND, bool WIDE, bool DUAL>
 struct ProductCfg {
-  static constexpr bool STAGED = KIND == kProductGroups || WIDE;
+  static constexpr bool STAGED = KIND != kProductRows || WIDE;
   static constexpr uint32_t B_BYTES = NT / 2 * 128;  // one block of rows
   static constexpr uint32_t STAGE = kPABytes + (DUAL ? 2 : 1) * B_BYTES;
   static constexpr int S_RAW = static_cast<int>((kPRing + (DUAL ? 8192 : 0) - (STAGED ? kStaging : 0)) / STAGE);
@@ -943,14 +943,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if (acc == 0) acc_phase ^= 1u;
           }
           const int64_t j = static_cast<int64_t>(t.j0) + col_begin;
-          if (KIND == kProductGroups && p.staged) {
+          if (C::STAGED && p.staged) {
+            constexpr int ROWS = COLS < 32 ? COLS : 32;  // rows of a piece
 #pragma unroll
-            for (int c = 0; c < COLS; c += 32) {
+            for (int c = 0; c < COLS; c += ROWS) {
               if (c < ncols) {
                 if (lane == 0) tma_store_read_done();
                 __syncwarp();
 #pragma unroll
-                for (int u = 0; u < 32; u += 2) {
+                for (int u = 0; u < ROWS; u += 2) {
                   const uint32_t v = swap_pair(packed[(c + u) / 2], lane);
                   asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage_at + (u + (lane & 1)) * 64 +
                                                                (lane & ~1) * 2),

@@ -53,7 +53,7 @@ bool tmap3(CUtensorMap* m, const void* base, int32_t type, int64_t inner, int64_
 // Map of a result [z][rows][cols] for bulk copies out of shared memory; false
 // where its address or strides are no multiples of 16 bytes.
 bool staged_out(CUtensorMap* m, void* out, int32_t type, int64_t cols, int64_t rows, int64_t z,
-                int64_t ld, int64_t zs) {
+                int64_t ld, int64_t zs, int nt) {
   const int64_t bytes = type == BEAM_DTYPE_F32 ? 4 : 2;
   if (z <= 1) zs = ld * rows;
   if ((reinterpret_cast<uintptr_t>(out) & 15u) || ld * bytes % 16 || zs * bytes % 16) return false;
@@ -61,7 +61,8 @@ bool staged_out(CUtensorMap* m, void* out, int32_t type, int64_t cols, int64_t r
                         static_cast<cuuint64_t>(z)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * bytes),
                            static_cast<cuuint64_t>(zs * bytes)};
-  cuuint32_t box[3] = {32, type == BEAM_DTYPE_F32 ? 16u : 32u, 1};
+  cuuint32_t box[3] = {
+      32, static_cast<cuuint32_t>(beam::product_out_rows(nt, type == BEAM_DTYPE_F32)), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType t = type == BEAM_DTYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                 : type == BEAM_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
@@ -214,7 +215,7 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   // 16-bit rows leave straight from registers
   if (kind == beam::kProductGroups || g.out_dtype == BEAM_DTYPE_F32)
     p.staged = staged_out(&to, out, g.out_dtype, M, N,
-                          kind == beam::kProductGroups ? g.n_groups : 1, ld_out, z_out);
+                          kind == beam::kProductGroups ? g.n_groups : 1, ld_out, z_out, nt);
   return launched(beam::launch_pair_product(kind, nt, a_mn, b_mn, ta, tb, to, p, s));
 }
 
@@ -524,7 +525,14 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
   base.out_type = F16;
   base.status = static_cast<uint32_t*>(workspace);
   base.wait_limit_ns = beam::host::wait_limit_ns();
-  const CUtensorMap none = {};
+  // results leave by bulk copy; the caller's `out` where its rows allow it
+  CUtensorMap og, op, ox[2], oo = {};
+  if (!staged_out(&og, gram, F16, m, m, batch, L.ldm, m * L.ldm, nt_gram) ||
+      !staged_out(&op, poly, F16, m, m, batch, L.ldm, m * L.ldm, nt_poly) ||
+      !staged_out(&ox[0], x[0], F16, C, R, batch, L.ld, R * L.ld, nt_step) ||
+      !staged_out(&ox[1], x[1], F16, C, R, batch, L.ld, R * L.ld, nt_step))
+    return BEAM_ERR_CUDA;
+  const bool out_staged = staged_out(&oo, out, d->out_dtype, C, R, batch, C, R * C, nt_step);
   for (int t = 0; t < d->steps; ++t) {
     const bool last = t + 1 == d->steps;
     const int cur = t & 1;
@@ -536,10 +544,11 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
     g.ld_out = L.ldm;
     g.z_out = m * L.ldm;
     g.symmetric = 1;
+    g.staged = 1;
     g.alpha = t == 0 ? 1.f : kScaleGram / (kScaleX * kScaleX);
     g.alpha_z = t == 0 ? n.alpha_gram : nullptr;
     cudaError_t e = beam::launch_pair_product(beam::kProductDense, nt_gram, !wide, !wide, ga[cur],
-                                              gb[cur], none, g, s);
+                                              gb[cur], og, g, s);
     if (e != cudaSuccess) return BEAM_ERR_CUDA;
 
     ProductArgs q = base;  // P = a I + b A + c A A
@@ -550,11 +559,12 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
     q.ld_out = L.ldm;
     q.z_out = m * L.ldm;
     q.symmetric = 1;
+    q.staged = 1;
     q.alpha = kScalePoly * d->c / (kScaleGram * kScaleGram);
     q.beta = kScalePoly * d->b / kScaleGram;
     q.diag = kScalePoly * d->a;
     q.add = gram;
-    e = beam::launch_pair_product(beam::kProductDense, nt_poly, false, false, pa, pb, none, q, s);
+    e = beam::launch_pair_product(beam::kProductDense, nt_poly, false, false, pa, pb, op, q, s);
     if (e != cudaSuccess) return BEAM_ERR_CUDA;
 
     ProductArgs u = base;  // X <- P X (wide) or X P (tall)
@@ -567,16 +577,17 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
       (wide ? u.wrap_za : u.wrap_zb) = d->batch;
     }
     u.out = last ? out : x[cur ^ 1];
+    u.staged = !last || out_staged ? 1 : 0;
     u.out_type = last ? d->out_dtype : F16;
     u.ld_out = last ? C : L.ld;
     u.z_out = last ? R * C : R * L.ld;
     const float out_scale = last ? 1.f : kScaleX;
     u.alpha = t == 0 ? 1.f : out_scale / (kScalePoly * kScaleX);
     u.alpha_z = t == 0 ? n.alpha_step : nullptr;
-    e = wide ? beam::launch_pair_product(beam::kProductDense, nt_step, true, false, sx[cur], sp, none,
-                                         u, s)
+    e = wide ? beam::launch_pair_product(beam::kProductDense, nt_step, true, false, sx[cur], sp,
+                                         last ? oo : ox[cur ^ 1], u, s)
              : beam::launch_pair_product(beam::kProductDense, nt_step, false, false, sp, sx[cur],
-                                         none, u, s);
+                                         last ? oo : ox[cur ^ 1], u, s);
     if (e != cudaSuccess) return BEAM_ERR_CUDA;
   }
   return BEAM_OK;
