@@ -1,0 +1,579 @@
+// The orthogonalised update of stacks of matrices: every product of every
+// step in one persistent launch.
+//
+// Per matrix and step, with X [rows, cols] and m = min(rows, cols):
+//   gram  A = X X^T (wide) or X^T X (tall)   symmetric, m x m
+//   poly  P = aI + bA + cA^2                 symmetric, m x m
+//   step  X <- P X (wide) or X P (tall)      rows x cols
+// Each is out[j, i] = sum_k A[i, k] B[j, k] in tiles of 256 columns i by NT
+// rows j on a CTA pair, the machinery of pair_product_kernel.cuh: M = 256
+// tcgen05 MMAs over both CTAs, one operand K-major or both, or MN-major where
+// the matrix is stored the other way round (X as operand i of a wide step, both
+// operands of a tall gram), so nothing is ever transposed in memory.  The two
+// symmetric products compute the tiles with j >= i and write their mirror
+// images too.
+//
+// As separate launches the 3 * steps products lost 5 to 50 microseconds each
+// to partly filled last waves, start-up and completion.  Here the tiles of
+// all products stand in one list -- step, product, matrix, tile -- and pair p
+// takes every num_pairs-th.  A tile may start when its matrix has finished
+// the product before: the epilogue warps count finished tiles per matrix
+// (release), producers wait for the count (acquire).  Counts only wait on
+// tiles earlier in the list and every pair works in list order, so with all
+// pairs resident (cooperative launch) some tile can always run.  With several
+// matrices the wait is over before it starts; with one it is a grid barrier.
+// Waits are bounded like all others.
+//
+// Between the products X, A and P are F16 (see beam_moe_orthogonalize).
+#include "ortho_chain.cuh"
+
+#include <algorithm>
+#include <mutex>
+
+#include "launch_once.cuh"
+#include "ortho_scale.cuh"
+#include "pair_common.cuh"
+#include "pair_product.cuh"
+
+namespace beam {
+namespace {
+
+template <int NT>
+struct ChainCfg {
+  static constexpr uint32_t B_BYTES = NT / 2 * 128;
+  static constexpr uint32_t STAGE = kPABytes + B_BYTES;
+  static constexpr int S = static_cast<int>((kPRing - kStaging) / STAGE);
+  static constexpr uint32_t TMEM_COLS = 2 * NT;
+  static constexpr uint32_t NUM_BARS = 2 * S + 6;
+  static constexpr uint32_t STAGING = S * STAGE;
+  static constexpr uint32_t BARS = STAGING + kStaging;
+  static constexpr uint32_t SMEM_BYTES = 1024 + BARS + NUM_BARS * 8 + 16;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+  static_assert(STAGE % 1024 == 0, "swizzle atoms are 1024-byte aligned");
+};
+
+enum : int { kGram = 0, kPoly = 1, kStep = 2 };
+
+struct ChainTile {
+  int t, product, z;     // step, kGram / kPoly / kStep, matrix
+  int i0, j0, nvalid, n_mma;
+  int columns;           // of the result
+  int k_blocks;
+  uint32_t after;        // finished half tiles of the matrix before this product
+};
+
+template <int NT>
+struct ChainWalk {
+  const OrthoChainArgs& p;
+  int tile, step, total;
+  int m_mt, m_nt, x_mt, x_nt;      // tiles along i and j of m x m and of X
+  int sym_z, step_z;               // tiles per matrix
+  static constexpr int R = kProductTileM / NT;
+
+  __device__ ChainWalk(const OrthoChainArgs& args, int first, int stride)
+      : p(args), tile(first), step(stride) {
+    m_mt = (p.m + kProductTileM - 1) / kProductTileM;
+    m_nt = (p.m + NT - 1) / NT;
+    x_mt = (p.cols + kProductTileM - 1) / kProductTileM;
+    x_nt = (p.rows + NT - 1) / NT;
+    sym_z = m_mt * m_nt - R * (m_mt * (m_mt - 1) / 2);
+    step_z = x_mt * x_nt;
+    total = p.steps * p.batch * (2 * sym_z + step_z);
+  }
+  __device__ bool done() const { return tile >= total; }
+  __device__ void next() { tile += step; }
+
+  __device__ ChainTile get() const {
+    ChainTile c;
+    const int per_step = p.batch * (2 * sym_z + step_z);
+    c.t = tile / per_step;
+    int left = tile - c.t * per_step;
+    c.product = left < p.batch * sym_z ? kGram : left < 2 * p.batch * sym_z ? kPoly : kStep;
+    left -= c.product * p.batch * sym_z;
+    int bi, bj;
+    uint32_t before = static_cast<uint32_t>(c.t) * (2 * sym_z + step_z) +
+                      static_cast<uint32_t>(c.product) * sym_z;
+    if (c.product == kStep) {
+      c.z = left / step_z;
+      left -= c.z * step_z;
+      bi = left / x_nt;
+      bj = left - bi * x_nt;
+      c.columns = p.cols;
+      c.nvalid = min(NT, p.rows - bj * NT);
+    } else {
+      c.z = left / sym_z;
+      left -= c.z * sym_z;
+      bi = 0;  // tiles with j >= i, in units of 256 columns and NT rows
+      while (left >= m_nt - bi * R) {
+        left -= m_nt - bi * R;
+        ++bi;
+      }
+      bj = bi * R + left;
+      c.columns = p.m;
+      c.nvalid = min(NT, p.m - bj * NT);
+    }
+    c.i0 = bi * kProductTileM;
+    c.j0 = bj * NT;
+    c.n_mma = (c.nvalid + 15) & ~15;
+    const int k = c.product == kGram ? max(p.rows, p.cols) : p.m;
+    c.k_blocks = (k + kPBK - 1) / kPBK;
+    // the first step of a 32-bit update adds the product with X's low parts
+    if (c.product == kStep && c.t == 0 && p.split) c.k_blocks *= 2;
+    c.after = before * 2;  // each CTA of the pair counts
+    return c;
+  }
+};
+
+// Wait until `count` half tiles of a matrix are finished; false as
+// Waiter::wait.  One lane of a warp looks, all learn.
+__device__ __forceinline__ bool wait_count(const Waiter& w, const uint32_t* done, uint32_t count) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) {
+    const uint64_t t0 = ptx::globaltimer();
+    for (uint32_t n = 1;; ++n) {
+      uint32_t v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(done) : "memory");
+      if (v >= count) break;
+      if ((n & 63u) == 0) {
+        if (*w.abort_flag) {
+          ok = false;
+          break;
+        }
+        if (ptx::globaltimer() - t0 > w.limit_ns) {
+          *w.abort_flag = 1;
+          latch_status(w.status, kStatusTimeout);
+          ok = false;
+          break;
+        }
+      }
+    }
+  }
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kPThreads, 1)
+    ortho_chain_kernel(const __grid_constant__ OrthoChainMaps maps, const OrthoChainArgs p) {
+  using C = ChainCfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = ptx::smem_addr(smem_raw);
+  const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t ring = raw_addr + pad;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::BARS);
+  int32_t* misc = reinterpret_cast<int32_t*>(bars + C::NUM_BARS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc);
+  volatile int32_t* abort_flag = misc + 1;
+
+  const uint32_t bar0 = ptx::smem_addr(bars);
+  auto full = [&](int s) { return bar0 + 8u * s; };
+  auto empty = [&](int s) { return bar0 + 8u * (C::S + s); };
+  auto tfull = [&](int a) { return bar0 + 8u * (2 * C::S + a); };
+  auto tempty = [&](int a) { return bar0 + 8u * (2 * C::S + 2 + a); };
+  const uint32_t done_bar = bar0 + 8u * (2 * C::S + 4);
+  const uint32_t stored = bar0 + 8u * (2 * C::S + 5);  // epilogue warps' parts of a tile
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+  const int num_pairs = static_cast<int>(gridDim.x >> 1);
+  const bool wide = p.rows <= p.cols;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::S; ++s) {
+      ptx::mbar_init(full(s), 1);  // the leader's producer; bytes of both CTAs
+      ptx::mbar_init(empty(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      ptx::mbar_init(tfull(a), 1);
+      ptx::mbar_init(tempty(a), 2 * kPEpiWarps);
+    }
+    ptx::mbar_init(done_bar, 1);
+    ptx::mbar_init(stored, kPEpiWarps);
+    *abort_flag = 0;
+    ptx::fence_barrier_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), C::TMEM_COLS);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const Waiter W{abort_flag, p.status, p.wait_limit_ns};
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- producer
+    const uint64_t pol = ptx::policy_evict_normal();
+    const bool elected = ptx::elect_one();
+    uint32_t used = 0, parities = 0;  // bit s: stage s was filled, its last phase
+    int seen_z = -1;
+    uint32_t seen_after = 0;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (ChainWalk<NT> walk(p, pair, num_pairs); ok && !walk.done(); walk.next()) {
+      const ChainTile t = walk.get();
+      const int cur = t.t & 1;
+      const CUtensorMap* ma;
+      const CUtensorMap* mb;
+      bool a_mn = false, b_mn = false;
+      if (t.product == kGram) {
+        ma = &maps.gram_a[cur];
+        mb = &maps.gram_b[cur];
+        a_mn = b_mn = !wide;
+      } else if (t.product == kPoly) {
+        ma = &maps.poly_a;
+        mb = &maps.poly_b;
+      } else {
+        ma = wide ? &maps.step_x[cur] : &maps.step_p;
+        mb = wide ? &maps.step_p : &maps.step_x[cur];
+        a_mn = wide;
+      }
+      const int i = t.i0 + static_cast<int>(rank) * 128;
+      const int j = t.j0 + static_cast<int>(rank) * (t.n_mma / 2);
+      const int boxes = (t.n_mma / 2 + kProductBoxRows - 1) / kProductBoxRows;
+      const uint32_t bytes =
+          kPABytes + (b_mn ? C::B_BYTES : static_cast<uint32_t>(boxes) * kProductBoxRows * 128u);
+      const int half = t.product == kStep && t.t == 0 && p.split ? t.k_blocks / 2 : t.k_blocks;
+      // the matrix's product before this one is in memory, and what generic
+      // stores of other SMs wrote of it is seen by this SM's bulk copies
+      // (asked once: the next tiles are mostly the same product's)
+      if (t.after != 0 && (t.z != seen_z || t.after != seen_after)) {
+        if (!wait_count(W, p.done + t.z, t.after)) break;
+        asm volatile("fence.proxy.async;" ::: "memory");
+        seen_z = t.z;
+        seen_after = t.after;
+      }
+      for (int kb = 0; kb < t.k_blocks; ++kb) {
+        if (!W.wait(empty(stage), phase ^ 1u)) {
+          ok = false;
+          break;
+        }
+        const bool low = kb >= half;
+        const int k = (low ? kb - half : kb) * kPBK;
+        const int zx = t.z + (low ? p.batch : 0);  // X's z; P has no low parts
+        const int za = t.product == kStep && !wide ? t.z : zx;
+        const int zb = t.product == kStep && wide ? t.z : zx;
+        const uint32_t sa = ring + stage * C::STAGE;
+        const uint32_t sb = sa + kPABytes;
+        const uint32_t bar = ptx::map_to_rank(full(stage), 0);
+        if (elected) {
+          if (leader) ptx::mbar_arrive_expect_tx(full(stage), 2 * bytes);
+          if (a_mn) {
+            tma_load_3d_pair(sa, ma, bar, i, k, za, pol);
+            tma_load_3d_pair(sa + kAtom, ma, bar, i + 64, k, za, pol);
+          } else {
+            tma_load_3d_pair(sa, ma, bar, k, i, za, pol);
+          }
+          if (b_mn) {
+#pragma unroll
+            for (int c = 0; c < NT / 128; ++c)
+              tma_load_3d_pair(sb + c * kAtom, mb, bar, j + c * 64, k, zb, pol);
+          } else {
+#pragma unroll
+            for (int c = 0; c < NT / 2 / kProductBoxRows; ++c)
+              if (c < boxes)
+                tma_load_3d_pair(sb + c * (kProductBoxRows * 128), mb, bar, k,
+                                 j + c * kProductBoxRows, zb, pol);
+          }
+        }
+        __syncwarp();
+        used |= 1u << stage;
+        parities = (parities & ~(1u << stage)) | (phase << stage);
+        if (++stage == C::S) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // No CTA exits with a copy into its shared memory in flight: see the
+    // producer of pair_product_kernel.
+    if (lane == 0) {
+      if (!ok || *abort_flag) {
+        const uint64_t t0 = ptx::globaltimer();
+        while (ptx::globaltimer() - t0 < kPPeerDrainNs) {
+        }
+      } else if (leader) {
+        for (int s = 0; s < C::S; ++s)
+          if (used >> s & 1u) W.wait_final(full(s), parities >> s & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (leader) {
+      const uint64_t a_k0 = ptx::sdesc_sw128(ring), a_mn0 = sdesc_mn_sw128(ring);
+      const uint64_t b_k0 = ptx::sdesc_sw128(ring + kPABytes);
+      const uint64_t b_mn0 = sdesc_mn_sw128(ring + kPABytes);
+      const bool elected = ptx::elect_one();
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      ChainWalk<NT> walk(p, pair, num_pairs);
+      ChainTile ahead;
+      if (!walk.done()) ahead = walk.get();
+      while (ok && !walk.done()) {
+        const ChainTile t = ahead;
+        const bool a_mn = t.product == kGram ? !wide : t.product == kStep && wide;
+        const bool b_mn = t.product == kGram && !wide;
+        // F16 operands, FP32 sums, M = 256
+        const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) |
+                               (static_cast<uint32_t>(b_mn) << 16) |
+                               (static_cast<uint32_t>(t.n_mma >> 3) << 17) | ((256u >> 4) << 24);
+        const uint64_t a0 = a_mn ? a_mn0 : a_k0, b0 = b_mn ? b_mn0 : b_k0;
+        const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+        if (!W.wait(tempty(acc), acc_phase ^ 1u)) break;
+        const uint32_t d0 = tmem_base + acc * NT;
+        for (int kb = 0; kb < t.k_blocks; ++kb) {
+          if (!W.wait(full(stage), phase)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          if (elected) {
+            const uint64_t ad = a0 + stage * (C::STAGE >> 4);
+            const uint64_t bd = b0 + stage * (C::STAGE >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kPBK / 16; ++kk)
+              ptx::mma_bf16_pair(d0, ad + kk * a_step, bd + kk * b_step, idesc,
+                                 (kb | kk) ? 1u : 0u);
+            if (kb + 1 == t.k_blocks) ptx::mma_commit_pair_both(tfull(acc));
+            ptx::mma_commit_pair_both(empty(stage));
+          }
+          __syncwarp();
+          if (kb == 0) {
+            // the next tile's place, found while the tensor cores work
+            walk.next();
+            if (!walk.done()) ahead = walk.get();
+          }
+          if (++stage == C::S) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      // every MMA issued completes before TMEM is released
+      if (elected) ptx::mma_commit_pair_self(done_bar);
+      __syncwarp();
+      W.wait_final(done_bar, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 3) {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // TMEM lane quarter this warp may access
+    constexpr int COLS = NT / (kPEpiWarps / 4);  // rows j per warp
+    const int col_begin = ((warp - 3) >> 2) * COLS;
+    const uint32_t stage_at = ring + C::STAGING + (warp - 3) * 2048;
+    int acc = 0;
+    uint32_t acc_phase = 0, stored_phase = 0;
+    int seen_z = -1;
+    uint32_t seen_after = 0;
+    for (ChainWalk<NT> walk(p, pair, num_pairs); !walk.done(); walk.next()) {
+      const ChainTile t = walk.get();
+      const bool last = t.product == kStep && t.t + 1 == p.steps;
+      const int i = t.i0 + static_cast<int>(rank) * 128 + q * 32 + lane;
+      const int ncols = min(t.nvalid - col_begin, COLS);  // <= 0: nothing for this warp
+      const int64_t j = static_cast<int64_t>(t.j0) + col_begin;
+      float alpha, beta = 0.f, diag = 0.f;
+      uint16_t* out;
+      int64_t ld_out;
+      const CUtensorMap* mo;
+      if (t.product == kGram) {
+        alpha = t.t == 0 ? p.alpha_gram[t.z] : kScaleGram / (kScaleX * kScaleX);
+        out = p.gram + t.z * p.m * p.ldm;
+        ld_out = p.ldm;
+        mo = &maps.o_gram;
+      } else if (t.product == kPoly) {
+        alpha = kScalePoly * p.c / (kScaleGram * kScaleGram);
+        beta = kScalePoly * p.b / kScaleGram;
+        diag = kScalePoly * p.a;
+        out = p.poly + t.z * p.m * p.ldm;
+        ld_out = p.ldm;
+        mo = &maps.o_poly;
+      } else {
+        alpha = t.t == 0 ? p.alpha_step[t.z] : (last ? 1.f : kScaleX) / (kScalePoly * kScaleX);
+        ld_out = last ? p.cols : p.ld;
+        out = (last ? static_cast<uint16_t*>(p.out) : p.x[(t.t & 1) ^ 1]) +
+              static_cast<int64_t>(t.z) * p.rows * ld_out;
+        mo = last ? &maps.out : &maps.ox[(t.t & 1) ^ 1];
+      }
+      uint32_t packed[COLS / 2];  // rows (2c, 2c + 1) of this lane's column
+      if (t.product == kPoly) {
+        // A, fetched while the tile's MMAs run: two columns and one row per
+        // lane (rows are padded to even lengths), then swapped to one column
+        // and two rows as the results will be
+        if (t.z != seen_z || t.after != seen_after) {
+          if (!wait_count(W, p.done + t.z, t.after)) break;
+          seen_z = t.z;
+          seen_after = t.after;
+        }
+        const uint16_t* src = p.gram + t.z * p.m * p.ldm + (j + (lane & 1)) * p.ldm + (i & ~1);
+#pragma unroll
+        for (int c = 0; c < COLS; c += 2)
+          packed[c / 2] = (i & ~1) < p.m && c + (lane & 1) < ncols
+                              ? __ldcg(reinterpret_cast<const uint32_t*>(src + c * p.ldm))
+                              : 0u;
+#pragma unroll
+        for (int c = 0; c < COLS; c += 2) packed[c / 2] = swap_pair(packed[c / 2], lane);
+      }
+      if (!W.wait(tfull(acc), acc_phase)) break;
+      ptx::tc_fence_after();
+      const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NT + col_begin;
+      const bool f16 = !last || p.out_type == kF16;
+      const int on_diag = i - t.j0 - col_begin;  // the row where j == i
+#pragma unroll
+      for (int c = 0; c < COLS; c += 32) {
+        if (c < ncols) {
+          uint32_t r[32];
+          ptx::tmem_ld32(tq + c, r);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int u = 0; u < 32; u += 2) {
+            float v0 = alpha * __uint_as_float(r[u]), v1 = alpha * __uint_as_float(r[u + 1]);
+            if (t.product == kPoly) {
+              const __half2 g = *reinterpret_cast<const __half2*>(&packed[(c + u) / 2]);
+              v0 = fmaf(beta, __low2float(g), v0);
+              v1 = fmaf(beta, __high2float(g), v1);
+              if (c + u == on_diag) v0 += diag;
+              if (c + u + 1 == on_diag) v1 += diag;
+            }
+            packed[(c + u) / 2] = pack_out(v0, v1, f16);
+          }
+        }
+      }
+      // the accumulator is free before any store
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_relaxed_cluster(ptx::map_to_rank(tempty(acc), 0));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+      if (!last || p.out_staged) {
+#pragma unroll
+        for (int c = 0; c < COLS; c += 32) {
+          if (c < ncols) {
+            if (lane == 0) tma_store_read_done();
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 32; u += 2) {
+              const uint32_t v = swap_pair(packed[(c + u) / 2], lane);
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage_at + (u + (lane & 1)) * 64 +
+                                                           (lane & ~1) * 2),
+                           "r"(v)
+                           : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && i < t.columns)
+              tma_store_3d<false>(mo, stage_at, i, static_cast<int>(j) + c, t.z);
+          }
+        }
+      } else if (i < t.columns) {
+        uint16_t* dst = out + j * ld_out + i;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c)
+          if (c < ncols) dst[c * ld_out] = static_cast<uint16_t>(packed[c / 2] >> (16 * (c & 1)));
+      }
+      if (t.product != kStep && t.j0 >= t.i0 + kProductTileM && i < p.m) {
+        // the mirror image: row i, columns j (8 at a time; rows are padded to
+        // multiples of 64 elements)
+        uint16_t* dst = out + static_cast<int64_t>(i) * ld_out + j;
+#pragma unroll
+        for (int c = 0; c < COLS; c += 8)
+          if (c < ncols)
+            *reinterpret_cast<uint4*>(dst + c) = make_uint4(packed[c / 2], packed[c / 2 + 1],
+                                                            packed[c / 2 + 2], packed[c / 2 + 3]);
+      }
+      if (!last) {
+        // this warp's part of the tile is in memory; the first epilogue warp
+        // waits for all parts and tells both kinds of readers (plain stores
+        // and bulk copies alike)
+        if (lane == 0) tma_store_done();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(stored);
+        if (warp == 3) {
+          if (!W.wait(stored, stored_phase)) break;
+          stored_phase ^= 1u;
+          if (lane == 0) {
+            asm volatile("fence.proxy.async;" ::: "memory");
+            asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.done + t.z) : "memory");
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) tma_store_done();
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  // no signal, copy or MMA read crosses between the two CTAs after this
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+  }
+}
+
+template <int NT>
+cudaError_t launch_chain(const OrthoChainMaps& maps, const OrthoChainArgs& p, cudaStream_t s) {
+  using C = ChainCfg<NT>;
+  constexpr auto kern = ortho_chain_kernel<NT>;
+  const cudaError_t err = smem_limit_once<kern>(static_cast<int>(C::SMEM_BYTES));
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  // pairs wait on one another's tiles: all of them run at once
+  attr[1].id = cudaLaunchAttributeCooperative;
+  attr[1].val.cooperative = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(kPThreads);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;  // the occupancy query takes the cluster shape only
+  static std::mutex mu;
+  static int resident[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices)
+    return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (resident[dev] == 0) {
+      int n = 0;
+      const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+      if (e != cudaSuccess) return e;
+      resident[dev] = n;
+    }
+  }
+  if (resident[dev] <= 0) return cudaErrorUnknown;
+  // more pairs than the largest product has tiles would only wait
+  const int64_t m_mt = (p.m + 255) / 256, m_nt = (p.m + NT - 1) / NT;
+  const int64_t most = std::max(m_mt * m_nt - 256 / NT * (m_mt * (m_mt - 1) / 2),
+                                static_cast<int64_t>((p.cols + 255) / 256) *
+                                    ((p.rows + NT - 1) / NT)) * p.batch;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min<int64_t>(resident[dev], most)));
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, maps, p);
+}
+
+}  // namespace
+
+cudaError_t launch_ortho_chain(int nt, const OrthoChainMaps& maps, const OrthoChainArgs& p,
+                               cudaStream_t s) {
+  return nt == 128 ? launch_chain<128>(maps, p, s) : launch_chain<256>(maps, p, s);
+}
+
+}  // namespace beam

@@ -1,0 +1,43 @@
+// All steps of the orthogonalised update in one launch (ortho_chain.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace beam {
+
+// F16 tensor maps [z][row][contiguous] of the buffers in their roles as
+// operand A (columns i) and B (rows j) of the three products, and as results
+// (boxes 32 x 32, no swizzle).  Of X there are two, used in turn; ox[k] is
+// X[k] as a result.  `out` is only read with OrthoChainArgs::out_staged.
+struct OrthoChainMaps {
+  CUtensorMap gram_a[2], gram_b[2], poly_a, poly_b, step_x[2], step_p;
+  CUtensorMap o_gram, o_poly, ox[2], out;
+};
+
+struct OrthoChainArgs {
+  int32_t batch, rows, cols, m;   // m = min(rows, cols)
+  int32_t steps;
+  int32_t split;                  // X[0] is followed by its low parts (z + batch)
+  int64_t ld, ldm;                // row strides of X and of the m x m products
+  uint16_t* x[2];
+  uint16_t* gram;
+  uint16_t* poly;
+  void* out;
+  int32_t out_type, out_staged;
+  const float* alpha_gram;        // [batch] factors of the first step
+  const float* alpha_step;
+  float a, b, c;
+  uint32_t* done;                 // [batch] warps' finished tiles, zero at the start
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+};
+
+// nt: rows j per tile, 128 or 256.  Boxes of the maps: 64 x 128 (A along k),
+// 64 x 64 (along i or j), 64 x 32 (B along k).
+cudaError_t launch_ortho_chain(int nt, const OrthoChainMaps& maps, const OrthoChainArgs& p,
+                               cudaStream_t s);
+
+}  // namespace beam

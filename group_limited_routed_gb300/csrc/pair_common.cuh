@@ -1,0 +1,146 @@
+// Pieces shared by the CTA-pair products of the training operators
+// (pair_product_kernel.cuh, ortho_chain.cu): tile constants, loads and
+// descriptors of both operand orders, accumulator loads, staged stores.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "gemm_common.cuh"
+#include "ptx.cuh"
+
+namespace beam {
+namespace {
+
+using gemm::Waiter;
+
+constexpr int kPBK = 64;                       // k elements per block (128 bytes)
+constexpr uint32_t kPABytes = 128 * 128;       // one CTA's A per stage
+constexpr int kPEpiWarps = 16;
+constexpr int kPThreads = 96 + 32 * kPEpiWarps;
+constexpr uint32_t kPRing = 216 * 1024;
+constexpr uint64_t kPPeerDrainNs = 1000000ull; // see the producers' teardown
+constexpr uint32_t kAtom = 64 * 128;           // MN-major atom: 64 k rows of 64 elements
+
+// Results that leave through shared memory: a warp stages 2 KB (16 rows of 32
+// FP32 columns, or 32 rows of 16-bit ones) and one bulk copy writes them.
+constexpr uint32_t kStaging = kPEpiWarps * 2048;
+
+// 3-D tiled load into this CTA's shared memory, bytes counted on a barrier of
+// either CTA of the pair.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m,
+                                                 uint32_t cluster_bar, int32_t x, int32_t y,
+                                                 int32_t z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar), "l"(policy)
+      : "memory");
+}
+
+// Shared-memory descriptor of an MN-major operand as a 128-byte-swizzled TMA
+// load of a 64 x 64 box leaves it: each k row is 128 bytes of 64 consecutive
+// elements; 8 k rows make a 1024-byte group (stride byte offset); the next 64
+// elements of the operand's own axis are one box further (leading byte offset).
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(kAtom >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// Arrive on either CTA's barrier without a release.  It frees TMEM columns
+// whose loads have completed (tcgen05.wait::ld): no memory is handed over,
+// and a release would wait for the warp's earlier global stores.
+__device__ __forceinline__ void arrive_relaxed_cluster(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+               : "memory");
+}
+// Waiter::wait for a barrier whose arrivals release at cluster scope.
+__device__ __forceinline__ bool wait_cluster(const Waiter& w, uint32_t bar, uint32_t parity) {
+  auto done = [&] {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+  };
+  if (done()) return true;
+  const uint64_t t0 = ptx::globaltimer();
+  for (uint32_t n = 1;; ++n) {
+    if (done()) return true;
+    if ((n & 63u) == 0) {
+      if (*w.abort_flag) return false;
+      if (ptx::globaltimer() - t0 > w.limit_ns) {
+        *w.abort_flag = 1;
+        latch_status(w.status, kStatusTimeout);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[16]) { ptx::tmem_ld16(at, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[32]) { ptx::tmem_ld32(at, r); }
+
+// Two values rounded to the 16-bit output type, the first in the low half.
+__device__ __forceinline__ uint32_t pack_out(float lo, float hi, bool f16) {
+  if (f16) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Bulk copy of a warp's staged rows, shared -> global; ADD: += in FP32.
+template <bool ADD>
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int32_t x,
+                                             int32_t y, int32_t z) {
+  if constexpr (ADD)
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group "
+        "[%0, {%1, %2, %3}], [%4];" ::"l"(reinterpret_cast<uint64_t>(m)),
+        "r"(x), "r"(y), "r"(z), "r"(src)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::
+            "l"(reinterpret_cast<uint64_t>(m)),
+        "r"(x), "r"(y), "r"(z), "r"(src)
+        : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Every staged row of this thread's copies has been read / written.
+__device__ __forceinline__ void tma_store_read_done() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_done() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// Two 16-bit values of one lane's column (rows j, j + 1) and its neighbour's
+// -> the word this lane stores: even lanes row j, odd lanes row j + 1, two
+// columns each.
+__device__ __forceinline__ uint32_t swap_pair(uint32_t mine, int lane) {
+  const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
+  return (lane & 1) ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
+}
+
+}  // namespace
+}  // namespace beam

@@ -64,14 +64,6 @@ cudaError_t launch_rows(bool a_mn, const CUtensorMap& a, const CUtensorMap& b,
               : launch_impl<NT, false, false, kProductRows, false>(a, b, out, p, tiles, s);
 }
 
-template <int NT>
-cudaError_t launch_dense(bool a_mn, const CUtensorMap& a, const CUtensorMap& b,
-                         const CUtensorMap& out, const ProductArgs& p, int64_t tiles,
-                         cudaStream_t s) {
-  return a_mn ? launch_impl<NT, true, false, kProductDense, false>(a, b, out, p, tiles, s)
-              : launch_impl<NT, false, false, kProductDense, false>(a, b, out, p, tiles, s);
-}
-
 }  // namespace
 
 cudaError_t launch_pair_product(int kind, int nt, bool a_mn, bool b_mn, const CUtensorMap& a,
@@ -94,20 +86,6 @@ cudaError_t launch_pair_product(int kind, int nt, bool a_mn, bool b_mn, const CU
     return p.out_type == kF32
                ? launch_impl<256, true, true, kProductGroups, true>(a, b, out, p, tiles, s)
                : launch_impl<256, true, true, kProductGroups, false, true>(a, b, out, p, tiles, s);
-  if (kind == kProductDense && p.out_type != kF32) {
-    if (!b_mn) {
-      switch (nt) {
-        case 64: return launch_dense<64>(a_mn, a, b, out, p, tiles, s);
-        case 128: return launch_dense<128>(a_mn, a, b, out, p, tiles, s);
-        case 256: return launch_dense<256>(a_mn, a, b, out, p, tiles, s);
-      }
-    } else if (a_mn) {
-      if (nt == 128)
-        return launch_impl<128, true, true, kProductDense, false>(a, b, out, p, tiles, s);
-      if (nt == 256)
-        return launch_impl<256, true, true, kProductDense, false>(a, b, out, p, tiles, s);
-    }
-  }
   return cudaErrorInvalidValue;
 }
 

@@ -17,45 +17,34 @@ enum : int32_t { kBf16 = 0, kF16 = 1, kF32 = 2 };
 enum ProductKind : int32_t {
   kProductRows = 0,     // rows j in groups (ragged): A is the group's weights
   kProductGroups = 1,   // k runs over a group's rows (ragged): one output per group
-  kProductDense = 2,    // a stack of equal products
 };
 
 struct ProductArgs {
   int32_t M;               // output columns i
   int32_t N;               // output rows j of one z (kProductRows: all rows)
-  int32_t k_blocks;        // 64-wide blocks of k (kProductDense, kProductRows)
-  int32_t k_wrap;          // k blocks after which k starts again ...
-  int32_t wrap_za;         // ... with A's z advanced by this,
-  int32_t wrap_zb;         // and B's (a second addend, e.g. low-order parts)
+  int32_t k_blocks;        // 64-wide blocks of k (kProductRows)
   int32_t a_z;             // A's z per group: 1, or 0 where all groups share one matrix
-  int32_t groups;          // groups E, or matrices of the stack
-  int32_t rows;            // ragged kinds: rows in all
-  const int32_t* offsets;  // ragged kinds: [groups + 1] first row of each group
+  int32_t groups;          // groups E
+  int32_t rows;            // rows in all
+  const int32_t* offsets;  // [groups + 1] first row of each group
   void* out;
   int64_t ld_out;          // elements between output rows
-  int64_t z_out;           // elements between outputs of the stack
+  int64_t z_out;           // elements between the groups' outputs (kProductGroups)
   int32_t out_type;        // kBf16, kF16 or kF32
   int32_t in_type;         // kBf16 or kF16
   int32_t accumulate;      // out += (kF32 outputs)
   int32_t staged;          // `tm_out` describes out: results may leave by bulk copy
-  int32_t symmetric;       // kDense, M == N: compute one triangle of tiles, mirror it
-  // out = alpha * product (+ beta * add) (+ diag on i == j); add: F16, laid
-  // out as out; alpha_z: a factor of each z, or nullptr
-  float alpha, beta, diag;
-  const uint16_t* add;
-  const float* alpha_z;
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
 
-// Rows of B one tile takes (the tile is 256 columns i by this many rows j).
-constexpr int kProductMaxTile = 256;
+// Columns i of a tile, groups a call may have.
 constexpr int kProductTileM = 256;
 constexpr int kProductMaxGroups = 1024;
 
 // Rows j of one box of a k-contiguous B (nt / 2 where that is less).
 constexpr int kProductBoxRows = 32;
-inline int product_out_rows(int nt, bool f32) { return f32 || nt < 128 ? 16 : 32; }
+inline int product_out_rows(bool f32) { return f32 ? 16 : 32; }
 inline int product_box_rows(int nt) { return nt / 2 < kProductBoxRows ? nt / 2 : kProductBoxRows; }
 
 // nt: rows j per tile, 32, 64, 128 or 256 (kProductGroups: 256).  a_mn, b_mn:
@@ -63,7 +52,7 @@ inline int product_box_rows(int nt) { return nt / 2 < kProductBoxRows ? nt / 2 :
 // three-dimensional (contiguous, row, z); a and b with 128-byte swizzle and
 // boxes 64 x 128 (a, k contiguous), 64 x 64 (a_mn, b_mn), 64 x
 // product_box_rows(nt) (b, k contiguous); out (only read with p.staged)
-// without swizzle, boxes 32 x product_out_rows(nt, FP32?).
+// without swizzle, boxes 32 x product_out_rows.
 cudaError_t launch_pair_product(int kind, int nt, bool a_mn, bool b_mn, const CUtensorMap& a,
                                 const CUtensorMap& b, const CUtensorMap& out,
                                 const ProductArgs& p, cudaStream_t s);

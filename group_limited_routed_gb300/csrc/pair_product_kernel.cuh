@@ -24,9 +24,6 @@
 //                   a group also covers rows of the next group; those rows
 //                   are zeroed in shared memory (in both operands: 0 * inf
 //                   would not be 0) before the MMA reads them.
-//   kProductDense   stacks of equal products (the orthogonalisation), with an
-//                   affine epilogue and, for symmetric results, one triangle
-//                   of tiles that writes its mirror image as well.
 //
 // Sums: FP32 in TMEM.  A chain of MMAs into one accumulator truncates at
 // every step, an error that grows with the chain and reaches 1e-5 relative
@@ -48,6 +45,7 @@
 
 #include "common.cuh"
 #include "gemm_common.cuh"
+#include "pair_common.cuh"
 #include "pair_product.cuh"
 #include "ptx.cuh"
 
@@ -56,22 +54,11 @@ namespace {
 
 using gemm::Waiter;
 
-constexpr int kPBK = 64;                       // k elements per block (128 bytes)
-constexpr uint32_t kPABytes = 128 * 128;       // one CTA's A per stage
-constexpr int kPEpiWarps = 16;
-constexpr int kPThreads = 96 + 32 * kPEpiWarps;
-constexpr uint32_t kPRing = 216 * 1024;
-constexpr int kWideBlocks = 8;                 // k blocks per accumulator chain, FP32 outputs
-constexpr uint64_t kPPeerDrainNs = 1000000ull; // see the producer's teardown
-constexpr uint32_t kAtom = 64 * 128;           // MN-major atom: 64 k rows of 64 elements
-
-// Results that leave through shared memory: a warp stages 2 KB (16 rows of 32
-// FP32 columns, or 32 rows of 16-bit ones) and one bulk copy writes them.
-constexpr uint32_t kStaging = kPEpiWarps * 2048;
+constexpr int kWideBlocks = 8;  // k blocks per accumulator chain, FP32 outputs
 
 template <int NT, int KIND, bool WIDE, bool DUAL>
 struct ProductCfg {
-  static constexpr bool STAGED = KIND != kProductRows || WIDE;
+  static constexpr bool STAGED = KIND == kProductGroups || WIDE;
   static constexpr uint32_t B_BYTES = NT / 2 * 128;  // one block of rows
   static constexpr uint32_t STAGE = kPABytes + (DUAL ? 2 : 1) * B_BYTES;
   static constexpr int S_RAW = static_cast<int>((kPRing + (DUAL ? 8192 : 0) - (STAGED ? kStaging : 0)) / STAGE);
@@ -89,70 +76,6 @@ struct ProductCfg {
   static_assert(STAGE % 1024 == 0, "swizzle atoms are 1024-byte aligned");
   static_assert(TMEM_COLS <= 512, "TMEM columns");
 };
-
-// 3-D tiled load into this CTA's shared memory, bytes counted on a barrier of
-// either CTA of the pair.
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* m,
-                                                 uint32_t cluster_bar, int32_t x, int32_t y,
-                                                 int32_t z, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".cta_group::2.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(cluster_bar), "l"(policy)
-      : "memory");
-}
-
-// Shared-memory descriptor of an MN-major operand as a 128-byte-swizzled TMA
-// load of a 64 x 64 box leaves it: each k row is 128 bytes of 64 consecutive
-// elements; 8 k rows make a 1024-byte group (stride byte offset); the next 64
-// elements of the operand's own axis are one box further (leading byte offset).
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(kAtom >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
-}
-
-// Arrive on either CTA's barrier without a release.  It frees TMEM columns
-// whose loads have completed (tcgen05.wait::ld): no memory is handed over,
-// and a release would wait for the warp's earlier global stores.
-__device__ __forceinline__ void arrive_relaxed_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
-               : "memory");
-}
-// Waiter::wait for a barrier whose arrivals release at cluster scope.
-__device__ __forceinline__ bool wait_cluster(const Waiter& w, uint32_t bar, uint32_t parity) {
-  auto done = [&] {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-  };
-  if (done()) return true;
-  const uint64_t t0 = ptx::globaltimer();
-  for (uint32_t n = 1;; ++n) {
-    if (done()) return true;
-    if ((n & 63u) == 0) {
-      if (*w.abort_flag) return false;
-      if (ptx::globaltimer() - t0 > w.limit_ns) {
-        *w.abort_flag = 1;
-        latch_status(w.status, kStatusTimeout);
-        return false;
-      }
-    }
-  }
-}
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
 
 struct ProductTile {
   int z;         // group or matrix
@@ -252,7 +175,7 @@ struct ProductWalk {
       t.nvalid2 = 0;
       t.k_blocks = p.k_blocks;
       t.k0 = t.k_count = 0;
-    } else if constexpr (KIND == kProductGroups) {
+    } else {
       t.z = z;
       t.i0 = i * kProductTileM;
       t.j0 = j * kSpan;
@@ -267,99 +190,11 @@ struct ProductWalk {
       t.k0 = k_first;
       t.k_count = k_rows;
       t.k_blocks = (t.k_count + kPBK - 1) / kPBK;
-    } else {
-      int bi, bj;
-      if (p.symmetric) {
-        // tiles with j >= i, in units of 256 columns and NT rows
-        constexpr int R = kProductTileM / NT;
-        const int per_z = mt * nt - R * (mt * (mt - 1) / 2);
-        t.z = tile / per_z;
-        int left = tile - t.z * per_z;
-        bi = 0;
-        while (left >= nt - bi * R) {
-          left -= nt - bi * R;
-          ++bi;
-        }
-        bj = bi * R + left;
-      } else {
-        t.z = tile / (mt * nt);
-        const int local = tile - t.z * mt * nt;
-        bi = local / nt;
-        bj = local - bi * nt;
-      }
-      t.i0 = bi * kProductTileM;
-      t.j0 = bj * NT;
-      t.nvalid = min(NT, p.N - t.j0);
-      t.nvalid2 = 0;
-      t.k_blocks = p.k_blocks;
-      t.k0 = t.k_count = 0;
     }
     t.n_mma = (t.nvalid + 15) & ~15;
     return t;
   }
 };
-
-__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[16]) { ptx::tmem_ld16(at, r); }
-__device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[32]) { ptx::tmem_ld32(at, r); }
-
-template <int NT, int KIND, bool DUAL>
-__device__ __forceinline__ int product_tiles(const ProductArgs& p, const int32_t* s_start) {
-  constexpr int kSpan = DUAL ? 2 * NT : NT;
-  const int mt = (p.M + kProductTileM - 1) / kProductTileM;
-  const int nt = (p.N + kSpan - 1) / kSpan;
-  if constexpr (KIND == kProductRows) {
-    return s_start[p.groups];
-  } else if (KIND == kProductDense && p.symmetric) {
-    constexpr int R = kProductTileM / NT;
-    return p.groups * (mt * nt - R * (mt * (mt - 1) / 2));
-  } else {
-    return p.groups * mt * nt;
-  }
-}
-
-// Two values rounded to the 16-bit output type, the first in the low half.
-__device__ __forceinline__ uint32_t pack_out(float lo, float hi, bool f16) {
-  if (f16) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Bulk copy of a warp's staged rows, shared -> global; ADD: += in FP32.
-template <bool ADD>
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int32_t x,
-                                             int32_t y, int32_t z) {
-  if constexpr (ADD)
-    asm volatile(
-        "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group "
-        "[%0, {%1, %2, %3}], [%4];" ::"l"(reinterpret_cast<uint64_t>(m)),
-        "r"(x), "r"(y), "r"(z), "r"(src)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::
-            "l"(reinterpret_cast<uint64_t>(m)),
-        "r"(x), "r"(y), "r"(z), "r"(src)
-        : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// Every staged row of this thread's copies has been read / written.
-__device__ __forceinline__ void tma_store_read_done() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-__device__ __forceinline__ void tma_store_done() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
-
-// Two 16-bit values of one lane's column (rows j, j + 1) and its neighbour's
-// -> the word this lane stores: even lanes row j, odd lanes row j + 1, two
-// columns each.
-__device__ __forceinline__ uint32_t swap_pair(uint32_t mine, int lane) {
-  const uint32_t other = __shfl_xor_sync(0xffffffffu, mine, 1);
-  return (lane & 1) ? __byte_perm(other, mine, 0x7632) : __byte_perm(mine, other, 0x5410);
-}
 
 template <int NT, bool A_MN, bool B_MN, int KIND, bool WIDE, bool DUAL>
 __global__ void __launch_bounds__(kPThreads, 1)
@@ -483,7 +318,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int num_tiles = product_tiles<NT, KIND, DUAL>(p, s_start);
+  int num_tiles;
+  if constexpr (KIND == kProductRows)
+    num_tiles = s_start[p.groups];
+  else
+    num_tiles = p.groups * ((p.M + kProductTileM - 1) / kProductTileM) *
+                ((p.N + Walk::kSpan - 1) / Walk::kSpan);
   const Waiter W{abort_flag, p.status, p.wait_limit_ns};
 
   if (warp == 0) {
@@ -515,19 +355,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
             break;
           }
           const bool ragged = RAGGED_K && (kb + 1) * kPBK > t.k_count;
-          int k = kb, za = t.z * p.a_z, zb = KIND == kProductRows ? 0 : t.z;
-          if constexpr (KIND == kProductDense) {
-            if (kb >= p.k_wrap) {
-              k -= p.k_wrap;
-              za += p.wrap_za;
-              zb += p.wrap_zb;
-            }
-          }
-          k *= kPBK;
-          if constexpr (RAGGED_K) {
-            k += t.k0;
-            za = zb = 0;
-          }
+          const int k = kb * kPBK + (RAGGED_K ? t.k0 : 0);
+          const int za = RAGGED_K ? 0 : t.z * p.a_z;  // B's rows are one matrix
           const uint32_t sa = ring + stage * C::STAGE;
           const uint32_t sb = sa + kPABytes;
           // the leader's full barrier counts both CTAs' bytes; a group's
@@ -551,18 +380,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if constexpr (B_MN) {
 #pragma unroll
               for (int c = 0; c < NT / 128; ++c)
-                tma_load_3d_pair(sb + c * kAtom, &tm_b, bar, j + c * 64, k, zb, pol);
+                tma_load_3d_pair(sb + c * kAtom, &tm_b, bar, j + c * 64, k, 0, pol);
               if (DUAL && n2) {
 #pragma unroll
                 for (int c = 0; c < NT / 128; ++c)
-                  tma_load_3d_pair(sb + C::B_BYTES + c * kAtom, &tm_b, bar, j2 + c * 64, k, zb,
+                  tma_load_3d_pair(sb + C::B_BYTES + c * kAtom, &tm_b, bar, j2 + c * 64, k, 0,
                                    pol);
               }
             } else {
 #pragma unroll
               for (int c = 0; c < NT / 2 / BOX; ++c)
                 if (c < boxes)
-                  tma_load_3d_pair(sb + c * (BOX * 128), &tm_b, bar, k, j + c * BOX, zb, pol);
+                  tma_load_3d_pair(sb + c * (BOX * 128), &tm_b, bar, k, j + c * BOX, 0, pol);
             }
           }
           __syncwarp();
@@ -875,22 +704,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (;;) {
           const bool live = t.k_blocks > 0;
           uint32_t packed[COLS / 2];  // rows (2c, 2c + 1) of this lane's column
-          const bool with_add = KIND == kProductDense && p.add;
-          if (with_add) {
-            // the addend, fetched while the tile's MMAs run: two columns and
-            // one row per lane (rows are padded to even lengths), then swapped
-            // to one column and two rows as the results will be
-            const uint16_t* src = p.add + zbase +
-                                  (static_cast<int64_t>(t.j0) + col_begin + (lane & 1)) * p.ld_out +
-                                  (i & ~1);
-#pragma unroll
-            for (int c = 0; c < COLS; c += 2)
-              packed[c / 2] = (i & ~1) < p.M && c + (lane & 1) < ncols
-                                  ? *reinterpret_cast<const uint32_t*>(src + c * p.ld_out)
-                                  : 0u;
-#pragma unroll
-            for (int c = 0; c < COLS; c += 2) packed[c / 2] = swap_pair(packed[c / 2], lane);
-          }
           if (live) {
             if (!W.wait(tfull(acc), acc_phase)) {
               ok = false;
@@ -899,10 +712,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             ptx::tc_fence_after();
           }
           const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NT + col_begin;
-          float alpha = p.alpha;
-          if (KIND == kProductDense && p.alpha_z) alpha *= p.alpha_z[t.z];
           uint16_t* out = static_cast<uint16_t*>(p.out) + zbase;
-          const int on_diag = i - t.j0 - col_begin;
 #pragma unroll
           for (int c = 0; c < COLS; c += LD) {
             if (c < ncols) {
@@ -915,23 +725,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 for (int u = 0; u < LD; ++u) r[u] = 0u;
               }
 #pragma unroll
-              for (int u = 0; u < LD; u += 2) {
-                float v0 = __uint_as_float(r[u]), v1 = __uint_as_float(r[u + 1]);
-                if constexpr (KIND == kProductDense) {
-                  v0 *= alpha;
-                  v1 *= alpha;
-                  if (with_add) {
-                    const __half2 a =
-                        *reinterpret_cast<const __half2*>(&packed[(c + u) / 2]);
-                    v0 = fmaf(p.beta, __low2float(a), v0);
-                    v1 = fmaf(p.beta, __high2float(a), v1);
-                  }
-                  // on the diagonal (i == j)
-                  if (c + u == on_diag) v0 += p.diag;
-                  if (c + u + 1 == on_diag) v1 += p.diag;
-                }
-                packed[(c + u) / 2] = pack_out(v0, v1, f16);
-              }
+              for (int u = 0; u < LD; u += 2)
+                packed[(c + u) / 2] = pack_out(__uint_as_float(r[u]), __uint_as_float(r[u + 1]), f16);
             }
           }
           if (live) {
@@ -944,14 +739,13 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           const int64_t j = static_cast<int64_t>(t.j0) + col_begin;
           if (C::STAGED && p.staged) {
-            constexpr int ROWS = COLS < 32 ? COLS : 32;  // rows of a piece
 #pragma unroll
-            for (int c = 0; c < COLS; c += ROWS) {
+            for (int c = 0; c < COLS; c += 32) {
               if (c < ncols) {
                 if (lane == 0) tma_store_read_done();
                 __syncwarp();
 #pragma unroll
-                for (int u = 0; u < ROWS; u += 2) {
+                for (int u = 0; u < 32; u += 2) {
                   const uint32_t v = swap_pair(packed[(c + u) / 2], lane);
                   asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage_at + (u + (lane & 1)) * 64 +
                                                                (lane & ~1) * 2),
@@ -980,16 +774,6 @@ __global__ void __launch_bounds__(kPThreads, 1)
             for (int c = 0; c < COLS; ++c)
               if (c < ncols)
                 dst[c * p.ld_out] = static_cast<uint16_t>(packed[c / 2] >> (16 * (c & 1)));
-          }
-          if (KIND == kProductDense && p.symmetric && t.j0 >= t.i0 + kProductTileM && i < p.M) {
-            // the mirror image: row i, columns j (16 at a time; rows are padded
-            // to multiples of 16 elements)
-            uint16_t* dst = out + static_cast<int64_t>(i) * p.ld_out + j;
-#pragma unroll
-            for (int c = 0; c < COLS; c += 8)
-              if (c < ncols)
-                *reinterpret_cast<uint4*>(dst + c) = make_uint4(packed[c / 2], packed[c / 2 + 1],
-                                                                packed[c / 2 + 2], packed[c / 2 + 3]);
           }
           if (!DUAL || t.nvalid2 == 0) break;
           // the tile's second block

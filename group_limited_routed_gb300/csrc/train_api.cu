@@ -12,6 +12,7 @@
 #include "../../include/beam_moe.h"
 #include "common.cuh"
 #include "host.cuh"
+#include "ortho_chain.cuh"
 #include "ortho_scale.cuh"
 #include "ortho_small.cuh"
 #include "pair_product.cuh"
@@ -53,7 +54,7 @@ bool tmap3(CUtensorMap* m, const void* base, int32_t type, int64_t inner, int64_
 // Map of a result [z][rows][cols] for bulk copies out of shared memory; false
 // where its address or strides are no multiples of 16 bytes.
 bool staged_out(CUtensorMap* m, void* out, int32_t type, int64_t cols, int64_t rows, int64_t z,
-                int64_t ld, int64_t zs, int nt) {
+                int64_t ld, int64_t zs) {
   const int64_t bytes = type == BEAM_DTYPE_F32 ? 4 : 2;
   if (z <= 1) zs = ld * rows;
   if ((reinterpret_cast<uintptr_t>(out) & 15u) || ld * bytes % 16 || zs * bytes % 16) return false;
@@ -62,7 +63,7 @@ bool staged_out(CUtensorMap* m, void* out, int32_t type, int64_t cols, int64_t r
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * bytes),
                            static_cast<cuuint64_t>(zs * bytes)};
   cuuint32_t box[3] = {
-      32, static_cast<cuuint32_t>(beam::product_out_rows(nt, type == BEAM_DTYPE_F32)), 1};
+      32, static_cast<cuuint32_t>(beam::product_out_rows(type == BEAM_DTYPE_F32)), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType t = type == BEAM_DTYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                 : type == BEAM_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
@@ -197,7 +198,6 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   p.M = static_cast<int32_t>(M);
   p.N = static_cast<int32_t>(N);
   p.k_blocks = static_cast<int32_t>((k + 63) / 64);
-  p.k_wrap = p.k_blocks;
   p.a_z = a.z > 1 ? 1 : 0;
   p.groups = g.n_groups;
   p.rows = static_cast<int32_t>(g.rows);
@@ -208,14 +208,13 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   p.out_type = g.out_dtype;
   p.in_type = g.dtype;
   p.accumulate = accumulate;
-  p.alpha = 1.f;
   p.status = static_cast<uint32_t*>(ws);
   p.wait_limit_ns = beam::host::wait_limit_ns();
   CUtensorMap to = {};
   // 16-bit rows leave straight from registers
   if (kind == beam::kProductGroups || g.out_dtype == BEAM_DTYPE_F32)
     p.staged = staged_out(&to, out, g.out_dtype, M, N,
-                          kind == beam::kProductGroups ? g.n_groups : 1, ld_out, z_out, nt);
+                          kind == beam::kProductGroups ? g.n_groups : 1, ld_out, z_out);
   return launched(beam::launch_pair_product(kind, nt, a_mn, b_mn, ta, tb, to, p, s));
 }
 
@@ -226,7 +225,7 @@ using beam::kScaleX;
 
 struct OrthoLayout {
   int64_t m, ld, ldm;   // smaller extent, row strides of X and of the m x m products
-  size_t amax, sum_exp, sumsq, alpha_gram, alpha_step, x0, x1, gram, poly, total;
+  size_t amax, sum_exp, sumsq, alpha_gram, alpha_step, done, x0, x1, gram, poly, total;
 };
 
 bool ortho_layout(int32_t batch, int32_t rows, int32_t cols, int32_t dtype, OrthoLayout* L) {
@@ -249,6 +248,7 @@ bool ortho_layout(int32_t batch, int32_t rows, int32_t cols, int32_t dtype, Orth
   L->sumsq = take(static_cast<size_t>(batch) * beam::kNormBlocks * 4);
   L->alpha_gram = take(static_cast<size_t>(batch) * 4);
   L->alpha_step = take(static_cast<size_t>(batch) * 4);
+  L->done = take(static_cast<size_t>(batch) * 4);
   // a 32-bit update starts as two F16 parts, stacked
   L->x0 = take(dtype == BEAM_DTYPE_F32 ? 2 * x : x);
   L->x1 = take(x);
@@ -257,12 +257,6 @@ bool ortho_layout(int32_t batch, int32_t rows, int32_t cols, int32_t dtype, Orth
   L->total = off;
   return true;
 }
-
-// Time of a tile of 256 columns by nt rows, for choosing nt: per 64-wide k
-// block (the MMAs of 256 rows, else the loads of A and of the rows), and once
-// (start-up, epilogue).  Measured on stacks of products of m = 777 and 2560.
-double dense_block_us(int nt) { return nt == 64 ? 0.22 : nt == 128 ? 0.25 : 0.36; }
-double dense_tile_us(int nt) { return 4.0 + nt / 128.0; }
 
 template <typename T>
 T* at(void* ws, size_t off) {
@@ -480,117 +474,62 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
   n.alpha_step = at<float>(workspace, L.alpha_step);
   n.scale_gram = kScaleGram;
   n.scale_step = (d->steps == 1 ? 1.f : kScaleX) / kScalePoly;
+  n.done = at<uint32_t>(workspace, L.done);
   n.eps = d->eps;
   if (beam::launch_norm(n, s) != cudaSuccess) return BEAM_ERR_CUDA;
 
+  // Tiles of 256 rows keep the tensor cores busiest; where all products
+  // together have too few of them for the CTA pairs, 128 rows spread wider.
   const int64_t pairs = dev.sms / 2;
-  // the symmetric products compute the tiles with j >= i only
-  auto tiles = [&](int64_t cols, int64_t rows, int nt, bool symmetric) {
-    const int64_t mt = (cols + 255) / 256, rt = (rows + nt - 1) / nt;
-    return batch * (mt * rt - (symmetric ? 256 / nt * (mt * (mt - 1) / 2) : 0));
-  };
-  auto tile_rows = [&](int64_t cols, int64_t rows, int64_t k, bool symmetric, int least) {
-    int best = 256;
-    double best_us = 1e30;
-    for (int nt = least; nt <= 256; nt *= 2) {
-      const double waves = static_cast<double>((tiles(cols, rows, nt, symmetric) + pairs - 1) / pairs);
-      const double us = waves * ((k + 63) / 64 * dense_block_us(nt) + dense_tile_us(nt));
-      if (us < best_us) best = nt, best_us = us;
-    }
-    return best;
-  };
-  // (MN-major rows come in atoms of 64: a pair's tile has at least 128)
-  const int nt_gram = tile_rows(m, m, std::max(R, C), true, wide ? 64 : 128);
-  const int nt_poly = tile_rows(m, m, m, true, 64);
-  const int nt_step = tile_rows(C, R, m, false, 64);
+  const int64_t mt = (m + 255) / 256;
+  const int64_t wide_tiles =
+      batch * std::min(mt * (mt + 1) / 2, (C + 255) / 256 * ((R + 255) / 256));
+  const int nt = wide_tiles >= pairs ? 256 : 128;
+  const uint32_t rows_box = beam::kProductBoxRows;
 
   const int32_t F16 = BEAM_DTYPE_F16;
-  CUtensorMap ga[2], gb[2], pa, pb, sx[2], sp;  // gram, polynomial, step
+  beam::OrthoChainMaps maps = {};
   for (int i = 0; i < 2; ++i) {
     const int64_t z = i == 0 && split ? 2 * batch : batch;
-    if (!tmap3(&ga[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? 128 : 64) ||
-        !tmap3(&gb[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? beam::product_box_rows(nt_gram) : 64) ||
-        !tmap3(&sx[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? 64 : beam::product_box_rows(nt_step)))
+    if (!tmap3(&maps.gram_a[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? 128 : 64) ||
+        !tmap3(&maps.gram_b[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? rows_box : 64) ||
+        !tmap3(&maps.step_x[i], x[i], F16, C, R, z, L.ld, R * L.ld, wide ? 64 : rows_box) ||
+        !staged_out(&maps.ox[i], x[i], F16, C, R, batch, L.ld, R * L.ld))
       return BEAM_ERR_CUDA;
   }
-  if (!tmap3(&pa, gram, F16, m, m, batch, L.ldm, m * L.ldm, 128) ||
-      !tmap3(&pb, gram, F16, m, m, batch, L.ldm, m * L.ldm, beam::product_box_rows(nt_poly)) ||
-      !tmap3(&sp, poly, F16, m, m, batch, L.ldm, m * L.ldm, wide ? beam::product_box_rows(nt_step) : 128))
+  if (!tmap3(&maps.poly_a, gram, F16, m, m, batch, L.ldm, m * L.ldm, 128) ||
+      !tmap3(&maps.poly_b, gram, F16, m, m, batch, L.ldm, m * L.ldm, rows_box) ||
+      !tmap3(&maps.step_p, poly, F16, m, m, batch, L.ldm, m * L.ldm, wide ? rows_box : 128) ||
+      !staged_out(&maps.o_gram, gram, F16, m, m, batch, L.ldm, m * L.ldm) ||
+      !staged_out(&maps.o_poly, poly, F16, m, m, batch, L.ldm, m * L.ldm))
     return BEAM_ERR_CUDA;
 
-  ProductArgs base = {};
-  base.a_z = 1;
-  base.groups = d->batch;
-  base.in_type = F16;
-  base.out_type = F16;
-  base.status = static_cast<uint32_t*>(workspace);
-  base.wait_limit_ns = beam::host::wait_limit_ns();
+  beam::OrthoChainArgs o = {};
   // results leave by bulk copy; the caller's `out` where its rows allow it
-  CUtensorMap og, op, ox[2], oo = {};
-  if (!staged_out(&og, gram, F16, m, m, batch, L.ldm, m * L.ldm, nt_gram) ||
-      !staged_out(&op, poly, F16, m, m, batch, L.ldm, m * L.ldm, nt_poly) ||
-      !staged_out(&ox[0], x[0], F16, C, R, batch, L.ld, R * L.ld, nt_step) ||
-      !staged_out(&ox[1], x[1], F16, C, R, batch, L.ld, R * L.ld, nt_step))
-    return BEAM_ERR_CUDA;
-  const bool out_staged = staged_out(&oo, out, d->out_dtype, C, R, batch, C, R * C, nt_step);
-  for (int t = 0; t < d->steps; ++t) {
-    const bool last = t + 1 == d->steps;
-    const int cur = t & 1;
-    ProductArgs g = base;  // A = X X^T (wide) or X^T X (tall)
-    g.M = g.N = static_cast<int32_t>(m);
-    g.k_blocks = static_cast<int32_t>((std::max(R, C) + 63) / 64);
-    g.k_wrap = g.k_blocks;
-    g.out = gram;
-    g.ld_out = L.ldm;
-    g.z_out = m * L.ldm;
-    g.symmetric = 1;
-    g.staged = 1;
-    g.alpha = t == 0 ? 1.f : kScaleGram / (kScaleX * kScaleX);
-    g.alpha_z = t == 0 ? n.alpha_gram : nullptr;
-    cudaError_t e = beam::launch_pair_product(beam::kProductDense, nt_gram, !wide, !wide, ga[cur],
-                                              gb[cur], og, g, s);
-    if (e != cudaSuccess) return BEAM_ERR_CUDA;
-
-    ProductArgs q = base;  // P = a I + b A + c A A
-    q.M = q.N = static_cast<int32_t>(m);
-    q.k_blocks = static_cast<int32_t>((m + 63) / 64);
-    q.k_wrap = q.k_blocks;
-    q.out = poly;
-    q.ld_out = L.ldm;
-    q.z_out = m * L.ldm;
-    q.symmetric = 1;
-    q.staged = 1;
-    q.alpha = kScalePoly * d->c / (kScaleGram * kScaleGram);
-    q.beta = kScalePoly * d->b / kScaleGram;
-    q.diag = kScalePoly * d->a;
-    q.add = gram;
-    e = beam::launch_pair_product(beam::kProductDense, nt_poly, false, false, pa, pb, op, q, s);
-    if (e != cudaSuccess) return BEAM_ERR_CUDA;
-
-    ProductArgs u = base;  // X <- P X (wide) or X P (tall)
-    u.M = d->cols;
-    u.N = d->rows;
-    u.k_blocks = q.k_blocks;
-    u.k_wrap = q.k_blocks;
-    if (t == 0 && split) {
-      u.k_blocks *= 2;
-      (wide ? u.wrap_za : u.wrap_zb) = d->batch;
-    }
-    u.out = last ? out : x[cur ^ 1];
-    u.staged = !last || out_staged ? 1 : 0;
-    u.out_type = last ? d->out_dtype : F16;
-    u.ld_out = last ? C : L.ld;
-    u.z_out = last ? R * C : R * L.ld;
-    const float out_scale = last ? 1.f : kScaleX;
-    u.alpha = t == 0 ? 1.f : out_scale / (kScalePoly * kScaleX);
-    u.alpha_z = t == 0 ? n.alpha_step : nullptr;
-    e = wide ? beam::launch_pair_product(beam::kProductDense, nt_step, true, false, sx[cur], sp,
-                                         last ? oo : ox[cur ^ 1], u, s)
-             : beam::launch_pair_product(beam::kProductDense, nt_step, false, false, sp, sx[cur],
-                                         last ? oo : ox[cur ^ 1], u, s);
-    if (e != cudaSuccess) return BEAM_ERR_CUDA;
-  }
-  return BEAM_OK;
+  o.out_staged = staged_out(&maps.out, out, d->out_dtype, C, R, batch, C, R * C) ? 1 : 0;
+  o.batch = d->batch;
+  o.rows = d->rows;
+  o.cols = d->cols;
+  o.m = static_cast<int32_t>(m);
+  o.steps = d->steps;
+  o.split = split ? 1 : 0;
+  o.ld = L.ld;
+  o.ldm = L.ldm;
+  o.x[0] = x[0];
+  o.x[1] = x[1];
+  o.gram = gram;
+  o.poly = poly;
+  o.out = out;
+  o.out_type = d->out_dtype;
+  o.alpha_gram = n.alpha_gram;
+  o.alpha_step = n.alpha_step;
+  o.a = d->a;
+  o.b = d->b;
+  o.c = d->c;
+  o.done = n.done;
+  o.status = static_cast<uint32_t*>(workspace);
+  o.wait_limit_ns = beam::host::wait_limit_ns();
+  return launched(beam::launch_ortho_chain(nt, maps, o, s));
 }
 
 }  // extern "C"

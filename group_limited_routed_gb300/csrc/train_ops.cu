@@ -345,6 +345,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormArgs p) {
     const float inv = inverse_norm(amax, acc, k, p.eps);
     p.alpha_gram[z] = p.scale_gram * inv * inv;
     p.alpha_step[z] = p.scale_step * inv;
+    p.done[z] = 0;
   }
 }
 

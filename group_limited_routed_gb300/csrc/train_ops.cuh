@@ -59,6 +59,7 @@ struct NormArgs {
   int64_t ld;
   float* alpha_gram;       // [batch] scale_gram / norm^2
   float* alpha_step;       // [batch] scale_step / norm
+  uint32_t* done;          // [batch] set to zero
   float scale_gram, scale_step, eps;
 };
 // Two launches: magnitudes with sums of squares, the scaled F16 copy with the norms.
