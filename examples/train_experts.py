@@ -1,0 +1,51 @@
+"""Fit the experts of the small layer to another layer's outputs.
+
+    python examples/train_experts.py [steps]
+
+Each step routes a batch with the serving router, runs the experts forward and
+backward (grouped products with both gradients, the gated activation with the
+routing weight), and updates the three weight stacks with orthogonalised
+momentum.  Prints the loss, relative to the target's power.
+"""
+import os
+import sys
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+import torch  # noqa: E402
+
+import group_limited_routed_gb300 as pkg  # noqa: E402
+from group_limited_routed_gb300 import inputs, training  # noqa: E402
+
+
+def main(steps: int = 60, seed: int = 0) -> list[float]:
+    cfg = inputs.CONFIGS["tiny"].replace(T=1024)
+    t = inputs.generate(cfg, "cuda")
+    names = ("w_gate", "w_up", "w_down")
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    # the student starts elsewhere: fresh draws of the same distribution
+    params = [torch.nn.Parameter(torch.empty_like(t[n]).normal_(0, 0.02, generator=g))
+              for n in names]
+    momenta = [torch.zeros(p.shape, dtype=torch.float32, device="cuda") for p in params]
+    ws = pkg.Workspace(cfg, cfg.T)
+    losses = []
+    for step in range(steps):
+        x = torch.randn(cfg.T, cfg.d, generator=g, device="cuda").bfloat16()
+        idx, w = pkg.route(cfg, x, t["router_w"], t["corr_bias"], ws=ws)
+        target = pkg.forward_routed(cfg, x, idx, w, *(t[n] for n in names), ws=ws).float()
+        out = training.experts(x, idx, w, *params)
+        loss = (out.float() - target).square().mean() / target.square().mean()
+        loss.backward()
+        lr = 0.02 * (1 - step / steps)
+        for p, m in zip(params, momenta):
+            training.muon_step(p, p.grad, m, lr)
+            p.grad = None
+        losses.append(loss.item())
+        if step % 10 == 0 or step + 1 == steps:
+            print(f"step {step:4d}  loss {losses[-1]:.4f}")
+    assert pkg.check_status(ws) == 0
+    return losses
+
+
+if __name__ == "__main__":
+    main(int(sys.argv[1]) if len(sys.argv) > 1 else 60)

@@ -1,0 +1,130 @@
+"""Training the routed experts: autograd around the package's own products.
+
+The layer's serving entry points keep nothing for a backward pass.  These
+functions run the same experts -- gather, SwiGLU with the routing weight,
+down, combine -- from the operators that have gradients (``grouped_matmul``,
+``swiglu``) and update stacked weights with ``orthogonalize``.  Routing comes
+from the serving side (``route``): choices are data, weights may be trained
+through.  All sums over rows run in a fixed order.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import api
+
+
+class _GroupedMatmul(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, offsets, out_dtype):
+        ctx.save_for_backward(x, w, offsets)
+        return api.grouped_matmul(x, w, offsets, out_dtype=out_dtype)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, offsets = ctx.saved_tensors
+        dy = dy.to(x.dtype).contiguous()
+        dx = api.grouped_matmul_dx(dy, w, offsets) if ctx.needs_input_grad[0] else None
+        dw = api.grouped_matmul_dw(dy, x, offsets) if ctx.needs_input_grad[1] else None
+        return dx, dw, None, None
+
+
+def grouped_linear(x, w, offsets, out_dtype=None):
+    """``grouped_matmul`` with gradients for x [rows, K] and w [E, N, K].  An
+    FP32 result's gradient is rounded to x's type before the products."""
+    return _GroupedMatmul.apply(x, w, offsets, out_dtype)
+
+
+class _SwiGLU(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate, up, row_weight):
+        ctx.save_for_backward(gate, up, row_weight)
+        return api.swiglu(gate, up, row_weight)
+
+    @staticmethod
+    def backward(ctx, dh):
+        gate, up, row_weight = ctx.saved_tensors
+        got = api.swiglu_grad(dh.contiguous(), gate, up, row_weight)
+        return got[0], got[1], None if row_weight is None else got[2]
+
+
+def gated_rows(gate, up, row_weight=None):
+    """``swiglu`` with gradients for gate, up and row_weight."""
+    return _SwiGLU.apply(gate, up, row_weight)
+
+
+def sort_rows(topk_idx, n_experts: int):
+    """Order (token, slot) pairs by expert, then token, then slot.
+
+    Returns (pairs, place, offsets): pairs[row] = token * topk + slot of each
+    permuted row, place its inverse, offsets int32 [n_experts + 1]."""
+    flat = topk_idx.reshape(-1).long()
+    pairs = torch.sort(flat, stable=True).indices
+    place = torch.empty_like(pairs)
+    place[pairs] = torch.arange(pairs.numel(), device=pairs.device)
+    counts = torch.bincount(flat, minlength=n_experts)
+    offsets = torch.zeros(n_experts + 1, dtype=torch.int32, device=flat.device)
+    offsets[1:] = counts.cumsum(0)
+    return pairs, place, offsets
+
+
+class _Dispatch(torch.autograd.Function):
+    """Token rows [T, d] -> permuted rows [T * k, d]; the gradient adds a
+    token's k rows in slot order, in FP32."""
+
+    @staticmethod
+    def forward(ctx, hidden, pairs, place, topk):
+        ctx.save_for_backward(place)
+        ctx.topk = topk
+        return hidden[pairs // topk]
+
+    @staticmethod
+    def backward(ctx, drows):
+        (place,) = ctx.saved_tensors
+        per_token = drows[place].view(-1, ctx.topk, drows.shape[1])
+        return per_token.float().sum(1).to(drows.dtype), None, None, None
+
+
+class _Combine(torch.autograd.Function):
+    """Permuted expert rows [T * k, d] -> tokens [T, d]: the FP32 sum over a
+    token's slots in order, rounded once."""
+
+    @staticmethod
+    def forward(ctx, rows, pairs, place, topk, dtype):
+        ctx.save_for_backward(pairs)
+        ctx.topk, ctx.dtype = topk, rows.dtype
+        return rows[place].view(-1, topk, rows.shape[1]).float().sum(1).to(dtype)
+
+    @staticmethod
+    def backward(ctx, dout):
+        (pairs,) = ctx.saved_tensors
+        return dout[pairs // ctx.topk].to(ctx.dtype), None, None, None, None
+
+
+def experts(hidden, topk_idx, topk_w, w_gate, w_up, w_down):
+    """The routed experts of a given routing, with gradients for hidden
+    [T, d], topk_w [T, k] (FP32) and the three weights.
+
+    As ``forward_routed``, except that the routing weight multiplies the
+    activation before the down product (the same number, and its gradient
+    comes with the activation's)."""
+    T, topk = topk_idx.shape
+    pairs, place, offsets = sort_rows(topk_idx, w_gate.shape[0])
+    rows = _Dispatch.apply(hidden, pairs, place, topk)
+    gate = grouped_linear(rows, w_gate, offsets)
+    up = grouped_linear(rows, w_up, offsets)
+    h = gated_rows(gate, up, topk_w.reshape(-1)[pairs])
+    y = grouped_linear(h, w_down, offsets, out_dtype=torch.float32)
+    return _Combine.apply(y, pairs, place, topk, hidden.dtype)
+
+
+@torch.no_grad()
+def muon_step(weight, grad, momentum, lr: float, beta: float = 0.95, steps: int = 5, ws=None):
+    """One Muon update of stacked weights [..., R, C] in place: momentum (FP32)
+    <- beta momentum + grad, weight <- weight - lr sqrt(max(1, R / C))
+    orthogonalize(grad + beta momentum)."""
+    momentum.mul_(beta).add_(grad.to(momentum.dtype))
+    step = api.orthogonalize(torch.add(grad, momentum, alpha=beta).to(momentum.dtype),
+                             steps=steps, out_dtype=torch.bfloat16, ws=ws)
+    R, C = weight.shape[-2:]
+    weight.add_(step.to(weight.dtype), alpha=-lr * max(1.0, R / C) ** 0.5)
