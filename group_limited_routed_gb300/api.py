@@ -840,12 +840,21 @@ def _raw_stream(stream, index: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _temporary(t: torch.Tensor, stream) -> torch.Tensor:
-    """Memory this module allocated for a call on a stream that is not the
-    current one: the allocator must not hand it out before that work is done."""
-    if isinstance(stream, torch.cuda.Stream):
-        t.record_stream(stream)
-    return t
+def _on(stream, device):
+    """A context in which torch allocates (and copies) on the call's stream:
+    memory it hands out there is free of the current stream's pending work."""
+    if stream is None:
+        return _HERE_ALREADY
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_raw_stream(stream, device.index), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _grouped_desc(rows, E, N, K, dtype, out_dtype, x_ld, y_ld, w_strides) -> _Grouped:
@@ -897,9 +906,9 @@ def grouped_matmul_workspace_size(rows: int, n_groups: int, N: int, K: int,
 
 def _grouped_ws(d, a, b, stream) -> OpWorkspace:
     """A workspace for one call, when the caller keeps none."""
-    ws = OpWorkspace(_grouped_size(d, bool(a.data_ptr() % 16 or b.data_ptr() % 16)), a.device)
-    _temporary(ws.buf, stream)
-    return ws
+    with _on(stream, a.device):
+        return OpWorkspace(_grouped_size(d, bool(a.data_ptr() % 16 or b.data_ptr() % 16)),
+                           a.device)
 
 
 @_plans
@@ -926,9 +935,7 @@ def _rows_call(transpose, a, w, offsets, out, out_dtype, ws, stream):
         transpose, _meta(a, "dy" if transpose else "x"), _meta(w, "w"), _meta(offsets, "offsets"),
         None if out is None else _meta(out, "out"), out_dtype)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=device)
-        if stream is not None:
-            _temporary(out, stream)
+        out = _empty(shape, dt, device, stream)
     if ws is None:
         ws = _grouped_ws(d, a, w, stream)
     return ref, out, ws, device
@@ -992,9 +999,7 @@ def grouped_matmul_dw(dy, x, offsets, out=None, accumulate: bool = False, out_dt
                                       None if out is None else _meta(out, "out"),
                                       bool(accumulate), out_dtype)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
-        if stream is not None:
-            _temporary(out, stream)
+        out = _empty(shape, dt, dev, stream)
     if ws is None:
         ws = _grouped_ws(d, dy, x, stream)
     with _current(dev):
@@ -1022,10 +1027,9 @@ def _gate_plan(gate, up, row_weight, dh, outs):
 
 
 def _like(t, stream):
-    out = torch.empty_like(t, memory_format=torch.contiguous_format)
     if stream is not None:
-        _temporary(out, stream)
-    return out
+        return _empty(t.shape, t.dtype, t.device, stream)
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def swiglu(gate, up, row_weight=None, out=None, stream=None):
@@ -1117,19 +1121,16 @@ def orthogonalize(m, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: floa
         _meta(m, "m"), int(steps), tuple(float(v) for v in coeffs), float(eps),
         None if out is None else _meta(out, "out"), out_dtype)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
-        if stream is not None:
-            _temporary(out, stream)
+        out = _empty(shape, dt, dev, stream)
     if d is None:
         return out
     stack = m
     if m.dim() > 3:
-        stack = m.reshape(d.batch, d.rows, d.cols)
-        if stack.data_ptr() != m.data_ptr() and stream is not None:
-            _temporary(stack, stream)
+        with _on(stream, dev):
+            stack = m.reshape(d.batch, d.rows, d.cols)
     if ws is None:
-        ws = OpWorkspace(orthogonalize_workspace_size(d.batch, d.rows, d.cols, m.dtype), dev)
-        _temporary(ws.buf, stream)
+        with _on(stream, dev):
+            ws = OpWorkspace(orthogonalize_workspace_size(d.batch, d.rows, d.cols, m.dtype), dev)
     with _current(dev):
         _check(lib().beam_moe_orthogonalize(ref, stack.data_ptr(), out.data_ptr(), ws.ptr,
                                             ws.nbytes, _raw_stream(stream, dev.index)),

@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if (warp == 0) {
     // -------------------------------------------------------------- producer
     const uint64_t pol = ptx::policy_evict_normal();
-    const bool elected = ptx::elect_one();
+    const bool elected = elect_one();
     uint32_t used = 0, parities = 0;  // bit s: stage s was filled, its last phase
     int seen_z = -1;
     uint32_t seen_after = 0;
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const uint64_t a_k0 = ptx::sdesc_sw128(ring), a_mn0 = sdesc_mn_sw128(ring);
       const uint64_t b_k0 = ptx::sdesc_sw128(ring + kPABytes);
       const uint64_t b_mn0 = sdesc_mn_sw128(ring + kPABytes);
-      const bool elected = ptx::elect_one();
+      const bool elected = elect_one();
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int c = 0; c < COLS; c += 32) {
         if (c < ncols) {
           uint32_t r[32];
-          ptx::tmem_ld32(tq + c, r);
+          tmem_ld32(tq + c, r);
           ptx::tmem_wait_ld();
 #pragma unroll
           for (int u = 0; u < 32; u += 2) {

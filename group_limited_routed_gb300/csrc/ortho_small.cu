@@ -32,13 +32,12 @@
 #include "gemm_common.cuh"
 #include "launch_once.cuh"
 #include "ortho_scale.cuh"
+#include "pair_common.cuh"
 #include "pair_product.cuh"
 #include "ptx.cuh"
 
 namespace beam {
 namespace {
-
-using gemm::Waiter;
 
 constexpr int kThreads = 512;
 constexpr int kWarpCols = 128 / (kThreads / 128);  // columns of A and P per warp
@@ -256,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
 
   const Waiter W{abort_flag, p.status, p.wait_limit_ns};
   // warp 0 walks the products as a whole, one lane of it issues
-  const bool elected = ptx::elect_one();
+  const bool elected = elect_one();
   uint32_t phase = 0;
   constexpr uint32_t kF16Idesc = (1u << 4) | ((128u >> 4) << 24);  // F16 A and B, FP32 D, M = 128
   const uint32_t idesc_m16 = kF16Idesc | (static_cast<uint32_t>(m16 >> 3) << 17);

@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // one elected lane arms the barriers and issues the copies.
     {
       const uint64_t pol = ptx::policy_evict_normal();
-      const bool elected = ptx::elect_one();
+      const bool elected = elect_one();
       uint32_t used = 0, parities = 0;  // bit s: stage s was filled, its last phase
       int stage = 0;
       uint32_t phase = 0;
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const uint64_t b_desc0 =
           B_MN ? sdesc_mn_sw128(ring + kPABytes) : ptx::sdesc_sw128(ring + kPABytes);
       constexpr uint32_t A_STEP = (A_MN ? 2048 : 32) >> 4, B_STEP = (B_MN ? 2048 : 32) >> 4;
-      const bool elected = ptx::elect_one();
+      const bool elected = elect_one();
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;

@@ -298,6 +298,71 @@ def test_repeats_streams_and_graphs(pkg):
         assert torch.equal(a, b)
 
 
+def test_a_stream_of_the_callers_choice(pkg):
+    """Outputs and workspaces that the call itself allocates belong to the
+    stream it runs on, also when that is not the current one."""
+    g = gen(31)
+    counts = [9, 0, 61, 130]
+    off = bounds(counts)
+    x, w, dy = randn(g, 200, 131), randn(g, 4, 65, 131), randn(g, 200, 65)  # copies needed
+    m = randn(g, 2, 3, 40, 70).transpose(0, 1)                              # a copy needed
+    want = [pkg.grouped_matmul(x, w, off), pkg.grouped_matmul_dx(dy, w, off),
+            pkg.grouped_matmul_dw(dy, x, off), pkg.swiglu(dy, dy),
+            pkg.swiglu_grad(dy, dy, dy)[0], pkg.orthogonalize(m)]
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        s.wait_stream(torch.cuda.current_stream())
+        got = [pkg.grouped_matmul(x, w, off, stream=stream),
+               pkg.grouped_matmul_dx(dy, w, off, stream=stream),
+               pkg.grouped_matmul_dw(dy, x, off, stream=stream),
+               pkg.swiglu(dy, dy, stream=stream),
+               pkg.swiglu_grad(dy, dy, dy, stream=stream)[0],
+               pkg.orthogonalize(m, stream=stream)]
+        s.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
+def test_no_group_has_a_row(pkg):
+    g = gen(37)
+    x, dy, w = randn(g, 5, 64), randn(g, 5, 32), randn(g, 3, 32, 64)
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    assert (pkg.grouped_matmul(x, w, off) == 0).all()
+    assert (pkg.grouped_matmul_dx(dy, w, off, out_dtype=torch.float32) == 0).all()
+    assert (pkg.grouped_matmul_dw(dy, x, off) == 0).all()
+    assert (pkg.grouped_matmul_dw(dy, x, off, out_dtype=torch.float32) == 0).all()
+
+
+def test_back_to_back_calls_wait_for_one_another(pkg):
+    """Calls launched early behind one another (programmatic serialization)
+    read what the call before wrote: a chain equals its single steps."""
+    g = gen(41)
+    off = bounds([33, 0, 90, 5])
+    x, w = randn(g, 128, 256), randn(g, 4, 256, 256, scale=0.05)
+    m = randn(g, 3, 100, 160)
+
+    def chain(wait):
+        y = x
+        out = []
+        for _ in range(4):
+            y = pkg.grouped_matmul(y, w, off)
+            wait()
+            h = pkg.swiglu(y, y)
+            wait()
+            y = pkg.grouped_matmul_dx(h, w, off)
+            wait()
+            out.append(pkg.grouped_matmul_dw(h, y, off))
+            wait()
+        out.append(pkg.orthogonalize(pkg.orthogonalize(m)))
+        wait()
+        out.append(pkg.orthogonalize(out[0][:, :200].contiguous()))
+        return out + [y]
+    single = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        for a, b in zip(single, chain(lambda: None)):
+            assert torch.equal(a, b)
+
+
 # -------------------------------------------------------------- activation
 def plain_gate(g, u, w):
     return w[:, None] * g * torch.sigmoid(g) * u
