@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
   const uint32_t idesc_m16 = kF16Idesc | (static_cast<uint32_t>(m16 >> 3) << 17);
   // writes of shared memory -> the tensor core's reads
   auto publish = [&] {
-    asm volatile("fence.proxy.async;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
       const uint32_t to = g_at + word_at(c, r4 >> 3) + (r4 & 4) * 2;
       for (int q = 0; q < cs; ++q) store_peer2(cs > 1 ? ptx::map_to_rank(to, q) : to, lo, hi);
     }
-    asm volatile("fence.proxy.async;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
     if (cs > 1) ptx::cluster_sync();
     // ----------------------------------------------------- P = aI + bA + cA^2
     publish();
