@@ -274,6 +274,15 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
   const int quarter = warp & 3, part = warp >> 2;
   const int row = quarter * 32 + lane;  // TMEM lane
   const uint32_t tq = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  // the squared norm is the trace of the copy's A: FP32 sums in an order that
+  // no memory layout of the update changes
+  auto norm = [&] {
+    float sum = 0.f;
+    for (int k = lane; k < m16; k += 32) sum += squares[k];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    inv = amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : 1.f / (sqrtf(sum) + p.eps * k0);
+  };
   const bool vector_out = p.ocol == 1 && p.orow % 8 == 0 && p.oz % 8 == 0 &&
                           (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
 
@@ -291,62 +300,83 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
       __syncwarp();
     }
     finish();
-    // partial sums, one column of 128 rows after another (A is symmetric:
-    // column c is also row c)
-    for (int c = part * kWarpCols; c < min(m16, (part + 1) * kWarpCols); c += 16) {
-      uint32_t r[16];
-      ptx::tmem_ld16(tq + c, r);
-      ptx::tmem_wait_ld();
+    if (cs == 1) {
+      // the whole sum is here: its trace, then A straight from TMEM
+      if (t == 0) {
+        for (int c = part * kWarpCols; c < min(m16, (part + 1) * kWarpCols); c += 16) {
+          uint32_t r[16];
+          ptx::tmem_ld16(tq + c, r);
+          ptx::tmem_wait_ld();
 #pragma unroll
-      for (int u = 0; u < 16; ++u)
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(part_at + ((c + u) * 128 + row) * 4), "r"(r[u])
-                     : "memory");
-    }
-    ptx::tc_fence_before();
-    if (cs > 1)
-      ptx::cluster_sync();
-    else
-      __syncthreads();
-    ptx::tc_fence_after();
-    if (t == 0) {
-      // the squared norm is the trace of the copy's A: FP32 sums in an order
-      // that no memory layout of the update changes
-      if (threadIdx.x < 128) {
-        float d = 0.f;
-        if (threadIdx.x < static_cast<unsigned>(m16)) {
-          const uint32_t from = part_at + threadIdx.x * (128 + 1) * 4;
-          for (int q = 0; q < cs; ++q)
-            d += __uint_as_float(load_peer(cs > 1 ? ptx::map_to_rank(from, q) : from));
+          for (int u = 0; u < 16; ++u)
+            if (c + u == row) squares[row] = __uint_as_float(r[u]);
         }
-        squares[threadIdx.x] = d;
+        __syncthreads();
+        norm();
       }
-      __syncthreads();
-      float sum = 0.f;
-      for (int k = lane; k < 128; k += 32) sum += squares[k];
+      const float gram_scale = t == 0 ? kScaleGram * inv * inv : kScaleGram / (kScaleX * kScaleX);
+      for (int c = part * kWarpCols; c < min(m16, (part + 1) * kWarpCols); c += 16) {
+        uint32_t r[16];
+        ptx::tmem_ld16(tq + c, r);
+        ptx::tmem_wait_ld();
+        uint32_t o[8];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      inv = amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : 1.f / (sqrtf(sum) + p.eps * k0);
-    }
-    const float gram_scale = t == 0 ? kScaleGram * inv * inv : kScaleGram / (kScaleX * kScaleX);
-    // this CTA's share of A: words of 4 rows of columns c = rank, rank + cs, ...
-    const int quads = m16 / 4;
-    const int mine = (m16 - static_cast<int>(rank) + cs - 1) / cs;
-    for (int at = threadIdx.x; at < mine * quads; at += kThreads) {
-      const int c = static_cast<int>(rank) + at / quads * cs;
-      const int r4 = at % quads * 4;
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int q = 0; q < cs; ++q) {
-        const uint32_t from = part_at + (c * 128 + r4) * 4;
-        const float4 v = load_peer4(cs > 1 ? ptx::map_to_rank(from, q) : from);
-        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        for (int u = 0; u < 8; ++u)
+          o[u] = half2_bits(__uint_as_float(r[2 * u]) * gram_scale,
+                            __uint_as_float(r[2 * u + 1]) * gram_scale);
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           g_at + word_at(row, (c >> 3) + w)),
+                       "r"(o[4 * w]), "r"(o[4 * w + 1]), "r"(o[4 * w + 2]), "r"(o[4 * w + 3])
+                       : "memory");
       }
-      const uint32_t lo = half2_bits(s.x * gram_scale, s.y * gram_scale);
-      const uint32_t hi = half2_bits(s.z * gram_scale, s.w * gram_scale);
-      const uint32_t to = g_at + word_at(c, r4 >> 3) + (r4 & 4) * 2;
-      for (int q = 0; q < cs; ++q) store_peer2(cs > 1 ? ptx::map_to_rank(to, q) : to, lo, hi);
+    } else {
+      // partial sums, one column of 128 rows after another (A is symmetric:
+      // column c is also row c)
+      for (int c = part * kWarpCols; c < min(m16, (part + 1) * kWarpCols); c += 16) {
+        uint32_t r[16];
+        ptx::tmem_ld16(tq + c, r);
+        ptx::tmem_wait_ld();
+#pragma unroll
+        for (int u = 0; u < 16; ++u)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(part_at + ((c + u) * 128 + row) * 4),
+                       "r"(r[u])
+                       : "memory");
+      }
+      ptx::tc_fence_before();
+      ptx::cluster_sync();
+      ptx::tc_fence_after();
+      if (t == 0) {
+        if (threadIdx.x < static_cast<unsigned>(m16)) {
+          float d = 0.f;
+          const uint32_t from = part_at + threadIdx.x * (128 + 1) * 4;
+          for (int q = 0; q < cs; ++q) d += __uint_as_float(load_peer(ptx::map_to_rank(from, q)));
+          squares[threadIdx.x] = d;
+        }
+        __syncthreads();
+        norm();
+      }
+      const float gram_scale = t == 0 ? kScaleGram * inv * inv : kScaleGram / (kScaleX * kScaleX);
+      // this CTA's share of A: words of 4 rows of columns c = rank, rank + cs, ...
+      const int quads = m16 / 4;
+      const int mine = (m16 - static_cast<int>(rank) + cs - 1) / cs;
+      for (int at = threadIdx.x; at < mine * quads; at += kThreads) {
+        const int c = static_cast<int>(rank) + at / quads * cs;
+        const int r4 = at % quads * 4;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int q = 0; q < cs; ++q) {
+          const float4 v = load_peer4(ptx::map_to_rank(part_at + (c * 128 + r4) * 4, q));
+          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        const uint32_t lo = half2_bits(s.x * gram_scale, s.y * gram_scale);
+        const uint32_t hi = half2_bits(s.z * gram_scale, s.w * gram_scale);
+        const uint32_t to = g_at + word_at(c, r4 >> 3) + (r4 & 4) * 2;
+        for (int q = 0; q < cs; ++q) store_peer2(ptx::map_to_rank(to, q), lo, hi);
+      }
+      asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+      ptx::cluster_sync();
     }
-    asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
-    if (cs > 1) ptx::cluster_sync();
     // ----------------------------------------------------- P = aI + bA + cA^2
     publish();
     if (warp == 0) {
@@ -547,10 +577,12 @@ bool ortho_small_shape(int32_t batch, int32_t m, int32_t n, int32_t type, int nu
   if (least > kOrthoSmallCluster) return false;
   // clusters of more than 8 CTAs depend on the device
   if (least > 8 && !large_clusters(type)) return false;
-  // more CTAs than needed while the stack leaves SMs free and a slice has
-  // more than 64 columns
+  // One CTA needs no exchange (128 x 128, five steps: 21 us in one CTA, 33 in
+  // two).  Beyond, more CTAs than needed while the stack leaves SMs free and
+  // a slice has more than 64 columns, for the loads and epilogues (64 x 512:
+  // 28 us in 2 CTAs, 26 in 8; 128 x 300, FP32: 69 us in 2, 53 in 5).
   int32_t c = least;
-  while (c < 8 && batch * (c + 1) <= num_sms && (n + c - 1) / c > 64) ++c;
+  while (c > 1 && c < 8 && batch * (c + 1) <= num_sms && (n + c - 1) / c > 64) ++c;
   *cluster = c;
   *slice = ((n + c - 1) / c + 63) / 64 * 64;
   // whole slices of 64 may need fewer CTAs than c
