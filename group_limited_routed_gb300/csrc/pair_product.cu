@@ -74,7 +74,6 @@ cudaError_t launch_pair_product(int kind, int nt, bool a_mn, bool b_mn, const CU
     // at most one ragged block more than rows / nt per group that has rows
     const int64_t tiles = mt * (p.rows / nt + std::min(p.groups, p.rows));
     switch (nt) {
-      case 32: return launch_rows<32>(a_mn, a, b, out, p, tiles, s);
       case 64: return launch_rows<64>(a_mn, a, b, out, p, tiles, s);
       case 128: return launch_rows<128>(a_mn, a, b, out, p, tiles, s);
       case 256: return launch_rows<256>(a_mn, a, b, out, p, tiles, s);

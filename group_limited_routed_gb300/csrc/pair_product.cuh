@@ -42,16 +42,15 @@ struct ProductArgs {
 constexpr int kProductTileM = 256;
 constexpr int kProductMaxGroups = 1024;
 
-// Rows j of one box of a k-contiguous B (nt / 2 where that is less).
+// Rows j of one box of a k-contiguous B.
 constexpr int kProductBoxRows = 32;
 inline int product_out_rows(bool f32) { return f32 ? 16 : 32; }
-inline int product_box_rows(int nt) { return nt / 2 < kProductBoxRows ? nt / 2 : kProductBoxRows; }
 
-// nt: rows j per tile, 32, 64, 128 or 256 (kProductGroups: 256).  a_mn, b_mn:
+// nt: rows j per tile, 64, 128 or 256 (kProductGroups: 256).  a_mn, b_mn:
 // the operand's contiguous axis is i (j) rather than k.  Tensor maps are
 // three-dimensional (contiguous, row, z); a and b with 128-byte swizzle and
 // boxes 64 x 128 (a, k contiguous), 64 x 64 (a_mn, b_mn), 64 x
-// product_box_rows(nt) (b, k contiguous); out (only read with p.staged)
+// kProductBoxRows (b, k contiguous); out (only read with p.staged)
 // without swizzle, boxes 32 x product_out_rows.
 cudaError_t launch_pair_product(int kind, int nt, bool a_mn, bool b_mn, const CUtensorMap& a,
                                 const CUtensorMap& b, const CUtensorMap& out,

@@ -28,9 +28,32 @@
 // Sums: FP32 in TMEM.  A chain of MMAs into one accumulator truncates at
 // every step, an error that grows with the chain and reaches 1e-5 relative
 // over thousands of k.  16-bit outputs round at 2^-9 or 2^-12 and take one
-// chain; FP32 outputs (kWide) restart the accumulator every kWideBlocks k
+// chain; FP32 outputs (WIDE) restart the accumulator every kWideBlocks k
 // blocks, alternating the two TMEM buffers, and the epilogue warps add the
-// pieces in FP32 registers.
+// pieces in FP32 registers (the truncation adds 1.3e-8 of the sum per step:
+// chains of 512 k leave an error of 4.7e-7 of the result's norm, of 256 k
+// 2.3e-7 at twice the drains).
+//
+// Measured on a GB300.  Full tiles (8 groups x 4096 rows, 5120 -> 5120): 896
+// us, 1918 TFLOP/s, as fast as the library's dense product (1910 to 1970); the
+// tensor cores are busy 98 % of the cycles and the power limit holds the clock
+// near 1.5 GHz.  Ragged blocks are bound by the loads: a k block of n rows
+// moves 16 KB + 64 n bytes into each SM for 2 n cycles of MMA, and the L2
+// gives an SM about 95 GB/s (192 KB of ring over a loaded latency of 2 us).  A
+// decode batch streams weights at 7.1 TB/s.  Weight gradients of small groups
+// are bound by their stores: 16 x 256 rows, 2560 x 5120 in FP32 149 us, 6.1
+// TB/s.
+//
+// What made the difference, step by step: one elected lane of a uniform warp
+// issues MMAs and copies (a divergent lane's address moves cost 700 cycles per
+// k block instead of 520); freeing an accumulator without a release (a release
+// at cluster scope waits for the warp's global stores, 3000 cycles per tile);
+// stores of weight gradients through shared memory, written by the copy
+// engine.  Tried and dropped: two row blocks of a group per tile sharing A
+// (both TMEM buffers in one tile leave the epilogue exposed: 1024-row groups
+// 518 -> 527 us, 600-row groups 370 -> 450); row blocks in steps of 64 rows,
+// whole load boxes (400-row groups 229 -> 245 us: uneven blocks); finding the
+// producer's next tile ahead (no change).
 //
 // Every wait is bounded (gemm::Waiter); after an abort all roles still reach
 // the cluster barrier that precedes the release of TMEM.
@@ -56,14 +79,20 @@ using gemm::Waiter;
 
 constexpr int kWideBlocks = 8;  // k blocks per accumulator chain, FP32 outputs
 
+// DUAL (16-bit weight gradients): a tile takes two blocks of NT rows j, one per
+// TMEM buffer, that share the stage's A -- 48 KB per k block for what two
+// tiles load as 64 KB, where the loads are what a tile waits for (16 x 1024
+// rows, 2560 x 5120: 293 -> 263 us; 16 x 256 rows 112 -> 110).
 template <int NT, int KIND, bool WIDE, bool DUAL>
 struct ProductCfg {
   static constexpr bool STAGED = KIND == kProductGroups || WIDE;
   static constexpr uint32_t B_BYTES = NT / 2 * 128;  // one block of rows
   static constexpr uint32_t STAGE = kPABytes + (DUAL ? 2 : 1) * B_BYTES;
-  static constexpr int S_RAW = static_cast<int>((kPRing + (DUAL ? 8192 : 0) - (STAGED ? kStaging : 0)) / STAGE);
+  // DUAL stages are 48 KB: 8 KB more than the ring make it four of them
+  static constexpr int S_RAW = static_cast<int>(
+      (kPRing + (DUAL ? 8192 : 0) - (STAGED ? kStaging : 0)) / STAGE);
   static constexpr int S = S_RAW > 12 ? 12 : S_RAW;
-  static constexpr uint32_t TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
+  static constexpr uint32_t TMEM_COLS = 2 * NT;
   static constexpr uint32_t NUM_BARS = 4 * S + 5;
   // group boundaries and first tiles in shared memory (kProductGroups reads
   // the boundaries where they are)
@@ -343,7 +372,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const int i = t.i0 + static_cast<int>(rank) * 128;
         const int j = t.j0 + static_cast<int>(rank) * (t.n_mma / 2);
         // k-contiguous B comes in boxes of BOX rows, as many as the tile has
-        constexpr int BOX = NT / 2 < kProductBoxRows ? NT / 2 : kProductBoxRows;
+        constexpr int BOX = kProductBoxRows;
         const int boxes = (t.n_mma / 2 + BOX - 1) / BOX;
         const int n2 = (t.nvalid2 + 15) & ~15;
         const int j2 = t.j0 + t.nvalid + static_cast<int>(rank) * (n2 / 2);
@@ -569,7 +598,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;  // TMEM lane quarter this warp may access
     constexpr int GROUPS = kPEpiWarps / 4;
-    constexpr int COLS = NT / GROUPS < 16 ? 16 : NT / GROUPS;  // rows j per warp
+    constexpr int COLS = NT / GROUPS;  // rows j per warp
     const int col_begin = ((warp - 3) >> 2) * COLS;
     // TMEM columns per load
     constexpr int LD = COLS < 32 ? 16 : 32;

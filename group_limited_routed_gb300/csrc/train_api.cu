@@ -161,13 +161,16 @@ Operand operand_w(const beam_moe_grouped_t& g, const void* w) {
   return o;
 }
 
-// Rows per tile.  A tile costs at least its weights' bytes whatever its rows,
-// so the tile follows the mean group: narrow tiles leave the ring to weight
-// stages (12 in flight instead of 6) and load no rows of later groups; wide
-// ones read each weight once for up to 256 rows.
+// Rows per tile, by the mean group.  Narrow tiles keep more weight stages in
+// flight and their rows' MMAs short; wide ones read each weight once for more
+// rows.  64 groups, 5120 -> 2560, in us for 64 / 128 / 256 rows a tile: mean
+// 8 rows 245 / 245 / 258, 32: 251 / 252 / 268, 48: 260 / 255 / 272, 96: 302 /
+// 270 / 281, 128: 364 / 288 / 288, 192: 486 / 324 / 300; 16 groups, 1024 ->
+// 2048: mean 24: 13 / 14 / 16, 64: 17 / 14 / 20, 128: 25 / 19 / 22.  (32 rows
+// were not faster anywhere: 221 against 215 at a mean of 2.)
 int rows_tile(const beam_moe_grouped_t& g) {
   const int64_t mean = g.rows / g.n_groups;
-  return mean <= 12 ? 32 : mean <= 40 ? 64 : mean <= 96 ? 128 : 256;
+  return mean <= 40 ? 64 : mean <= 144 ? 128 : 256;
 }
 
 // Common tail of the three products.
@@ -192,7 +195,7 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
     return BEAM_ERR_CUDA;
   CUtensorMap ta, tb;
   if (!tmap3(&ta, a.base, g.dtype, a.inner, a.outer, a.z, a.ld, a.zs, a_mn ? 64 : 128) ||
-      !tmap3(&tb, b.base, g.dtype, b.inner, b.outer, b.z, b.ld, b.zs, b_mn ? 64 : beam::product_box_rows(nt)))
+      !tmap3(&tb, b.base, g.dtype, b.inner, b.outer, b.z, b.ld, b.zs, b_mn ? 64 : beam::kProductBoxRows))
     return BEAM_ERR_CUDA;
   ProductArgs p = {};
   p.M = static_cast<int32_t>(M);
@@ -256,6 +259,24 @@ bool ortho_layout(int32_t batch, int32_t rows, int32_t cols, int32_t dtype, Orth
   L->poly = take(mm);
   L->total = off;
   return true;
+}
+
+// Rows per tile of a chain of products (ortho_chain.cu): 256 keep the tensor
+// cores busiest (0.36 us per 64-wide k block for twice the rows of 128 in
+// 0.26), 128 spread small products over more CTA pairs.  The estimate is the
+// waves of each product times its k blocks; measured, in us for 128 / 256:
+// 512 x 1024 128 / 169, 1536 x 1536 197 / 245, 4 x 1024 x 2048 246 / 257,
+// 2048 x 4096 423 / 393, 8 x 2560 x 5120 (by rule) 256.
+int chain_tile(int64_t batch, int64_t R, int64_t C, int64_t pairs) {
+  const int64_t m = std::min(R, C), mt = (m + 255) / 256;
+  auto cost = [&](int64_t nt, double block_us) {
+    auto waves = [&](int64_t tiles) { return static_cast<double>((tiles + pairs - 1) / pairs); };
+    const int64_t sym = batch * (mt * ((m + nt - 1) / nt) - 256 / nt * (mt * (mt - 1) / 2));
+    const int64_t step = batch * ((C + 255) / 256) * ((R + nt - 1) / nt);
+    const int64_t km = (m + 63) / 64, kn = (std::max(R, C) + 63) / 64;
+    return block_us * (waves(sym) * (kn + km) + waves(step) * km);
+  };
+  return cost(256, 0.36) <= cost(128, 0.26) ? 256 : 128;
 }
 
 template <typename T>
@@ -478,13 +499,7 @@ beam_status_t beam_moe_orthogonalize(const beam_moe_ortho_t* d, const void* src,
   n.eps = d->eps;
   if (beam::launch_norm(n, s) != cudaSuccess) return BEAM_ERR_CUDA;
 
-  // Tiles of 256 rows keep the tensor cores busiest; where all products
-  // together have too few of them for the CTA pairs, 128 rows spread wider.
-  const int64_t pairs = dev.sms / 2;
-  const int64_t mt = (m + 255) / 256;
-  const int64_t wide_tiles =
-      batch * std::min(mt * (mt + 1) / 2, (C + 255) / 256 * ((R + 255) / 256));
-  const int nt = wide_tiles >= pairs ? 256 : 128;
+  const int nt = chain_tile(batch, R, C, dev.sms / 2);
   const uint32_t rows_box = beam::kProductBoxRows;
 
   const int32_t F16 = BEAM_DTYPE_F16;
