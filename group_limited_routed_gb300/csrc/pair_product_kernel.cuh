@@ -78,6 +78,11 @@ namespace {
 using gemm::Waiter;
 
 constexpr int kWideBlocks = 8;  // k blocks per accumulator chain, FP32 outputs
+// FP32 weight gradients leave by bulk copy up to this many k blocks (16 x 256
+// rows: 145 us, plain stores 192), by plain stores beyond, where the copies
+// would queue in front of the next blocks' loads (16 x 400 rows: 231 us by
+// copy, 201 plain; 1024: 349, 331).
+constexpr int kStagedBlocks = 5;
 
 // DUAL (16-bit weight gradients): a tile takes two blocks of NT rows j, one per
 // TMEM buffer, that share the stage's A -- 48 KB per k block for what two
@@ -85,7 +90,7 @@ constexpr int kWideBlocks = 8;  // k blocks per accumulator chain, FP32 outputs
 // rows, 2560 x 5120: 293 -> 263 us; 16 x 256 rows 112 -> 110).
 template <int NT, int KIND, bool WIDE, bool DUAL>
 struct ProductCfg {
-  static constexpr bool STAGED = KIND == kProductGroups || WIDE;
+  static constexpr bool STAGED = KIND == kProductGroups;
   static constexpr uint32_t B_BYTES = NT / 2 * 128;  // one block of rows
   static constexpr uint32_t STAGE = kPABytes + (DUAL ? 2 : 1) * B_BYTES;
   // DUAL stages are 48 KB: 8 KB more than the ring make it four of them
@@ -632,31 +637,43 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int i = t.i0 + static_cast<int>(rank) * 128 + q * 32 + lane;
       const int64_t zbase = KIND == kProductRows ? 0 : static_cast<int64_t>(t.z) * p.z_out;
       int ncols = min(t.nvalid - col_begin, COLS);  // <= 0: nothing for this warp
-      if (WIDE && KIND == kProductGroups && p.staged && t.k_blocks > 0 &&
-          t.k_blocks <= kWideBlocks) {
-        // one chain: straight from TMEM to the staged pieces
+      // a group without rows adds nothing
+      if (WIDE && KIND == kProductGroups && p.accumulate && t.k_blocks == 0) continue;
+      const bool by_copy = C::STAGED && p.staged && t.k_blocks <= kStagedBlocks;
+      if (WIDE && KIND == kProductGroups && t.k_blocks > 0 && t.k_blocks <= kWideBlocks &&
+          (by_copy || !p.accumulate)) {
+        // one chain: straight from TMEM to the stores
         if (!W.wait(tfull(acc), acc_phase)) break;
         ptx::tc_fence_after();
         const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NT + col_begin;
+        float* dst = static_cast<float*>(p.out) + zbase +
+                     (static_cast<int64_t>(t.j0) + col_begin) * p.ld_out + i;
 #pragma unroll 1
         for (int c = 0; c < COLS; c += 16) {
           if (c >= ncols) break;
           uint32_t r[16];
           ptx::tmem_ld16(tq + c, r);
-          if (lane == 0) tma_store_read_done();
+          if (by_copy && lane == 0) tma_store_read_done();
           ptx::tmem_wait_ld();
           __syncwarp();
+          if (by_copy) {
 #pragma unroll
-          for (int u = 0; u < 16; ++u)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage_at + u * 128 + lane * 4), "r"(r[u])
-                         : "memory");
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && i < p.M) {
-            if (p.accumulate)
-              tma_store_3d<true>(&tm_out, stage_at, i, t.j0 + col_begin + c, t.z);
-            else
-              tma_store_3d<false>(&tm_out, stage_at, i, t.j0 + col_begin + c, t.z);
+            for (int u = 0; u < 16; ++u)
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage_at + u * 128 + lane * 4),
+                           "r"(r[u])
+                           : "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && i < p.M) {
+              if (p.accumulate)
+                tma_store_3d<true>(&tm_out, stage_at, i, t.j0 + col_begin + c, t.z);
+              else
+                tma_store_3d<false>(&tm_out, stage_at, i, t.j0 + col_begin + c, t.z);
+            }
+          } else if (i < p.M) {
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+              if (c + u < ncols) __stcs(dst + (c + u) * p.ld_out, __uint_as_float(r[u]));
           }
         }
         ptx::tc_fence_before();
@@ -699,9 +716,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll
         for (int c = 0; c < COLS; c += 16) {
           if (c < ncols) {
-            // whole pieces of 16 rows leave by bulk copy (a group's last rows
-            // do not: the copy would reach into the next group's)
-            if (p.staged && (KIND == kProductGroups || c + 16 <= ncols)) {
+            // added to an FP32 gradient: by bulk copy where one is described
+            if (C::STAGED && p.staged && p.accumulate) {
               if (lane == 0) tma_store_read_done();
               __syncwarp();
 #pragma unroll
@@ -711,13 +727,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
                              : "memory");
               fence_proxy_async_smem();
               __syncwarp();
-              if (lane == 0 && i < p.M) {
-                const int z = KIND == kProductRows ? 0 : t.z;
-                if (p.accumulate)
-                  tma_store_3d<true>(&tm_out, stage_at, i, t.j0 + col_begin + c, z);
-                else
-                  tma_store_3d<false>(&tm_out, stage_at, i, t.j0 + col_begin + c, z);
-              }
+              if (lane == 0 && i < p.M)
+                tma_store_3d<true>(&tm_out, stage_at, i, t.j0 + col_begin + c, t.z);
             } else if (i < p.M) {
 #pragma unroll
               for (int u = 0; u < 16; ++u) {

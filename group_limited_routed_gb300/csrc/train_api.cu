@@ -214,10 +214,9 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   p.status = static_cast<uint32_t*>(ws);
   p.wait_limit_ns = beam::host::wait_limit_ns();
   CUtensorMap to = {};
-  // 16-bit rows leave straight from registers
-  if (kind == beam::kProductGroups || g.out_dtype == BEAM_DTYPE_F32)
-    p.staged = staged_out(&to, out, g.out_dtype, M, N,
-                          kind == beam::kProductGroups ? g.n_groups : 1, ld_out, z_out);
+  // (rows leave straight from registers)
+  if (kind == beam::kProductGroups)
+    p.staged = staged_out(&to, out, g.out_dtype, M, N, g.n_groups, ld_out, z_out);
   return launched(beam::launch_pair_product(kind, nt, a_mn, b_mn, ta, tb, to, p, s));
 }
 
