@@ -100,7 +100,8 @@ struct Operand {
   size_t packed_bytes() const {
     return align_up(static_cast<size_t>(z) * outer * round_up(inner, 8) * 2);
   }
-  cudaError_t pack_into(void* dst, const int32_t* offsets, cudaStream_t s) {
+  // The copy that puts an aligned stand-in at dst, and this operand there.
+  beam::PackArgs pack_into(void* dst, const int32_t* offsets) {
     beam::PackArgs p;
     p.src = static_cast<const uint16_t*>(base);
     p.sz = zs;
@@ -111,11 +112,10 @@ struct Operand {
     p.ld = static_cast<int32_t>(round_up(inner, 8));
     p.dst = static_cast<uint16_t*>(dst);
     p.offsets = z > 1 ? offsets : nullptr;  // a stack: one matrix per group
-    const cudaError_t e = beam::launch_pack(p, s);
     base = dst;
     ld = p.ld;
     zs = ld * outer;
-    return e;
+    return p;
   }
 };
 
@@ -189,10 +189,11 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   const beam_status_t st = device_ready(&dev);
   if (st != BEAM_OK) return st;
   if (!beam::host::encoder()) return BEAM_ERR_CUDA;
-  if (pack_a && a.pack_into(static_cast<uint8_t*>(ws) + at_a, offsets, s) != cudaSuccess)
-    return BEAM_ERR_CUDA;
-  if (pack_b && b.pack_into(static_cast<uint8_t*>(ws) + at_b, offsets, s) != cudaSuccess)
-    return BEAM_ERR_CUDA;
+  beam::PackArgs packs[2];
+  int n_packs = 0;
+  if (pack_a) packs[n_packs++] = a.pack_into(static_cast<uint8_t*>(ws) + at_a, offsets);
+  if (pack_b) packs[n_packs++] = b.pack_into(static_cast<uint8_t*>(ws) + at_b, offsets);
+  if (beam::launch_pack(packs, n_packs, s) != cudaSuccess) return BEAM_ERR_CUDA;
   CUtensorMap ta, tb;
   if (!tmap3(&ta, a.base, g.dtype, a.inner, a.outer, a.z, a.ld, a.zs, a_mn ? 64 : 128) ||
       !tmap3(&tb, b.base, g.dtype, b.inner, b.outer, b.z, b.ld, b.zs, b_mn ? 64 : beam::kProductBoxRows))

@@ -39,14 +39,22 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 // left out.  Memory bound: 2 bytes read, 2 written per element.
 constexpr int kPackSpan = 512;
 
-__global__ void __launch_bounds__(256) pack_kernel(const PackArgs p) {
+int64_t pack_units(const PackArgs& p) {
+  return p.zs * p.rows * ((p.ld + kPackSpan - 1) / kPackSpan);
+}
+
+// One launch copies a call's one or two such operands (units_a warps' pieces
+// of a, then b's).
+__global__ void __launch_bounds__(256)
+    pack_kernel(const PackArgs a, const PackArgs b, int64_t units_a, int64_t units) {
   ptx::grid_dep_wait();
   ptx::grid_dep_launch();
-  const int64_t rows = p.zs * p.rows;
   const int lane = threadIdx.x & 31;
-  const int spans = (p.ld + kPackSpan - 1) / kPackSpan;
-  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-       unit < rows * spans; unit += static_cast<int64_t>(gridDim.x) * 8) {
+  for (int64_t at_unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+       at_unit < units; at_unit += static_cast<int64_t>(gridDim.x) * 8) {
+    const PackArgs& p = at_unit < units_a ? a : b;
+    const int64_t unit = at_unit < units_a ? at_unit : at_unit - units_a;
+    const int spans = (p.ld + kPackSpan - 1) / kPackSpan;
     const int64_t row = unit / spans;
     const int first = static_cast<int>(unit - row * spans) * kPackSpan;
     const int64_t z = row / p.rows;
@@ -372,11 +380,15 @@ cudaError_t norm_typed(const NormArgs& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_pack(const PackArgs& p, cudaStream_t s) {
-  const int64_t units = p.zs * p.rows * ((p.ld + kPackSpan - 1) / kPackSpan);
+cudaError_t launch_pack(const PackArgs* p, int n, cudaStream_t s) {
+  if (n == 0) return cudaSuccess;
+  const PackArgs& b = p[n - 1];
+  const int64_t units_a = pack_units(p[0]);
+  const int64_t units = units_a + (n > 1 ? pack_units(b) : 0);
   const int64_t blocks = std::min<int64_t>((units + 7) / 8, 1 << 20);
   if (blocks == 0) return cudaSuccess;
-  return launch_dependent(pack_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, p);
+  return launch_dependent(pack_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, p[0],
+                          b, units_a, units);
 }
 
 cudaError_t launch_gate(const GateArgs& p, int num_sms, cudaStream_t s) {

@@ -22,7 +22,8 @@ struct PackArgs {
   uint16_t* dst;
   const int32_t* offsets;  // or nullptr: z with offsets[z + 1] <= offsets[z] are not copied
 };
-cudaError_t launch_pack(const PackArgs& p, cudaStream_t s);
+// n = 0, 1 or 2 operands, in one launch.
+cudaError_t launch_pack(const PackArgs* p, int n, cudaStream_t s);
 
 // -------------------------------------------------------------- gated rows
 struct GateArgs {
