@@ -25,7 +25,7 @@ int resident_clusters_once(const cudaLaunchConfig_t& cfg) {
 }
 
 template <int NT, bool A_MN, bool B_MN, int KIND, bool WIDE, bool DUAL = false>
-cudaError_t launch_impl(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& out,
+cudaError_t launch_impl(const CUtensorMap& a, const ProductMaps& b, const CUtensorMap& out,
                         const ProductArgs& p, int64_t max_tiles, cudaStream_t s) {
   using C = ProductCfg<NT, KIND, WIDE, DUAL>;
   constexpr auto kern = pair_product_kernel<NT, A_MN, B_MN, KIND, WIDE, DUAL>;
@@ -53,21 +53,21 @@ cudaError_t launch_impl(const CUtensorMap& a, const CUtensorMap& b, const CUtens
   return cudaLaunchKernelEx(&cfg, kern, a, b, out, p);
 }
 
-template <int NT>
-cudaError_t launch_rows(bool a_mn, const CUtensorMap& a, const CUtensorMap& b,
+template <int NT, bool DUAL = false>
+cudaError_t launch_rows(bool a_mn, const CUtensorMap& a, const ProductMaps& b,
                         const CUtensorMap& out, const ProductArgs& p, int64_t tiles, cudaStream_t s) {
   const bool wide = p.out_type == kF32;
   if (a_mn)
     return wide ? launch_impl<NT, true, false, kProductRows, true>(a, b, out, p, tiles, s)
-                : launch_impl<NT, true, false, kProductRows, false>(a, b, out, p, tiles, s);
+                : launch_impl<NT, true, false, kProductRows, false, DUAL>(a, b, out, p, tiles, s);
   return wide ? launch_impl<NT, false, false, kProductRows, true>(a, b, out, p, tiles, s)
-              : launch_impl<NT, false, false, kProductRows, false>(a, b, out, p, tiles, s);
+              : launch_impl<NT, false, false, kProductRows, false, DUAL>(a, b, out, p, tiles, s);
 }
 
 }  // namespace
 
-cudaError_t launch_pair_product(int kind, int nt, bool a_mn, bool b_mn, const CUtensorMap& a,
-                                const CUtensorMap& b, const CUtensorMap& out,
+cudaError_t launch_pair_product(int kind, int nt, bool dual, bool a_mn, bool b_mn, const CUtensorMap& a,
+                                const ProductMaps& b, const CUtensorMap& out,
                                 const ProductArgs& p, cudaStream_t s) {
   const int64_t mt = (p.M + kProductTileM - 1) / kProductTileM;
   if (kind == kProductRows && !b_mn) {
@@ -76,7 +76,9 @@ cudaError_t launch_pair_product(int kind, int nt, bool a_mn, bool b_mn, const CU
     switch (nt) {
       case 64: return launch_rows<64>(a_mn, a, b, out, p, tiles, s);
       case 128: return launch_rows<128>(a_mn, a, b, out, p, tiles, s);
-      case 256: return launch_rows<256>(a_mn, a, b, out, p, tiles, s);
+      case 256:
+        return dual ? launch_rows<256, true>(a_mn, a, b, out, p, tiles, s)
+                    : launch_rows<256>(a_mn, a, b, out, p, tiles, s);
     }
     return cudaErrorInvalidValue;
   }

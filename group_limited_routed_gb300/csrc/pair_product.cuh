@@ -38,22 +38,29 @@ struct ProductArgs {
   uint64_t wait_limit_ns;
 };
 
+// B's maps: a k-contiguous one is read in boxes of 32, 64 (tiles of 128 rows
+// and more) and 128 rows (256); an operand contiguous along j has the first.
+struct ProductMaps {
+  CUtensorMap rows[3];
+};
+
 // Columns i of a tile, groups a call may have.
 constexpr int kProductTileM = 256;
 constexpr int kProductMaxGroups = 1024;
 
-// Rows j of one box of a k-contiguous B.
+// Rows j of the smallest box of a k-contiguous B.
 constexpr int kProductBoxRows = 32;
 inline int product_out_rows(bool f32) { return f32 ? 16 : 32; }
 
 // nt: rows j per tile, 64, 128 or 256 (kProductGroups: 256).  a_mn, b_mn:
 // the operand's contiguous axis is i (j) rather than k.  Tensor maps are
 // three-dimensional (contiguous, row, z); a and b with 128-byte swizzle and
-// boxes 64 x 128 (a, k contiguous), 64 x 64 (a_mn, b_mn), 64 x
-// kProductBoxRows (b, k contiguous); out (only read with p.staged)
-// without swizzle, boxes 32 x product_out_rows.
-cudaError_t launch_pair_product(int kind, int nt, bool a_mn, bool b_mn, const CUtensorMap& a,
-                                const CUtensorMap& b, const CUtensorMap& out,
+// boxes 64 x 128 (a, k contiguous), 64 x 64 (a_mn, b_mn), 64 x 32, 64, 128
+// rows (b, k contiguous); out (only read with p.staged) without swizzle, boxes
+// 32 x product_out_rows.  dual (kProductRows, nt 256, 16-bit results): groups
+// of 257 to 384 rows are one tile.
+cudaError_t launch_pair_product(int kind, int nt, bool dual, bool a_mn, bool b_mn, const CUtensorMap& a,
+                                const ProductMaps& b, const CUtensorMap& out,
                                 const ProductArgs& p, cudaStream_t s);
 
 }  // namespace beam

@@ -39,8 +39,8 @@
 // tensor cores are busy 98 % of the cycles and the power limit holds the clock
 // near 1.5 GHz.  Ragged blocks are bound by the loads: a k block of n rows
 // moves 16 KB + 64 n bytes into each SM for 2 n cycles of MMA, and the L2
-// gives an SM about 95 GB/s (192 KB of ring over a loaded latency of 2 us).  A
-// decode batch streams weights at 7.1 TB/s.  Weight gradients of small groups
+// gives an SM 54 to 60 bytes a cycle.  A decode batch streams weights at 7.1
+// TB/s.  Weight gradients of small groups
 // are bound by their stores: 16 x 256 rows, 2560 x 5120 in FP32 149 us, 6.1
 // TB/s.
 //
@@ -49,11 +49,16 @@
 // k block instead of 520); freeing an accumulator without a release (a release
 // at cluster scope waits for the warp's global stores, 3000 cycles per tile);
 // stores of weight gradients through shared memory, written by the copy
-// engine.  Tried and dropped: two row blocks of a group per tile sharing A
-// (both TMEM buffers in one tile leave the epilogue exposed: 1024-row groups
-// 518 -> 527 us, 600-row groups 370 -> 450); row blocks in steps of 64 rows,
-// whole load boxes (400-row groups 229 -> 245 us: uneven blocks); finding the
-// producer's next tile ahead (no change).
+// engine.  Tried and dropped: row blocks in steps of 64 rows, whole load boxes
+// (400-row groups 229 -> 245 us: uneven blocks); finding the producer's next
+// tile ahead, and B's loads by a warp of their own (no change: the rate is the
+// L2's); k blocks of their own sizes one behind the other in the ring (deeper
+// for small tiles, but the roles' bookkeeping then takes 590 cycles a block of
+// 512: 1024-row groups 480 -> 499 us).  For 16-bit weight gradients: both
+// buffers of a tile read before either is stored (400-row groups 149 -> 165
+// us), 64 KB of staging (110 -> 114 at 256 rows, 149 -> 163 at 400: a stage
+// less), 128-byte rows staged by two warps (107 -> 113), vector stores by the
+// warps (107 -> 130).
 //
 // Every wait is bounded (gemm::Waiter); after an abort all roles still reach
 // the cluster barrier that precedes the release of TMEM.
@@ -84,18 +89,28 @@ constexpr int kWideBlocks = 8;  // k blocks per accumulator chain, FP32 outputs
 // copy, 201 plain; 1024: 349, 331).
 constexpr int kStagedBlocks = 5;
 
-// DUAL (16-bit weight gradients): a tile takes two blocks of NT rows j, one per
-// TMEM buffer, that share the stage's A -- 48 KB per k block for what two
-// tiles load as 64 KB, where the loads are what a tile waits for (16 x 1024
-// rows, 2560 x 5120: 293 -> 263 us; 16 x 256 rows 112 -> 110).
+// DUAL: a tile takes two blocks of rows j, one per TMEM buffer, that share the
+// stage's A, where the loads are what a tile waits for.  (The L2 gives an SM
+// 54 to 60 bytes a cycle, whatever the tile and however many warps issue.)
+//   16-bit weight gradients: two blocks of NT rows, 48 KB per k block for what
+//   two tiles load as 64 KB (16 x 1024 rows, 2560 x 5120: 293 -> 263 us; 16 x
+//   256 rows 112 -> 110).
+//   Grouped rows: groups of NT + 1 to kDualRows rows, whose two halves would
+//   load A twice (32 groups of 272 rows, 2560 -> 5120: 208 -> 180 us, 350
+//   rows: 219 -> 195).  Other groups lose by the larger stages (256 rows 163
+//   -> 168, 600 rows 322 -> 347), so a call takes it by its mean group.
+constexpr int kDualRows = 384;
+
 template <int NT, int KIND, bool WIDE, bool DUAL>
 struct ProductCfg {
   static constexpr bool STAGED = KIND == kProductGroups;
   static constexpr uint32_t B_BYTES = NT / 2 * 128;  // one block of rows
-  static constexpr uint32_t STAGE = kPABytes + (DUAL ? 2 : 1) * B_BYTES;
-  // DUAL stages are 48 KB: 8 KB more than the ring make it four of them
+  // DUAL: where the second block begins behind the first
+  static constexpr uint32_t B2_AT = KIND == kProductRows ? kDualRows / 4 * 128 : B_BYTES;
+  static constexpr uint32_t STAGE = kPABytes + (DUAL ? 2 * B2_AT : B_BYTES);
+  // 48 KB stages: 8 KB more than the ring make it four of them
   static constexpr int S_RAW = static_cast<int>(
-      (kPRing + (DUAL ? 8192 : 0) - (STAGED ? kStaging : 0)) / STAGE);
+      (kPRing + (DUAL && STAGED ? 8192 : 0) - (STAGED ? kStaging : 0)) / STAGE);
   static constexpr int S = S_RAW > 12 ? 12 : S_RAW;
   static constexpr uint32_t TMEM_COLS = 2 * NT;
   static constexpr uint32_t NUM_BARS = 4 * S + 5;
@@ -107,7 +122,7 @@ struct ProductCfg {
   static constexpr uint32_t BARS = STAGING + (STAGED ? kStaging : 0);
   static constexpr uint32_t SMEM_BYTES = 1024 + BARS + NUM_BARS * 8 + MISC;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-  static_assert(STAGE % 1024 == 0, "swizzle atoms are 1024-byte aligned");
+  static_assert(STAGE % 1024 == 0 && B2_AT % 1024 == 0, "swizzle atoms are 1024-byte aligned");
   static_assert(TMEM_COLS <= 512, "TMEM columns");
 };
 
@@ -128,6 +143,45 @@ struct ProductTile {
 __device__ __forceinline__ int small_div(int a, int b) {
   if (a < (1 << 20)) return static_cast<int>((static_cast<float>(a) + 0.5f) * __frcp_rn(static_cast<float>(b)));
   return a / b;
+}
+
+// n times 32 rows of a k-contiguous B (1 to NT / 64 times) in as few boxes as
+// make them up: a copy's cost is not its bytes alone (256-row blocks in boxes
+// of 16 / 32 / up to 128 rows, 32 x 600 rows, 2560 -> 5120: 384 / 330 / 321 us).
+template <int NT>
+__device__ __forceinline__ void load_rows(const ProductMaps& b, int n, uint32_t dst, uint32_t bar,
+                                          int k, int j, uint64_t pol) {
+  if (NT == 256 && n == 4) {
+    tma_load_3d_pair(dst, &b.rows[2], bar, k, j, 0, pol);
+  } else {
+    if (NT > 64 && n >= 2) tma_load_3d_pair(dst, &b.rows[1], bar, k, j, 0, pol);
+    if (n & 1) {
+      const int done = n - 1;
+      tma_load_3d_pair(dst + done * (kProductBoxRows * 128), &b.rows[0], bar, k,
+                       j + done * kProductBoxRows, 0, pol);
+    }
+  }
+}
+
+// Zeros over a row, by the lanes of a warp: single elements up to a 16-byte
+// boundary and behind the last one, whole vectors between.
+template <typename T>
+__device__ __forceinline__ void zero_row(T* row, int n, int lane) {
+  constexpr int V = 16 / sizeof(T);
+  const int head =
+      min(n, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / static_cast<int>(sizeof(T)));
+  const int vecs = (n - head) / V;
+  if (lane < head) row[lane] = T(0);
+  for (int v = lane; v < vecs; v += 32)
+    reinterpret_cast<uint4*>(row + head)[v] = make_uint4(0, 0, 0, 0);
+  const int at = head + vecs * V + lane;
+  if (at < n) row[at] = T(0);
+}
+
+// Tiles that a group's rows make for each block of columns.
+template <int NT, bool DUAL>
+__device__ __forceinline__ int row_tiles(int cnt) {
+  return DUAL && cnt > NT && cnt <= kDualRows ? 1 : (cnt + NT - 1) / NT;
 }
 
 // One role's walk over this pair's tiles: tile, tile + num_pairs, ...  With a
@@ -198,15 +252,16 @@ struct ProductWalk {
       const int local = tile - s_start[group];
       const int cnt = s_off[group + 1] - s_off[group];
       // blocks of nearly equal size, each a multiple of 16 rows
-      const int nb = (cnt + NT - 1) / NT;
+      const bool both = DUAL && cnt > NT && cnt <= kDualRows;
+      const int nb = both ? 2 : (cnt + NT - 1) / NT;
       const int per = (small_div(cnt + nb - 1, nb) + 15) & ~15;
-      const int block_i = small_div(local, nb);
-      const int b = local - block_i * nb;
+      const int block_i = both ? local : small_div(local, nb);
+      const int b = both ? 0 : local - block_i * nb;
       t.z = group;
       t.i0 = block_i * kProductTileM;
       t.j0 = s_off[group] + b * per;
       t.nvalid = min(per, cnt - b * per);
-      t.nvalid2 = 0;
+      t.nvalid2 = both ? cnt - per : 0;
       t.k_blocks = p.k_blocks;
       t.k0 = t.k_count = 0;
     } else {
@@ -233,7 +288,7 @@ struct ProductWalk {
 template <int NT, bool A_MN, bool B_MN, int KIND, bool WIDE, bool DUAL>
 __global__ void __launch_bounds__(kPThreads, 1)
     pair_product_kernel(const __grid_constant__ CUtensorMap tm_a,
-                        const __grid_constant__ CUtensorMap tm_b,
+                        const __grid_constant__ ProductMaps tm_b,
                         const __grid_constant__ CUtensorMap tm_out, const ProductArgs p) {
   using C = ProductCfg<NT, KIND, WIDE, DUAL>;
   using Walk = ProductWalk<NT, KIND, DUAL>;
@@ -284,7 +339,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
   if (warp == 0 && lane == 0) {
     ptx::prefetch_tmap(&tm_a);
-    ptx::prefetch_tmap(&tm_b);
+    ptx::prefetch_tmap(&tm_b.rows[0]);
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), C::TMEM_COLS);
@@ -334,7 +389,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       for (int base = 0; base < p.groups; base += 32) {
         const int e = base + lane;
         const int cnt = e < p.groups ? s_off[e + 1] - s_off[e] : 0;
-        const int v = mt * ((cnt + NT - 1) / NT);
+        const int v = mt * row_tiles<NT, DUAL>(cnt);
         int incl = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -376,13 +431,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const ProductTile t = walk.get();
         const int i = t.i0 + static_cast<int>(rank) * 128;
         const int j = t.j0 + static_cast<int>(rank) * (t.n_mma / 2);
-        // k-contiguous B comes in boxes of BOX rows, as many as the tile has
+        // k-contiguous B comes in units of BOX rows, as many as the tile has
         constexpr int BOX = kProductBoxRows;
         const int boxes = (t.n_mma / 2 + BOX - 1) / BOX;
         const int n2 = (t.nvalid2 + 15) & ~15;
+        const int boxes2 = (n2 / 2 + BOX - 1) / BOX;
         const int j2 = t.j0 + t.nvalid + static_cast<int>(rank) * (n2 / 2);
         const uint32_t bytes =
-            kPABytes + (B_MN ? (n2 ? 2 : 1) * C::B_BYTES : boxes * BOX * 128u);
+            kPABytes + (B_MN ? (n2 ? 2 : 1) * C::B_BYTES : (boxes + boxes2) * BOX * 128u);
         for (int kb = 0; kb < t.k_blocks; ++kb) {
           if (!W.wait(empty(stage), phase ^ 1u)) {
             ok = false;
@@ -414,18 +470,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
             if constexpr (B_MN) {
 #pragma unroll
               for (int c = 0; c < NT / 128; ++c)
-                tma_load_3d_pair(sb + c * kAtom, &tm_b, bar, j + c * 64, k, 0, pol);
+                tma_load_3d_pair(sb + c * kAtom, &tm_b.rows[0], bar, j + c * 64, k, 0, pol);
               if (DUAL && n2) {
 #pragma unroll
                 for (int c = 0; c < NT / 128; ++c)
-                  tma_load_3d_pair(sb + C::B_BYTES + c * kAtom, &tm_b, bar, j2 + c * 64, k, 0,
-                                   pol);
+                  tma_load_3d_pair(sb + C::B2_AT + c * kAtom, &tm_b.rows[0], bar, j2 + c * 64, k,
+                                   0, pol);
               }
             } else {
-#pragma unroll
-              for (int c = 0; c < NT / 2 / BOX; ++c)
-                if (c < boxes)
-                  tma_load_3d_pair(sb + c * (BOX * 128), &tm_b, bar, k, j + c * BOX, 0, pol);
+              load_rows<NT>(tm_b, boxes, sb, bar, k, j, pol);
+              if constexpr (DUAL) {
+                if (boxes2) load_rows<NT>(tm_b, boxes2, sb + C::B2_AT, bar, k, j2, pol);
+              }
             }
           }
           __syncwarp();
@@ -489,18 +545,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const uint32_t idesc = idesc_m | (static_cast<uint32_t>(t.n_mma >> 3) << 17);
         const uint32_t idesc2 =
             idesc_m | (static_cast<uint32_t>(((t.nvalid2 + 15) & ~15) >> 3) << 17);
-        uint32_t d0 = 0;
+        const bool two = DUAL && t.nvalid2 > 0;
         for (int kb = 0; kb < t.k_blocks; ++kb) {
           const bool fresh = kb == 0 || (WIDE && kb % kWideBlocks == 0);
           if (fresh) {
             if (!W.wait(tempty(acc), acc_phase ^ 1u)) {
-              ok = false;
-              break;
-            }
-            d0 = tmem_base + acc * NT;
-            // a second block takes the other buffer, one use later
-            if (DUAL && t.nvalid2 > 0 &&
-                !W.wait(tempty(acc ^ 1), (acc == 1 ? acc_phase ^ 1u : acc_phase) ^ 1u)) {
               ok = false;
               break;
             }
@@ -520,29 +569,39 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           ptx::tc_fence_after();
           const bool last = kb + 1 == t.k_blocks || (WIDE && (kb + 1) % kWideBlocks == 0);
-          if (elected) {
-            const uint64_t ad = a_desc0 + stage * (C::STAGE >> 4);
-            const uint64_t bd = b_desc0 + stage * (C::STAGE >> 4);
-            const int steps = ragged ? (t.k_count - kb * kPBK + 15) / 16 : kPBK / 16;
+          const uint64_t ad = a_desc0 + stage * (C::STAGE >> 4);
+          const uint64_t bd = b_desc0 + stage * (C::STAGE >> 4);
+          const int steps = ragged ? (t.k_count - kb * kPBK + 15) / 16 : kPBK / 16;
+          auto issue = [&](uint32_t d, uint64_t b, uint32_t shape) {
 #pragma unroll
             for (int kk = 0; kk < kPBK / 16; ++kk)
               if (!RAGGED_K || kk < steps)
-                ptx::mma_bf16_pair(d0, ad + kk * A_STEP, bd + kk * B_STEP, idesc,
+                ptx::mma_bf16_pair(d, ad + kk * A_STEP, b + kk * B_STEP, shape,
                                    (fresh && kk == 0) ? 0u : 1u);
+          };
+          if (elected) {
+            issue(tmem_base + acc * NT, bd, idesc);
             if (last) ptx::mma_commit_pair_both(tfull(acc));
-            if (DUAL && t.nvalid2 > 0) {
-              // the same A against the second block
-              const uint32_t d1 = tmem_base + (acc ^ 1) * NT;
-#pragma unroll
-              for (int kk = 0; kk < kPBK / 16; ++kk)
-                if (!RAGGED_K || kk < steps)
-                  ptx::mma_bf16_pair(d1, ad + kk * A_STEP, bd + (C::B_BYTES >> 4) + kk * B_STEP,
-                                     idesc2, (fresh && kk == 0) ? 0u : 1u);
-              if (last) ptx::mma_commit_pair_both(tfull(acc ^ 1));
-            }
-            ptx::mma_commit_pair_both(empty(stage));
+            if (!two) ptx::mma_commit_pair_both(empty(stage));
           }
           __syncwarp();
+          if (DUAL && two) {
+            // the same A against the second block, whose buffer is the other
+            // one, one use later
+            if (fresh) {
+              if (!W.wait(tempty(acc ^ 1), (acc == 1 ? acc_phase ^ 1u : acc_phase) ^ 1u)) {
+                ok = false;
+                break;
+              }
+              ptx::tc_fence_after();
+            }
+            if (elected) {
+              issue(tmem_base + (acc ^ 1) * NT, bd + (C::B2_AT >> 4), idesc2);
+              if (last) ptx::mma_commit_pair_both(tfull(acc ^ 1));
+              ptx::mma_commit_pair_both(empty(stage));
+            }
+            __syncwarp();
+          }
           if (kb == 0) {
             // the next tile's place, found while the tensor cores work
             walk.next();
@@ -553,7 +612,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             phase ^= 1u;
           }
           if (last) {
-            if (DUAL && t.nvalid2 > 0) {
+            if (two) {
               acc_phase ^= 1u;  // both buffers used: acc comes round to itself
             } else {
               acc ^= 1;
@@ -606,7 +665,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     constexpr int COLS = NT / GROUPS;  // rows j per warp
     const int col_begin = ((warp - 3) >> 2) * COLS;
     // TMEM columns per load
-    constexpr int LD = COLS < 32 ? 16 : 32;
+    constexpr int LD = COLS < 32 || (DUAL && !C::STAGED) ? 16 : 32;
     const uint32_t stage_at = ring + C::STAGING + (warp - 3) * 2048;
     const bool f16 = p.out_type == kF16;
     // two columns per store where every address of it is 4-byte aligned
@@ -615,17 +674,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if constexpr (KIND == kProductRows) {
       // rows outside every group are zero
       const int first = s_off[0], last = s_off[p.groups];
-      const int64_t gap = static_cast<int64_t>(first) + (p.rows - last);
-      const int64_t n = gap * p.M;
-      const int64_t step = static_cast<int64_t>(gridDim.x) * (32 * kPEpiWarps);
-      for (int64_t at = static_cast<int64_t>(blockIdx.x) * (32 * kPEpiWarps) + (threadIdx.x - 96);
-           at < n; at += step) {
-        const int64_t r = at / p.M;
-        const int64_t dst = (r < first ? r : r - first + last) * p.ld_out + at % p.M;
+      const int gap = first + (p.rows - last);
+      for (int g = static_cast<int>(blockIdx.x) * kPEpiWarps + warp - 3; g < gap;
+           g += static_cast<int>(gridDim.x) * kPEpiWarps) {
+        const int64_t at = static_cast<int64_t>(g < first ? g : g - first + last) * p.ld_out;
         if (WIDE)
-          static_cast<float*>(p.out)[dst] = 0.f;
+          zero_row(static_cast<float*>(p.out) + at, p.M, lane);
         else
-          static_cast<uint16_t*>(p.out)[dst] = 0;
+          zero_row(static_cast<uint16_t*>(p.out) + at, p.M, lane);
       }
     }
     int acc = 0;
@@ -633,10 +689,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
     bool ok = true;
     for (Walk walk(p, s_off, s_start, pair, num_pairs, num_tiles);
          ok && !walk.done(); walk.next()) {
-      ProductTile t = walk.get();
+      const ProductTile t = walk.get();
       const int i = t.i0 + static_cast<int>(rank) * 128 + q * 32 + lane;
       const int64_t zbase = KIND == kProductRows ? 0 : static_cast<int64_t>(t.z) * p.z_out;
-      int ncols = min(t.nvalid - col_begin, COLS);  // <= 0: nothing for this warp
+      const int ncols = min(t.nvalid - col_begin, COLS);  // <= 0: nothing for this warp
       // a group without rows adds nothing
       if (WIDE && KIND == kProductGroups && p.accumulate && t.k_blocks == 0) continue;
       const bool by_copy = C::STAGED && p.staged && t.k_blocks <= kStagedBlocks;
@@ -741,18 +797,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
         }
       } else {
-        for (;;) {
+        // Rows (2c, 2c + 1) of this lane's column, packed; the accumulator is
+        // free again before any store.
+        auto drain = [&](uint32_t(&packed)[COLS / 2], int ncols) {
           const bool live = t.k_blocks > 0;
-          uint32_t packed[COLS / 2];  // rows (2c, 2c + 1) of this lane's column
           if (live) {
-            if (!W.wait(tfull(acc), acc_phase)) {
-              ok = false;
-              break;
-            }
+            if (!W.wait(tfull(acc), acc_phase)) return false;
             ptx::tc_fence_after();
           }
           const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NT + col_begin;
-          uint16_t* out = static_cast<uint16_t*>(p.out) + zbase;
 #pragma unroll
           for (int c = 0; c < COLS; c += LD) {
             if (c < ncols) {
@@ -770,14 +823,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
             }
           }
           if (live) {
-            // the accumulator is free before any store
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_relaxed_cluster(ptx::map_to_rank(tempty(acc), 0));
             acc ^= 1;
             if (acc == 0) acc_phase ^= 1u;
           }
-          const int64_t j = static_cast<int64_t>(t.j0) + col_begin;
+          return true;
+        };
+        auto store = [&](const uint32_t(&packed)[COLS / 2], int j0, int ncols) {
+          uint16_t* out = static_cast<uint16_t*>(p.out) + zbase;
+          const int64_t j = static_cast<int64_t>(j0) + col_begin;
           if (C::STAGED && p.staged) {
 #pragma unroll
             for (int c = 0; c < COLS; c += 32) {
@@ -795,7 +851,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0 && i < p.M)
-                  tma_store_3d<false>(&tm_out, stage_at, i, t.j0 + col_begin + c, t.z);
+                  tma_store_3d<false>(&tm_out, stage_at, i, j0 + col_begin + c, t.z);
               }
             }
           } else if (paired) {
@@ -815,12 +871,23 @@ __global__ void __launch_bounds__(kPThreads, 1)
               if (c < ncols)
                 dst[c * p.ld_out] = static_cast<uint16_t>(packed[c / 2] >> (16 * (c & 1)));
           }
-          if (!DUAL || t.nvalid2 == 0) break;
-          // the tile's second block
-          t.j0 += t.nvalid;
-          t.nvalid = t.nvalid2;
-          t.nvalid2 = 0;
-          ncols = min(t.nvalid - col_begin, COLS);
+        };
+        uint32_t packed[COLS / 2];
+        const int ncols2 = min(t.nvalid2 - col_begin, COLS);
+        if (!drain(packed, ncols)) break;
+        if constexpr (DUAL && !C::STAGED) {
+          // both buffers are read before either is stored: the next tile's
+          // MMAs wait for the reads alone
+          uint32_t second[COLS / 2];
+          if (t.nvalid2 > 0 && !drain(second, ncols2)) break;
+          store(packed, t.j0, ncols);
+          if (t.nvalid2 > 0) store(second, t.j0 + t.nvalid, ncols2);
+        } else {
+          store(packed, t.j0, ncols);
+          if (DUAL && t.nvalid2 > 0) {
+            if (!drain(packed, ncols2)) break;
+            store(packed, t.j0 + t.nvalid, ncols2);
+          }
         }
       }
     }

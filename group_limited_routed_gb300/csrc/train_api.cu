@@ -129,6 +129,8 @@ bool valid_grouped(const beam_moe_grouped_t* g) {
     return false;
   if (!is16(g->dtype) || !(g->out_dtype == g->dtype || g->out_dtype == BEAM_DTYPE_F32)) return false;
   if (!good_ld(g->x_ld, g->K) || !good_ld(g->y_ld, g->N)) return false;
+  // sizes that address arithmetic in 64 bits holds with room to spare
+  if (static_cast<int64_t>(g->N) * g->K > kMaxStride) return false;
   // one axis of W contiguous, the other stepping past it, groups apart or shared
   const int64_t e = g->w_stride_e, n = g->w_stride_n, k = g->w_stride_k;
   const bool k_inner = k == 1 && (g->N == 1 || good_ld(n, g->K));
@@ -173,6 +175,16 @@ int rows_tile(const beam_moe_grouped_t& g) {
   return mean <= 40 ? 64 : mean <= 144 ? 128 : 256;
 }
 
+// Whether groups of 257 to 384 rows are one tile (see pair_product_kernel.cuh):
+// where many groups are of that size.  Equal groups, in us without / with: 200
+// rows 156 / 163, 256: 163 / 168, 272: 208 / 181, 350: 219 / 195, 400: 223 /
+// 240; groups spread around a mean of 256 rows (a third of them that size)
+// 1384 / 1317.
+bool dual_rows(const beam_moe_grouped_t& g) {
+  const int64_t mean = g.rows / g.n_groups;
+  return g.out_dtype != BEAM_DTYPE_F32 && mean > 224 && mean <= 352;
+}
+
 // Common tail of the three products.
 beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool a_mn, bool b_mn,
                              Operand a, Operand b, int64_t M, int64_t N, int64_t k,
@@ -194,10 +206,16 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   if (pack_a) packs[n_packs++] = a.pack_into(static_cast<uint8_t*>(ws) + at_a, offsets);
   if (pack_b) packs[n_packs++] = b.pack_into(static_cast<uint8_t*>(ws) + at_b, offsets);
   if (beam::launch_pack(packs, n_packs, s) != cudaSuccess) return BEAM_ERR_CUDA;
-  CUtensorMap ta, tb;
+  CUtensorMap ta;
+  beam::ProductMaps tb = {};
   if (!tmap3(&ta, a.base, g.dtype, a.inner, a.outer, a.z, a.ld, a.zs, a_mn ? 64 : 128) ||
-      !tmap3(&tb, b.base, g.dtype, b.inner, b.outer, b.z, b.ld, b.zs, b_mn ? 64 : beam::kProductBoxRows))
+      !tmap3(&tb.rows[0], b.base, g.dtype, b.inner, b.outer, b.z, b.ld, b.zs,
+             b_mn ? 64 : beam::kProductBoxRows))
     return BEAM_ERR_CUDA;
+  for (int i = 1; i < 3 && !b_mn; ++i)
+    if (nt >= 128 * i && !tmap3(&tb.rows[i], b.base, g.dtype, b.inner, b.outer, b.z, b.ld, b.zs,
+                                beam::kProductBoxRows << i))
+      return BEAM_ERR_CUDA;
   ProductArgs p = {};
   p.M = static_cast<int32_t>(M);
   p.N = static_cast<int32_t>(N);
@@ -218,7 +236,7 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   // (rows leave straight from registers)
   if (kind == beam::kProductGroups)
     p.staged = staged_out(&to, out, g.out_dtype, M, N, g.n_groups, ld_out, z_out);
-  return launched(beam::launch_pair_product(kind, nt, a_mn, b_mn, ta, tb, to, p, s));
+  return launched(beam::launch_pair_product(kind, nt, dual_rows(g), a_mn, b_mn, ta, tb, to, p, s));
 }
 
 // ------------------------------------------------------ orthogonalised update

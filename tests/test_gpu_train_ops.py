@@ -140,6 +140,44 @@ def test_every_row_tile_over_many_groups(pkg, rows):
     close(pkg.grouped_matmul_dx(y.bfloat16(), w, off), dx, mag, N)
 
 
+@pytest.mark.parametrize("counts", [
+    [257, 256, 320], [384, 385, 0, 257], [272], [320, 1, 383, 514, 300, 288, 255, 384],
+    [340] * 7], ids=str)
+@pytest.mark.parametrize("N,K", [(264, 1096), (136, 72), (129, 513)])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+def test_groups_of_two_row_blocks(pkg, counts, N, K, dt):
+    """Groups of 257 to 384 rows between others, mean groups of 226 to 340
+    rows: one tile of two row blocks; weights read along either axis."""
+    g = gen(sum(counts) + N)
+    off = bounds(counts)
+    E, n = len(counts), sum(counts)
+    x, dy = randn(g, n, K, dt=dt), randn(g, n, N, dt=dt)
+    for w in (randn(g, E, N, K, dt=dt, scale=0.1),
+              randn(g, E, K, N, dt=dt, scale=0.1).transpose(1, 2)):
+        y, mag = plain_product(x, w, off)
+        close(pkg.grouped_matmul(x, w, off), y, mag, K)
+        close(pkg.grouped_matmul(x, w, off, out_dtype=torch.float32), y, mag, K)
+        dx, mag = plain_product(dy, w.transpose(1, 2), off)
+        close(pkg.grouped_matmul_dx(dy, w, off), dx, mag, N)
+
+
+@pytest.mark.parametrize("N", [1, 7, 8, 33, 130, 1000])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_zero_rows_of_any_alignment(pkg, N, out):
+    """Rows outside all groups, in outputs of every base and row stride: zeros
+    there, and the neighbours of each row stay."""
+    g = gen(N)
+    off = bounds([3, 0, 5], lead=11)                        # rows 11 .. 19 of 60
+    x, w = randn(g, 60, 40), randn(g, 3, N, 40)
+    ref, mag = plain_product(x, w, off)
+    for at, ld in ((0, N), (1, N + 3), (5, N + 16), (8, N + 8)):
+        buf = torch.full((60, ld + at), 7.0, dtype=out, device="cuda")
+        pkg.grouped_matmul(x, w, off, out=buf[:, at:at + N])
+        close(buf[:, at:at + N].contiguous(), ref, mag, 40)
+        assert (buf[:11, at:at + N] == 0).all() and (buf[19:, at:at + N] == 0).all()
+        assert (buf[:, :at] == 7).all() and (buf[:, at + N:] == 7).all()
+
+
 def test_long_sums_in_32_bits(pkg):
     """FP32 results over a long k stay at FP32 accuracy (short chains, added in FP32)."""
     g = gen(5)
