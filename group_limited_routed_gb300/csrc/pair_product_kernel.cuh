@@ -654,7 +654,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_to_rank(cleared(s), 0));
+        if (lane == 0) arrive_release_smem_cluster(ptx::map_to_rank(cleared(s), 0));
       }
     }
     __syncwarp();
