@@ -84,10 +84,10 @@ using gemm::Waiter;
 
 constexpr int kWideBlocks = 8;  // k blocks per accumulator chain, FP32 outputs
 // FP32 weight gradients leave by bulk copy up to this many k blocks (16 x 256
-// rows: 145 us, plain stores 192), by plain stores beyond, where the copies
-// would queue in front of the next blocks' loads (16 x 400 rows: 231 us by
-// copy, 201 plain; 1024: 349, 331).
-constexpr int kStagedBlocks = 5;
+// rows: 149 us, plain stores 183; 350 rows: 178, 188), by plain stores beyond,
+// where the copies would queue in front of the next blocks' loads (400 rows:
+// 199 us by copy, 193 plain; 500: 220, 200).
+constexpr int kStagedBlocks = 6;
 
 // DUAL: a tile takes two blocks of rows j, one per TMEM buffer, that share the
 // stage's A, where the loads are what a tile waits for.  (The L2 gives an SM
