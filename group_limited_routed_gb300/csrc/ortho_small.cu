@@ -47,28 +47,38 @@ namespace beam {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kWarpCols = 128 / (kThreads / 128);  // columns of A and P per warp
-constexpr uint32_t kTile = 128 * 128;          // 128 rows of 64 F16 columns
-constexpr int kSliceMax = 320;                 // columns per CTA (256 for FP32 input)
-constexpr uint32_t kOffG = kSliceMax / 64 * kTile;
-constexpr uint32_t kOffP = kOffG + 2 * kTile;
-constexpr uint32_t kOffPart = kOffP + 2 * kTile;  // FP32 [128 columns][128 rows]; later X's low parts
-constexpr uint32_t kPartBytes = 128 * 128 * 4;
-constexpr uint32_t kOffMisc = kOffPart + kPartBytes;
-constexpr uint32_t kSmem = 1024 + kOffMisc + 32 + kThreads / 32 * 4 + 128 * 4;
-constexpr uint32_t kTmemStep = 128;            // TMEM column of P X
-static_assert(kSmem <= 227 * 1024, "shared memory budget");
+
+// Shared memory of matrices with m <= ROWS.  Tiles hold ROWS rows; the M = 128
+// products of 64-row tiles also read what lies behind and leave it in TMEM
+// lanes that nobody reads.
+template <int ROWS>
+struct SmallCfg {
+  static constexpr uint32_t TILE = ROWS * 128;         // ROWS rows of 64 F16 columns
+  static constexpr int SLICE = ROWS == 64 ? 512 : 320; // columns per CTA
+  static constexpr int SLICE_F32 = ROWS == 64 ? 512 : 256;  // (two F16 parts)
+  static constexpr uint32_t G = SLICE / 64 * TILE;
+  static constexpr uint32_t P = G + ROWS / 64 * TILE;
+  // FP32 [ROWS columns][ROWS rows]; later X's low parts
+  static constexpr uint32_t PART = P + ROWS / 64 * TILE;
+  static constexpr uint32_t MISC = PART + SLICE_F32 / 64 * TILE;
+  static constexpr uint32_t SMEM = 1024 + MISC + 32 + kThreads / 32 * 4 + 128 * 4;
+  static_assert(SMEM <= 227 * 1024, "shared memory budget");
+  static_assert(SLICE_F32 / 64 * TILE >= ROWS * ROWS * 4, "room for the partial sums");
+};
 
 // Byte offset of the 16-byte word of row r that holds columns 8w .. 8w + 7 of
 // the tiles at `base`.
+template <int ROWS>
 __device__ __forceinline__ uint32_t word_at(int r, int w) {
-  return static_cast<uint32_t>(w >> 3) * kTile + static_cast<uint32_t>(r) * 128 +
+  return static_cast<uint32_t>(w >> 3) * SmallCfg<ROWS>::TILE + static_cast<uint32_t>(r) * 128 +
          (static_cast<uint32_t>((w & 7) ^ (r & 7)) << 4);
 }
 
+template <int ROWS>
 __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr) {
-  // 64-column tiles kTile apart, groups of 8 rows (k) 1024 bytes apart
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(kTile >> 4) << 16) |
+  // 64-column tiles apart, groups of 8 rows (k) 1024 bytes apart
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
+         (static_cast<uint64_t>(SmallCfg<ROWS>::TILE >> 4) << 16) |
          (static_cast<uint64_t>(1024u >> 4) << 32) | (static_cast<uint64_t>(1u) << 46) |
          (static_cast<uint64_t>(2u) << 61);
 }
@@ -135,20 +145,22 @@ struct Raw8 {
   }
 };
 
-template <int TYPE>
+template <int TYPE, int ROWS>
 __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSmallArgs p) {
+  using C = SmallCfg<ROWS>;
+  constexpr int COLS = ROWS / (kThreads / 128);  // columns of A and P per warp
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = ptx::smem_addr(smem_raw);
   const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
-  const uint32_t x_at = raw_addr + pad, g_at = x_at + kOffG, p_at = x_at + kOffP,
-                 part_at = x_at + kOffPart;
-  uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + kOffMisc);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 16);
-  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + kOffMisc + 20);
-  uint32_t* share = reinterpret_cast<uint32_t*>(smem + kOffMisc + 24);  // this CTA's maximum
-  uint32_t* warp_max = reinterpret_cast<uint32_t*>(smem + kOffMisc + 32);
-  float* squares = reinterpret_cast<float*>(smem + kOffMisc + 32 + kThreads / 32 * 4);  // [128]
+  const uint32_t x_at = raw_addr + pad, g_at = x_at + C::G, p_at = x_at + C::P,
+                 part_at = x_at + C::PART;
+  uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + C::MISC);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC + 16);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + C::MISC + 20);
+  uint32_t* share = reinterpret_cast<uint32_t*>(smem + C::MISC + 24);  // this CTA's maximum
+  uint32_t* warp_max = reinterpret_cast<uint32_t*>(smem + C::MISC + 32);
+  float* squares = reinterpret_cast<float*>(smem + C::MISC + 32 + kThreads / 32 * 4);  // [128]
   const uint32_t bar = ptx::smem_addr(bar_mem);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -189,13 +201,13 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
   ptx::grid_dep_launch();
 
   // ------------------------------------------- the largest magnitude
-  constexpr int kItems = 128 * (TYPE == kF32 ? 256 : kSliceMax) / 8 / kThreads;
+  constexpr int kItems = ROWS * (TYPE == kF32 ? C::SLICE_F32 : C::SLICE) / 8 / kThreads;
   const bool vector_in = TYPE != kF32 && p.sc == 1 && p.sr % 8 == 0 && p.sz % 8 == 0 &&
                          (reinterpret_cast<uintptr_t>(p.src) & 15) == 0;
   Raw8<TYPE> raw[kItems];
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    int r = 128, w = 0;
+    int r = ROWS, w = 0;
     const int at = threadIdx.x + k * kThreads;
     if (at < items) item(at, r, w);
     raw[k].load(p, src, col0, ncols, r, w, vector_in);
@@ -253,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
           o[k] = half2_bits(a - __low2float(h), b - __high2float(h));
         }
       }
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + word_at(r, w)),
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst + word_at<ROWS>(r, w)),
                    "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
                    : "memory");
     }
@@ -280,6 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
   };
   const int quarter = warp & 3, part = warp >> 2;
   const int row = quarter * 32 + lane;  // TMEM lane
+  const bool live = ROWS == 128 || quarter < ROWS / 32;  // (lanes of the matrix)
   const uint32_t tq = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
   // the squared norm is the trace of the copy's A: FP32 sums in an order that
   // no memory layout of the update changes
@@ -299,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
     publish();
     if (warp == 0) {
       for (int k = 0; k < p.slice / 16; ++k) {
-        const uint32_t at = x_at + static_cast<uint32_t>(k >> 2) * kTile + (k & 3) * 32;
+        const uint32_t at = x_at + static_cast<uint32_t>(k >> 2) * C::TILE + (k & 3) * 32;
         if (elected)
           ptx::mma_bf16(tmem, ptx::sdesc_sw128(at), ptx::sdesc_sw128(at), idesc_m16, k ? 1u : 0u);
       }
@@ -310,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
     if (cs == 1) {
       // the whole sum is here: its trace, then A straight from TMEM
       if (t == 0) {
-        for (int c = part * kWarpCols; c < min(m16, (part + 1) * kWarpCols); c += 16) {
+        for (int c = part * COLS; live && c < min(m16, (part + 1) * COLS); c += 16) {
           uint32_t r[16];
           ptx::tmem_ld16(tq + c, r);
           ptx::tmem_wait_ld();
@@ -322,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
         norm();
       }
       const float gram_scale = t == 0 ? kScaleGram * inv * inv : kScaleGram / (kScaleX * kScaleX);
-      for (int c = part * kWarpCols; c < min(m16, (part + 1) * kWarpCols); c += 16) {
+      for (int c = part * COLS; live && c < min(m16, (part + 1) * COLS); c += 16) {
         uint32_t r[16];
         ptx::tmem_ld16(tq + c, r);
         ptx::tmem_wait_ld();
@@ -334,20 +347,20 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
 #pragma unroll
         for (int w = 0; w < 2; ++w)
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           g_at + word_at(row, (c >> 3) + w)),
+                           g_at + word_at<ROWS>(row, (c >> 3) + w)),
                        "r"(o[4 * w]), "r"(o[4 * w + 1]), "r"(o[4 * w + 2]), "r"(o[4 * w + 3])
                        : "memory");
       }
     } else {
       // partial sums, one column of 128 rows after another (A is symmetric:
       // column c is also row c)
-      for (int c = part * kWarpCols; c < min(m16, (part + 1) * kWarpCols); c += 16) {
+      for (int c = part * COLS; live && c < min(m16, (part + 1) * COLS); c += 16) {
         uint32_t r[16];
         ptx::tmem_ld16(tq + c, r);
         ptx::tmem_wait_ld();
 #pragma unroll
         for (int u = 0; u < 16; ++u)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(part_at + ((c + u) * 128 + row) * 4),
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(part_at + ((c + u) * ROWS + row) * 4),
                        "r"(r[u])
                        : "memory");
       }
@@ -357,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
       if (t == 0) {
         if (threadIdx.x < static_cast<unsigned>(m16)) {
           float d = 0.f;
-          const uint32_t from = part_at + threadIdx.x * (128 + 1) * 4;
+          const uint32_t from = part_at + threadIdx.x * (ROWS + 1) * 4;
           for (int q = 0; q < cs; ++q) d += __uint_as_float(load_peer(ptx::map_to_rank(from, q)));
           squares[threadIdx.x] = d;
         }
@@ -373,12 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
         const int r4 = at % quads * 4;
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int q = 0; q < cs; ++q) {
-          const float4 v = load_peer4(ptx::map_to_rank(part_at + (c * 128 + r4) * 4, q));
+          const float4 v = load_peer4(ptx::map_to_rank(part_at + (c * ROWS + r4) * 4, q));
           s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
         }
         const uint32_t lo = half2_bits(s.x * gram_scale, s.y * gram_scale);
         const uint32_t hi = half2_bits(s.z * gram_scale, s.w * gram_scale);
-        const uint32_t to = g_at + word_at(c, r4 >> 3) + (r4 & 4) * 2;
+        const uint32_t to = g_at + word_at<ROWS>(c, r4 >> 3) + (r4 & 4) * 2;
         for (int q = 0; q < cs; ++q) store_peer2(ptx::map_to_rank(to, q), lo, hi);
       }
       asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
@@ -388,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
     publish();
     if (warp == 0) {
       for (int k = 0; k < m16 / 16; ++k) {
-        const uint32_t at = g_at + static_cast<uint32_t>(k >> 2) * kTile + (k & 3) * 32;
+        const uint32_t at = g_at + static_cast<uint32_t>(k >> 2) * C::TILE + (k & 3) * 32;
         if (elected)
           ptx::mma_bf16(tmem, ptx::sdesc_sw128(at), ptx::sdesc_sw128(at), idesc_m16, k ? 1u : 0u);
       }
@@ -403,13 +416,13 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
       const float ca = kScalePoly * p.c / (kScaleGram * kScaleGram);
       const float cb = kScalePoly * p.b / kScaleGram;
       const float cd = kScalePoly * p.a;
-      for (int c = part * kWarpCols; c < min(m16, (part + 1) * kWarpCols); c += 16) {
+      for (int c = part * COLS; live && c < min(m16, (part + 1) * COLS); c += 16) {
         uint32_t r[16];
         ptx::tmem_ld16(tq + c, r);
         ptx::tmem_wait_ld();
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          const uint32_t at = word_at(row, (c >> 3) + w);
+          const uint32_t at = word_at<ROWS>(row, (c >> 3) + w);
           uint32_t g[4], o[4];
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(g[0]), "=r"(g[1]), "=r"(g[2]), "=r"(g[3])
@@ -438,11 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
         const uint32_t nn = static_cast<uint32_t>(min(256, p.slice - n0));
         const uint32_t idesc = kF16Idesc | (1u << 16) | ((nn >> 3) << 17);  // B MN-major
         for (int pass = 0; pass < (low ? 2 : 1); ++pass) {
-          const uint32_t xb = (pass ? part_at : x_at) + static_cast<uint32_t>(n0 / 64) * kTile;
+          const uint32_t xb = (pass ? part_at : x_at) + static_cast<uint32_t>(n0 / 64) * C::TILE;
           for (int k = 0; k < m16 / 16; ++k) {
-            const uint32_t at = p_at + static_cast<uint32_t>(k >> 2) * kTile + (k & 3) * 32;
+            const uint32_t at = p_at + static_cast<uint32_t>(k >> 2) * C::TILE + (k & 3) * 32;
             if (elected)
-              ptx::mma_bf16(tmem + kTmemStep + n0, ptx::sdesc_sw128(at), desc_mn(xb + k * 2048),
+              ptx::mma_bf16(tmem + n0, ptx::sdesc_sw128(at), desc_mn<ROWS>(xb + k * 2048),
                             idesc, (pass | k) ? 1u : 0u);
           }
         }
@@ -452,9 +465,9 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
     }
     finish();
     const float x_scale = (last ? 1.f : kScaleX) / kScalePoly * (t == 0 ? inv : 1.f / kScaleX);
-    for (int c = part * 16; c < p.slice; c += kThreads / 128 * 16) {
+    for (int c = part * 16; live && c < p.slice; c += kThreads / 128 * 16) {
       uint32_t r[16];
-      ptx::tmem_ld16(tq + kTmemStep + c, r);
+      ptx::tmem_ld16(tq + c, r);
       ptx::tmem_wait_ld();
       float v[16];
 #pragma unroll
@@ -464,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
 #pragma unroll
           for (int w = 0; w < 2; ++w)
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                             x_at + word_at(row, (c >> 3) + w)),
+                             x_at + word_at<ROWS>(row, (c >> 3) + w)),
                          "r"(half2_bits(v[w * 8], v[w * 8 + 1])),
                          "r"(half2_bits(v[w * 8 + 2], v[w * 8 + 3])),
                          "r"(half2_bits(v[w * 8 + 4], v[w * 8 + 5])),
@@ -509,9 +522,10 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
   }
 }
 
-template <int TYPE>
-cudaError_t launch_typed(const OrthoSmallArgs& p, int32_t batch, cudaStream_t s) {
-  constexpr auto kern = ortho_small_kernel<TYPE>;
+template <int TYPE, int ROWS>
+cudaError_t launch_sized(const OrthoSmallArgs& p, int32_t batch, cudaStream_t s) {
+  constexpr auto kern = ortho_small_kernel<TYPE, ROWS>;
+  constexpr uint32_t kSmem = SmallCfg<ROWS>::SMEM;
   const cudaError_t err = smem_limit_once<kern>(static_cast<int>(kSmem));
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr[2];
@@ -531,11 +545,17 @@ cudaError_t launch_typed(const OrthoSmallArgs& p, int32_t batch, cudaStream_t s)
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+template <int TYPE>
+cudaError_t launch_typed(const OrthoSmallArgs& p, int32_t batch, cudaStream_t s) {
+  return p.m <= 64 ? launch_sized<TYPE, 64>(p, batch, s) : launch_sized<TYPE, 128>(p, batch, s);
+}
+
 // Whether the device runs the kernel in clusters of 16 (asked once per device
 // and kernel).
-template <int TYPE>
+template <int TYPE, int ROWS>
 bool large_clusters_once() {
-  constexpr auto kern = ortho_small_kernel<TYPE>;
+  constexpr auto kern = ortho_small_kernel<TYPE, ROWS>;
+  constexpr uint32_t kSmem = SmallCfg<ROWS>::SMEM;
   static std::mutex mu;
   static int known[kMaxDevices] = {};  // 0: not asked, 1: no, 2: yes
   int dev = 0;
@@ -565,11 +585,12 @@ bool large_clusters_once() {
   return known[dev] == 2;
 }
 
+template <int ROWS>
 bool large_clusters(int32_t type) {
   switch (type) {
-    case kBf16: return large_clusters_once<kBf16>();
-    case kF16: return large_clusters_once<kF16>();
-    case kF32: return large_clusters_once<kF32>();
+    case kBf16: return large_clusters_once<kBf16, ROWS>();
+    case kF16: return large_clusters_once<kF16, ROWS>();
+    case kF32: return large_clusters_once<kF32, ROWS>();
   }
   return false;
 }
@@ -579,17 +600,24 @@ bool large_clusters(int32_t type) {
 bool ortho_small_shape(int32_t batch, int32_t m, int32_t n, int32_t type, int num_sms,
                        int32_t* cluster, int32_t* slice) {
   if (m > kOrthoSmallM) return false;
-  const int32_t most = type == kF32 ? 256 : kSliceMax;
+  const int32_t most = m <= 64         ? SmallCfg<64>::SLICE
+                       : type == kF32 ? SmallCfg<128>::SLICE_F32
+                                      : SmallCfg<128>::SLICE;
   const int32_t least = (n + most - 1) / most;  // CTAs
   if (least > kOrthoSmallCluster) return false;
   // clusters of more than 8 CTAs depend on the device
-  if (least > 8 && !large_clusters(type)) return false;
+  if (least > 8 && !(m <= 64 ? large_clusters<64>(type) : large_clusters<128>(type))) return false;
   // One CTA needs no exchange (128 x 128, five steps: 21 us in one CTA, 33 in
-  // two).  Beyond, more CTAs than needed while the stack leaves SMs free and
-  // a slice has more than 64 columns, for the loads and epilogues (64 x 512:
-  // 28 us in 2 CTAs, 26 in 8; 128 x 300, FP32: 69 us in 2, 53 in 5).
+  // two; 64 x 384: 22.6 in one, 24.3 in more).  Beyond, more CTAs than needed
+  // while the stack leaves SMs free -- clusters of 8 do not fill every part of
+  // the device: 16 x 64 x 512 takes 48 us in 8 CTAs each, 23 in 4 -- and a
+  // slice has more columns than `aim`, for the loads and epilogues (64 x 512:
+  // 25.8 us in one CTA, 26.0 in 2, 23.1 in 4, 23.4 in 8; 64 x 1024: 33.7 in 2,
+  // 27.2 in 4, 25.2 in 8; 128 x 300, FP32: 69 us in 2, 53 in 5).
   int32_t c = least;
-  while (c > 1 && c < 8 && batch * (c + 1) <= num_sms && (n + c - 1) / c > 64) ++c;
+  const int32_t aim = m <= 64 ? 128 : 64;
+  const bool spread = m <= 64 ? n > 384 : c > 1;
+  while (spread && c < 8 && batch * (c + 1) <= num_sms * 3 / 4 && (n + c - 1) / c > aim) ++c;
   *cluster = c;
   *slice = ((n + c - 1) / c + 63) / 64 * 64;
   // whole slices of 64 may need fewer CTAs than c
