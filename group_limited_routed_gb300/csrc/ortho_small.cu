@@ -3,9 +3,9 @@
 //
 // Taken product by product such an update is a chain of 15 launches (steps of
 // ortho_chain.cu) of a few microseconds, each with next to no work: 64 x 512
-// took 79 us, here 26.  Here a cluster of up to 16 CTAs
-// holds one matrix X [m, n] (n the larger extent; a tall matrix is held
-// transposed) in shared memory for all steps, each CTA a slice of columns:
+// took 79 us, here 23.  Here one CTA or a cluster of up to 16 holds one matrix
+// X [m, n] (n the larger extent; a tall matrix is held transposed) in shared
+// memory for all steps, each CTA a slice of columns:
 //
 //   A = X X^T       each CTA the product of its slice (tcgen05, M = 128); the
 //                   partial sums are added in FP32 over the cluster in rank
@@ -13,15 +13,18 @@
 //   P = aI + bA + cA^2    every CTA for itself
 //   X <- P X        each CTA its own slice, in place
 //
-// One layout serves both uses of X: tiles of 128 rows by 64 columns, 128-byte
-// rows with the 128-byte swizzle.  Read with rows as M or N and columns as k
-// it is a K-major operand (A = X X^T), with columns as N and rows as k an
-// MN-major one (P X).
+// One layout serves both uses of X: tiles of 128 rows (64 where m allows it) by
+// 64 columns, 128-byte rows with the 128-byte swizzle.  Read with rows as M or
+// N and columns as k it is a K-major operand (A = X X^T), with columns as N and
+// rows as k an MN-major one (P X).
 //
 // F16 operands with the scales and the FP32 second part of the first step as
 // in beam_moe_orthogonalize.
 //
-// Latency bound.  In one CTA (n <= 320, 256 for FP32) a step is three
+// 64-row tiles let one CTA hold 512 columns: 64 x 384 takes 23.0 us where a
+// cluster with 128-row tiles took 25.9, a stack of 300 x 64 x 512 52 us (114).
+//
+// Latency bound.  In one CTA (128 rows: n <= 320, 256 for FP32) a step is three
 // tensor-core products of a few hundred cycles, their epilogues and three
 // block barriers: 2.7 us at 128 x 128.  In a cluster the exchange of the
 // partial sums adds two cluster barriers and 96 KB per CTA through distributed
@@ -58,8 +61,10 @@ struct SmallCfg {
   static constexpr int SLICE_F32 = ROWS == 64 ? 512 : 256;  // (two F16 parts)
   static constexpr uint32_t G = SLICE / 64 * TILE;
   static constexpr uint32_t P = G + ROWS / 64 * TILE;
+  // P's second F16 part (64 rows)
+  static constexpr uint32_t P_LOW = P + ROWS / 64 * TILE;
   // FP32 [ROWS columns][ROWS rows]; later X's low parts
-  static constexpr uint32_t PART = P + ROWS / 64 * TILE;
+  static constexpr uint32_t PART = P_LOW + (ROWS == 64 ? TILE : 0);
   static constexpr uint32_t MISC = PART + SLICE_F32 / 64 * TILE;
   static constexpr uint32_t SMEM = 1024 + MISC + 32 + kThreads / 32 * 4 + 128 * 4;
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
@@ -149,12 +154,18 @@ template <int TYPE, int ROWS>
 __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSmallArgs p) {
   using C = SmallCfg<ROWS>;
   constexpr int COLS = ROWS / (kThreads / 128);  // columns of A and P per warp
+  // P in two F16 parts where rows are few: its rounding moves parts of the
+  // largest singular direction into the small ones, and with few of them one
+  // weighs (7 x 600: up to 4.4e-3 of the result's norm over 400 draws, 2.6e-3
+  // with two parts; 48 x 600: 2.8e-3, 2.0e-3).  64 x 384 would take 25.3 us
+  // for 22.8, 8 x 512 takes 18.7 for 18.2.
+  const bool fine = ROWS == 64 && p.m <= 32;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = ptx::smem_addr(smem_raw);
   const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
   const uint32_t x_at = raw_addr + pad, g_at = x_at + C::G, p_at = x_at + C::P,
-                 part_at = x_at + C::PART;
+                 p_low_at = x_at + C::P_LOW, part_at = x_at + C::PART;
   uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + C::MISC);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC + 16);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + C::MISC + 20);
@@ -423,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const uint32_t at = word_at<ROWS>(row, (c >> 3) + w);
-          uint32_t g[4], o[4];
+          uint32_t g[4], o[4], l[4];
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(g[0]), "=r"(g[1]), "=r"(g[2]), "=r"(g[3])
                        : "r"(g_at + at)
@@ -437,10 +448,18 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
             if (col == row) a += cd;
             if (col + 1 == row) b += cd;
             o[k] = half2_bits(a, b);
+            if (fine) {
+              const __half2 p2 = *reinterpret_cast<const __half2*>(&o[k]);
+              l[k] = half2_bits(a - __low2float(p2), b - __high2float(p2));
+            }
           }
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_at + at), "r"(o[0]),
                        "r"(o[1]), "r"(o[2]), "r"(o[3])
                        : "memory");
+          if (fine)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_low_at + at), "r"(l[0]),
+                         "r"(l[1]), "r"(l[2]), "r"(l[3])
+                         : "memory");
         }
       }
     }
@@ -450,15 +469,18 @@ __global__ void __launch_bounds__(kThreads, 1) ortho_small_kernel(const OrthoSma
       for (int n0 = 0; n0 < p.slice; n0 += 256) {
         const uint32_t nn = static_cast<uint32_t>(min(256, p.slice - n0));
         const uint32_t idesc = kF16Idesc | (1u << 16) | ((nn >> 3) << 17);  // B MN-major
-        for (int pass = 0; pass < (low ? 2 : 1); ++pass) {
-          const uint32_t xb = (pass ? part_at : x_at) + static_cast<uint32_t>(n0 / 64) * C::TILE;
+        auto product = [&](uint32_t pb, uint32_t xb, bool first) {
+          xb += static_cast<uint32_t>(n0 / 64) * C::TILE;
           for (int k = 0; k < m16 / 16; ++k) {
-            const uint32_t at = p_at + static_cast<uint32_t>(k >> 2) * C::TILE + (k & 3) * 32;
+            const uint32_t at = pb + static_cast<uint32_t>(k >> 2) * C::TILE + (k & 3) * 32;
             if (elected)
               ptx::mma_bf16(tmem + n0, ptx::sdesc_sw128(at), desc_mn<ROWS>(xb + k * 2048),
-                            idesc, (pass | k) ? 1u : 0u);
+                            idesc, first && k == 0 ? 0u : 1u);
           }
-        }
+        };
+        product(p_at, x_at, true);
+        if (fine) product(p_low_at, x_at, false);
+        if (low) product(p_at, part_at, false);
       }
       if (elected) ptx::mma_commit(bar);
       __syncwarp();
@@ -618,6 +640,12 @@ bool ortho_small_shape(int32_t batch, int32_t m, int32_t n, int32_t type, int nu
   const int32_t aim = m <= 64 ? 128 : 64;
   const bool spread = m <= 64 ? n > 384 : c > 1;
   while (spread && c < 8 && batch * (c + 1) <= num_sms * 3 / 4 && (n + c - 1) / c > aim) ++c;
+  // slices of more than 256 columns: 16 CTAs, where a few matrices leave room
+  // for such clusters (64 x 4096: 37.0 us in 8, 34.4 in 16; four of them 37.4,
+  // 35.0, eight 37.8, 69; with 128-row tiles 128 x 2048: 49.9, 53.2)
+  if (m <= 64 && c >= 8 && n > 8 * 256 && batch * kOrthoSmallCluster <= num_sms / 2 &&
+      large_clusters<64>(type))
+    c = kOrthoSmallCluster;
   *cluster = c;
   *slice = ((n + c - 1) / c + 63) / 64 * 64;
   // whole slices of 64 may need fewer CTAs than c

@@ -505,6 +505,22 @@ def test_update_over_shapes(pkg, b, R, C, dt):
         assert off <= 4e-3, (i, off)
 
 
+@pytest.mark.parametrize("b,R,C", [(1, 64, 384), (1, 64, 385), (1, 65, 384), (2, 64, 513),
+                                   (1, 50, 1025), (1, 64, 4096), (1, 17, 8192), (1, 30, 8200),
+                                   (1, 120, 5120), (17, 64, 700), (5, 2500, 60), (40, 7, 600),
+                                   (20, 128, 512), (160, 64, 100)])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_update_over_small_extents(pkg, b, R, C, dt):
+    """Both tile heights, one CTA and clusters of every size, more clusters
+    than the device runs at once, widths just past one launch's limit."""
+    m = momentum(gen(R * 31 + C + b), b, R, C, dt)
+    got = pkg.orthogonalize(m)
+    for i in range(b):
+        ref = plain_update(m[i])
+        off = ((got[i].double() - ref).norm() / ref.norm()).item()
+        assert off <= 4e-3, (i, off)
+
+
 def test_update_steps_coefficients_and_layouts(pkg):
     g = gen(7)
     m = momentum(g, 2, 96, 160, torch.bfloat16)
