@@ -83,6 +83,8 @@ beam_status_t device_ready(beam::host::DevInfo* dev) {
 beam_status_t launched(cudaError_t e) { return e == cudaSuccess ? BEAM_OK : BEAM_ERR_CUDA; }
 
 // ------------------------------------------------------------------ operands
+constexpr int64_t kPackAlign = 16;   // elements: rows of copies begin on 32-byte sectors
+
 // A 16-bit operand [z][outer][inner]: where TMA can read it in place (16-byte
 // base and strides) it does, else an aligned copy in the workspace stands in.
 struct Operand {
@@ -98,7 +100,7 @@ struct Operand {
     return (reinterpret_cast<uintptr_t>(base) & 15u) == 0 && ld % 8 == 0 && zs % 8 == 0;
   }
   size_t packed_bytes() const {
-    return align_up(static_cast<size_t>(z) * outer * round_up(inner, 8) * 2);
+    return align_up(static_cast<size_t>(z) * outer * round_up(inner, kPackAlign) * 2);
   }
   // The copy that puts an aligned stand-in at dst, and this operand there.
   beam::PackArgs pack_into(void* dst, const int32_t* offsets) {
@@ -109,7 +111,7 @@ struct Operand {
     p.zs = z;
     p.rows = outer;
     p.cols = static_cast<int32_t>(inner);
-    p.ld = static_cast<int32_t>(round_up(inner, 8));
+    p.ld = static_cast<int32_t>(round_up(inner, kPackAlign));
     p.dst = static_cast<uint16_t*>(dst);
     p.offsets = z > 1 ? offsets : nullptr;  // a stack: one matrix per group
     base = dst;
