@@ -82,7 +82,7 @@ cudaError_t launch_pair_product(int kind, int nt, bool dual, bool a_mn, bool b_m
     }
     return cudaErrorInvalidValue;
   }
-  const int64_t tiles = mt * ((p.N + nt - 1) / nt) * p.groups;
+  const int64_t tiles = mt * ((p.N + nt - 1) / nt) * p.groups * p.parts;
   if (kind == kProductGroups && a_mn && b_mn && nt == 256)
     return p.out_type == kF32
                ? launch_impl<256, true, true, kProductGroups, true>(a, b, out, p, tiles, s)

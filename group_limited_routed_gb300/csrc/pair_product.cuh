@@ -25,11 +25,12 @@ struct ProductArgs {
   int32_t k_blocks;        // 64-wide blocks of k (kProductRows)
   int32_t a_z;             // A's z per group: 1, or 0 where all groups share one matrix
   int32_t groups;          // groups E
+  int32_t parts;           // kProductGroups: results per group, each of a part of its rows
   int32_t rows;            // rows in all
   const int32_t* offsets;  // [groups + 1] first row of each group
   void* out;
   int64_t ld_out;          // elements between output rows
-  int64_t z_out;           // elements between the groups' outputs (kProductGroups)
+  int64_t z_out;           // elements between outputs (kProductGroups: part by part of each group)
   int32_t out_type;        // kBf16, kF16 or kF32
   int32_t in_type;         // kBf16 or kF16
   int32_t accumulate;      // out += (kF32 outputs)

@@ -163,7 +163,7 @@ __device__ __forceinline__ void load_rows(const ProductMaps& b, int n, uint32_t 
   }
 }
 
-// Zeros over a row, by the lanes of a warp: single elements up to a 16-byte
+// Zeros over n elements, by the lanes of a warp: single elements up to a 16-byte
 // boundary and behind the last one, whole vectors between.
 template <typename T>
 __device__ __forceinline__ void zero_row(T* row, int n, int lane) {
@@ -273,8 +273,16 @@ struct ProductWalk {
       if (z != known_z) {
         // made safe to index with: inside the rows, not backwards
         known_z = z;
-        k_first = min(max(p.offsets[z], 0), p.rows);
-        k_rows = max(0, min(p.offsets[z + 1], p.rows) - k_first);
+        const int group = p.parts == 1 ? z : z / p.parts;
+        k_first = min(max(p.offsets[group], 0), p.rows);
+        k_rows = max(0, min(p.offsets[group + 1], p.rows) - k_first);
+        if (p.parts > 1) {
+          // equal parts in whole k blocks
+          const int blocks = (k_rows + kPBK - 1) / kPBK;
+          const int skip = min(k_rows, (z - group * p.parts) * ((blocks + p.parts - 1) / p.parts) * kPBK);
+          k_first += skip;
+          k_rows = min(k_rows - skip, (blocks + p.parts - 1) / p.parts * kPBK);
+        }
       }
       t.k0 = k_first;
       t.k_count = k_rows;
@@ -411,7 +419,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   if constexpr (KIND == kProductRows)
     num_tiles = s_start[p.groups];
   else
-    num_tiles = p.groups * ((p.M + kProductTileM - 1) / kProductTileM) *
+    num_tiles = p.groups * p.parts * ((p.M + kProductTileM - 1) / kProductTileM) *
                 ((p.N + Walk::kSpan - 1) / Walk::kSpan);
   const Waiter W{abort_flag, p.status, p.wait_limit_ns};
 
@@ -693,10 +701,26 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int i = t.i0 + static_cast<int>(rank) * 128 + q * 32 + lane;
       const int64_t zbase = KIND == kProductRows ? 0 : static_cast<int64_t>(t.z) * p.z_out;
       const int ncols = min(t.nvalid - col_begin, COLS);  // <= 0: nothing for this warp
-      // a group without rows adds nothing
-      if (WIDE && KIND == kProductGroups && p.accumulate && t.k_blocks == 0) continue;
+      if (KIND == kProductGroups && t.k_blocks == 0) {
+        // No rows: nothing to add, or zeros -- each tile's CTAs write one
+        // stretch of the group's dense result, a warp 1/16 of it.  (As rows
+        // of the tile's columns 162 groups of 1256 x 704, half of them
+        // empty, took 86 us, so 56.)
+        if (p.accumulate) continue;
+        const int64_t pieces = static_cast<int64_t>(walk.mt) * walk.nt * (2 * kPEpiWarps);
+        const int64_t piece =
+            ((static_cast<int64_t>(t.j0 / Walk::kSpan) * walk.mt + t.i0 / kProductTileM) * 2 + rank) *
+                kPEpiWarps + warp - 3;
+        const int64_t from = p.z_out * piece / pieces;
+        const int n = static_cast<int>(p.z_out * (piece + 1) / pieces - from);
+        if (WIDE)
+          zero_row(static_cast<float*>(p.out) + zbase + from, n, lane);
+        else
+          zero_row(static_cast<uint16_t*>(p.out) + zbase + from, n, lane);
+        continue;
+      }
       const bool by_copy = C::STAGED && p.staged && t.k_blocks <= kStagedBlocks;
-      if (WIDE && KIND == kProductGroups && t.k_blocks > 0 && t.k_blocks <= kWideBlocks &&
+      if (WIDE && KIND == kProductGroups && t.k_blocks <= kWideBlocks &&
           (by_copy || !p.accumulate)) {
         // one chain: straight from TMEM to the stores
         if (!W.wait(tfull(acc), acc_phase)) break;
@@ -800,35 +824,25 @@ __global__ void __launch_bounds__(kPThreads, 1)
         // Rows (2c, 2c + 1) of this lane's column, packed; the accumulator is
         // free again before any store.
         auto drain = [&](uint32_t(&packed)[COLS / 2], int ncols) {
-          const bool live = t.k_blocks > 0;
-          if (live) {
-            if (!W.wait(tfull(acc), acc_phase)) return false;
-            ptx::tc_fence_after();
-          }
+          if (!W.wait(tfull(acc), acc_phase)) return false;
+          ptx::tc_fence_after();
           const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * NT + col_begin;
 #pragma unroll
           for (int c = 0; c < COLS; c += LD) {
             if (c < ncols) {
               uint32_t r[LD];
-              if (live) tmem_ld(tq + c, r);
-              if (live) {
-                ptx::tmem_wait_ld();
-              } else {
-#pragma unroll
-                for (int u = 0; u < LD; ++u) r[u] = 0u;
-              }
+              tmem_ld(tq + c, r);
+              ptx::tmem_wait_ld();
 #pragma unroll
               for (int u = 0; u < LD; u += 2)
                 packed[(c + u) / 2] = pack_out(__uint_as_float(r[u]), __uint_as_float(r[u + 1]), f16);
             }
           }
-          if (live) {
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_relaxed_cluster(ptx::map_to_rank(tempty(acc), 0));
-            acc ^= 1;
-            if (acc == 0) acc_phase ^= 1u;
-          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_relaxed_cluster(ptx::map_to_rank(tempty(acc), 0));
+          acc ^= 1;
+          if (acc == 0) acc_phase ^= 1u;
           return true;
         };
         auto store = [&](const uint32_t(&packed)[COLS / 2], int j0, int ncols) {

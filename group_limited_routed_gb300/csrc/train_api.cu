@@ -187,17 +187,47 @@ bool dual_rows(const beam_moe_grouped_t& g) {
   return g.out_dtype != BEAM_DTYPE_F32 && mean > 224 && mean <= 352;
 }
 
+// Parts that a weight gradient's sums over rows are taken in.  Few tiles with
+// long sums leave SM pairs idle (1 group of 65536 rows, 1024 x 1024: 16 tiles
+// of 76 pairs, 546 us in one part, 111 in five); each part is an FP32 result
+// in the workspace that a second kernel adds in order, which soon costs more
+// than it gives (8 x 2048 rows, 1024 x 1024: 37 us in one part, 68 in five).
+// The estimate is waves of tiles times their k blocks at 0.36 us, 1.5 us a
+// tile, and the parts' bytes written and read at 5 TB/s; parts have to win a
+// fifth.
+int32_t grad_parts(const beam_moe_grouped_t& g) {
+  constexpr double kPairs = 76;
+  const double tiles = static_cast<double>((g.K + 255ll) / 256 * ((g.N + 255ll) / 256) * g.n_groups);
+  const double blocks = static_cast<double>((g.rows / g.n_groups + 63) / 64);
+  if (tiles > 2 * kPairs || blocks < 32) return 1;
+  const double part_us = 2. * 4. * g.n_groups * g.N * g.K / 5e6;
+  auto cost = [&](int32_t parts) {
+    return std::ceil(tiles * parts / kPairs) * (std::ceil(blocks / parts) * 0.36 + 1.5) +
+           (parts > 1 ? 4. + parts * part_us : 0.);
+  };
+  int32_t best = 1;
+  for (int32_t parts = 2; parts <= 16 && parts * 8 <= blocks; ++parts)
+    if (cost(parts) < (best == 1 ? 0.8 : 1.) * cost(best)) best = parts;
+  return best;
+}
+size_t parts_bytes(const beam_moe_grouped_t& g, int32_t parts) {
+  return parts > 1 ? align_up(static_cast<size_t>(g.n_groups) * parts * g.N * g.K * 4) : 0;
+}
+
 // Common tail of the three products.
 beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool a_mn, bool b_mn,
                              Operand a, Operand b, int64_t M, int64_t N, int64_t k,
                              const int32_t* offsets, void* out, int64_t ld_out, int64_t z_out,
                              int accumulate, void* ws, size_t ws_bytes, cudaStream_t s) {
   const bool pack_a = !a.in_place(), pack_b = !b.in_place();
+  const int32_t parts = kind == beam::kProductGroups ? grad_parts(g) : 1;
   size_t need = kAlign;
   const size_t at_a = need;
   if (pack_a) need += a.packed_bytes();
   const size_t at_b = need;
   if (pack_b) need += b.packed_bytes();
+  const size_t at_parts = need;
+  need += parts_bytes(g, parts);
   if (ws_bytes < need) return BEAM_ERR_WORKSPACE;
   beam::host::DevInfo dev;
   const beam_status_t st = device_ready(&dev);
@@ -224,6 +254,7 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   p.k_blocks = static_cast<int32_t>((k + 63) / 64);
   p.a_z = a.z > 1 ? 1 : 0;
   p.groups = g.n_groups;
+  p.parts = parts;
   p.rows = static_cast<int32_t>(g.rows);
   p.offsets = offsets;
   p.out = out;
@@ -234,11 +265,28 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
   p.accumulate = accumulate;
   p.status = static_cast<uint32_t*>(ws);
   p.wait_limit_ns = beam::host::wait_limit_ns();
+  if (parts > 1) {
+    p.out = static_cast<uint8_t*>(ws) + at_parts;
+    p.out_type = BEAM_DTYPE_F32;
+    p.accumulate = 0;
+  }
   CUtensorMap to = {};
   // (rows leave straight from registers)
   if (kind == beam::kProductGroups)
-    p.staged = staged_out(&to, out, g.out_dtype, M, N, g.n_groups, ld_out, z_out);
-  return launched(beam::launch_pair_product(kind, nt, dual_rows(g), a_mn, b_mn, ta, tb, to, p, s));
+    p.staged = staged_out(&to, p.out, p.out_type, M, N, static_cast<int64_t>(g.n_groups) * parts,
+                          ld_out, z_out);
+  const cudaError_t err =
+      beam::launch_pair_product(kind, nt, dual_rows(g), a_mn, b_mn, ta, tb, to, p, s);
+  if (err != cudaSuccess || parts == 1) return launched(err);
+  beam::JoinArgs j = {};
+  j.part = static_cast<const float*>(p.out);
+  j.n = z_out;
+  j.groups = g.n_groups;
+  j.parts = parts;
+  j.out = out;
+  j.out_type = g.out_dtype;
+  j.accumulate = accumulate;
+  return launched(beam::launch_join(j, dev.sms, s));
 }
 
 // ------------------------------------------------------ orthogonalised update
@@ -315,7 +363,7 @@ size_t beam_moe_grouped_matmul_workspace_size(const beam_moe_grouped_t* g, int32
   const Operand ops[3] = {operand_x(*g, nullptr), operand_y(*g, nullptr), operand_w(*g, nullptr)};
   for (const Operand& o : ops)
     if (unaligned || !o.in_place()) need += o.packed_bytes();
-  return need;
+  return need + parts_bytes(*g, grad_parts(*g));
 }
 
 beam_status_t beam_moe_grouped_matmul(const beam_moe_grouped_t* g, const void* x, const void* w,

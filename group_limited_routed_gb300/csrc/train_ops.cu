@@ -97,6 +97,52 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// ------------------------------------------------------------ sums of parts
+// V consecutive elements a thread, a row of blocks a group.  Memory bound:
+// 4 bytes read per part and element, most of them still in the L2.
+template <int V>
+__global__ void __launch_bounds__(256) join_kernel(const JoinArgs p) {
+  ptx::grid_dep_wait();
+  ptx::grid_dep_launch();
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256 * V;
+  for (int e = blockIdx.y; e < p.groups; e += gridDim.y) {
+    const float* src = p.part + e * p.parts * p.n;
+    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * V; i < p.n; i += step) {
+      float sum[V];
+#pragma unroll
+      for (int u = 0; u < V; ++u) sum[u] = 0.f;
+#pragma unroll 4
+      for (int q = 0; q < p.parts; ++q) {
+        if constexpr (V == 4) {
+          const float4 v = __ldcs(reinterpret_cast<const float4*>(src + q * p.n + i));
+          sum[0] += v.x, sum[1] += v.y, sum[2] += v.z, sum[3] += v.w;
+        } else {
+          sum[0] += __ldcs(src + q * p.n + i);
+        }
+      }
+      if (p.out_type == kF32) {
+        float* out = static_cast<float*>(p.out) + e * p.n + i;
+#pragma unroll
+        for (int u = 0; u < V; ++u) sum[u] += p.accumulate ? out[u] : 0.f;
+        if constexpr (V == 4)
+          *reinterpret_cast<float4*>(out) = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        else
+          *out = sum[0];
+      } else {
+        uint16_t* out = static_cast<uint16_t*>(p.out) + e * p.n + i;
+        const bool f16 = p.out_type == kF16;
+        if constexpr (V == 4) {
+          *reinterpret_cast<uint2*>(out) =
+              f16 ? make_uint2(pack16<true>(sum[0], sum[1]), pack16<true>(sum[2], sum[3]))
+                  : make_uint2(pack16<false>(sum[0], sum[1]), pack16<false>(sum[2], sum[3]));
+        } else {
+          *out = static_cast<uint16_t>(f16 ? pack16<true>(sum[0], 0.f) : pack16<false>(sum[0], 0.f));
+        }
+      }
+    }
+  }
+}
+
 // -------------------------------------------------------------- gated rows
 // h = w_r * g * sigma(g) * u with sigma(g) = 1 / (1 + e^-g), in FP32, rounded
 // once.  Fast exponential and divide: a few parts in 10^7, far below the
@@ -389,6 +435,15 @@ cudaError_t launch_pack(const PackArgs* p, int n, cudaStream_t s) {
   if (blocks == 0) return cudaSuccess;
   return launch_dependent(pack_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, s, p[0],
                           b, units_a, units);
+}
+
+cudaError_t launch_join(const JoinArgs& p, int num_sms, cudaStream_t s) {
+  const bool vec = p.n % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+  const int64_t want = (p.n + 256 * (vec ? 4 : 1) - 1) / (256 * (vec ? 4 : 1));
+  const int64_t most = std::max<int64_t>(1, static_cast<int64_t>(num_sms) * 16 / p.groups);
+  const dim3 grid(static_cast<unsigned>(std::min(want, most)), static_cast<unsigned>(p.groups));
+  return vec ? launch_dependent(join_kernel<4>, grid, dim3(256), 0, s, p)
+             : launch_dependent(join_kernel<1>, grid, dim3(256), 0, s, p);
 }
 
 cudaError_t launch_gate(const GateArgs& p, int num_sms, cudaStream_t s) {

@@ -25,6 +25,19 @@ struct PackArgs {
 // n = 0, 1 or 2 operands, in one launch.
 cudaError_t launch_pack(const PackArgs* p, int n, cudaStream_t s);
 
+// ------------------------------------------------------- sums of parts
+// out[e][i] (+)= part[e * parts][i] + part[e * parts + 1][i] + ..., in that
+// order, i < n.
+struct JoinArgs {
+  const float* part;
+  int64_t n;
+  int32_t groups, parts;
+  void* out;
+  int32_t out_type;        // kBf16, kF16 or kF32
+  int32_t accumulate;      // kF32
+};
+cudaError_t launch_join(const JoinArgs& p, int num_sms, cudaStream_t s);
+
 // -------------------------------------------------------------- gated rows
 struct GateArgs {
   const void* gate;

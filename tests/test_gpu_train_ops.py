@@ -263,6 +263,41 @@ def test_weight_gradient_accumulates(pkg):
     assert (out == 0).all()
 
 
+@pytest.mark.parametrize("counts", [[5000], [3000, 0, 70, 2000, 1], [64, 9000, 63], [1024, 1025, 2111]],
+                         ids=str)
+@pytest.mark.parametrize("N,K", [(136, 520), (1, 257), (600, 33)])
+def test_weight_gradients_over_many_rows(pkg, counts, N, K):
+    """Few tiles with long sums: the rows are taken in parts, added in order."""
+    g = gen(sum(counts) + N)
+    off = bounds(counts)
+    dy, x = randn(g, sum(counts), N), randn(g, sum(counts), K)
+    ref, mag = plain_dw(dy, x, off)
+    n = max(counts)
+    close(pkg.grouped_matmul_dw(dy, x, off), ref, mag, n)
+    got = pkg.grouped_matmul_dw(dy, x, off, out_dtype=torch.float32)
+    close(got, ref, mag, n)
+    assert (got[[c == 0 for c in counts]] == 0).all()
+    assert torch.equal(got, pkg.grouped_matmul_dw(dy, x, off, out_dtype=torch.float32))
+    base = randn(g, len(counts), N, K, dt=torch.float32)
+    total = base.clone()
+    pkg.grouped_matmul_dw(dy, x, off, out=total, accumulate=True)
+    close(total, ref + base.double(), mag + base.double().abs(), n)
+
+
+@pytest.mark.parametrize("N,K", [(264, 1096), (129, 513), (1, 1), (513, 7)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_gradients_of_groups_without_rows(pkg, N, K, out):
+    """Zeros over whatever the output held, next to groups with rows."""
+    g = gen(N + K)
+    counts = [0, 9, 0, 0, 1, 0]
+    off = bounds(counts)
+    dy, x = randn(g, 10, N), randn(g, 10, K)
+    ref, mag = plain_dw(dy, x, off)
+    buf = torch.full((6, N, K), float("nan"), dtype=out, device="cuda")
+    pkg.grouped_matmul_dw(dy, x, off, out=buf)
+    close(buf, ref, mag, 9)
+
+
 def test_gradients_against_differences(pkg):
     """The products are linear: the gradient along a direction equals the
     central difference, up to FP32 sums."""
