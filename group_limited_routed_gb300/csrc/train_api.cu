@@ -178,13 +178,19 @@ int rows_tile(const beam_moe_grouped_t& g) {
 }
 
 // Whether groups of 257 to 384 rows are one tile (see pair_product_kernel.cuh):
-// where many groups are of that size.  Equal groups, in us without / with: 200
-// rows 156 / 163, 256: 163 / 168, 272: 208 / 181, 350: 219 / 195, 400: 223 /
-// 240; groups spread around a mean of 256 rows (a third of them that size)
-// 1384 / 1317.
-bool dual_rows(const beam_moe_grouped_t& g) {
+// where many groups are of that size.  32 equal groups, 2560 -> 5120, in us
+// without / with: 200 rows 156 / 163, 256: 163 / 168, 272: 208 / 181, 350: 219
+// / 195, 400: 223 / 240; 256 groups spread around a mean of 256 rows (a third
+// of them that size), the input gradient: 1384 / 1317.
+// Such a tile takes about 1.75 times one of half the rows, so it has to save
+// waves of the pairs too (272 rows a group, without / with: 4 x 2048 columns
+// 17.7 / 22.8 us, 8 x 2048 30.4 / 24.9, 16 x 1280 38.4 / 42.0, 24 x 2560 161 /
+// 156).
+bool dual_rows(const beam_moe_grouped_t& g, int64_t columns) {
   const int64_t mean = g.rows / g.n_groups;
-  return g.out_dtype != BEAM_DTYPE_F32 && mean > 224 && mean <= 352;
+  if (g.out_dtype == BEAM_DTYPE_F32 || mean <= 224 || mean > 352) return false;
+  const double waves = static_cast<double>(g.n_groups * ((columns + 255) / 256)) / 76;
+  return std::ceil(waves) * 1.75 <= std::ceil(2 * waves);
 }
 
 // Parts that a weight gradient's sums over rows are taken in.  Few tiles with
@@ -276,7 +282,7 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
     p.staged = staged_out(&to, p.out, p.out_type, M, N, static_cast<int64_t>(g.n_groups) * parts,
                           ld_out, z_out);
   const cudaError_t err =
-      beam::launch_pair_product(kind, nt, dual_rows(g), a_mn, b_mn, ta, tb, to, p, s);
+      beam::launch_pair_product(kind, nt, dual_rows(g, M), a_mn, b_mn, ta, tb, to, p, s);
   if (err != cudaSuccess || parts == 1) return launched(err);
   beam::JoinArgs j = {};
   j.part = static_cast<const float*>(p.out);

@@ -161,6 +161,26 @@ def test_groups_of_two_row_blocks(pkg, counts, N, K, dt):
         close(pkg.grouped_matmul_dx(dy, w, off), dx, mag, N)
 
 
+@pytest.mark.parametrize("counts", [[257, 256, 320, 384, 385, 0, 300, 290], [340, 1, 300, 383]],
+                         ids=str)
+@pytest.mark.parametrize("N,K", [(136, 72), (129, 513), (256, 200)])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+def test_many_groups_of_two_row_blocks(pkg, counts, N, K, dt):
+    """As above with 48 groups: enough of them that the tiles of two blocks
+    save a wave of the device's SM pairs."""
+    counts = (counts * 12)[:48]
+    g = gen(sum(counts) + K)
+    off = bounds(counts)
+    E, n = len(counts), sum(counts)
+    x, dy = randn(g, n, K, dt=dt), randn(g, n, N, dt=dt)
+    for w in (randn(g, E, N, K, dt=dt, scale=0.1),
+              randn(g, E, K, N, dt=dt, scale=0.1).transpose(1, 2)):
+        y, mag = plain_product(x, w, off)
+        close(pkg.grouped_matmul(x, w, off), y, mag, K)
+        dx, mag = plain_product(dy, w.transpose(1, 2), off)
+        close(pkg.grouped_matmul_dx(dy, w, off), dx, mag, N)
+
+
 @pytest.mark.parametrize("N", [1, 7, 8, 33, 130, 1000])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 def test_zero_rows_of_any_alignment(pkg, N, out):
