@@ -171,9 +171,14 @@ Operand operand_w(const beam_moe_grouped_t& g, const void* w) {
 // 8 rows 245 / 245 / 258, 32: 251 / 252 / 268, 48: 260 / 255 / 272, 96: 302 /
 // 270 / 281, 128: 364 / 288 / 288, 192: 486 / 324 / 300; 16 groups, 1024 ->
 // 2048: mean 24: 13 / 14 / 16, 64: 17 / 14 / 20, 128: 25 / 19 / 22.  (32 rows
-// were not faster anywhere: 221 against 215 at a mean of 2.)
-int rows_tile(const beam_moe_grouped_t& g) {
+// were not faster anywhere: 221 against 215 at a mean of 2.)  Where all tiles
+// run at once, the narrowest that do: 1 group of 1000 rows, 1024 -> 1024 8.0 /
+// 8.4 / 12.6, 4000 -> 416 16.3 / 17.0 / 24.7; 4 x 200, 2048 -> 2048 (two waves
+// of 64) 17.7 / 12.1 / 16.7.
+int rows_tile(const beam_moe_grouped_t& g, int64_t columns) {
   const int64_t mean = g.rows / g.n_groups;
+  for (int nt : {64, 128})
+    if (g.n_groups * ((columns + 255) / 256) * ((mean + nt) / nt) <= 76) return nt;
   return mean <= 40 ? 64 : mean <= 144 ? 128 : 256;
 }
 
@@ -378,7 +383,7 @@ beam_status_t beam_moe_grouped_matmul(const beam_moe_grouped_t* g, const void* x
   if (!valid_grouped(g)) return BEAM_ERR_INVALID_ARG;
   if (g->rows == 0) return BEAM_OK;
   if (!x || !w || !offsets || !y || !aligned16(workspace)) return BEAM_ERR_INVALID_ARG;
-  return grouped_launch(*g, beam::kProductRows, rows_tile(*g), !w_k_inner(*g), false,
+  return grouped_launch(*g, beam::kProductRows, rows_tile(*g, g->N), !w_k_inner(*g), false,
                         operand_w(*g, w), operand_x(*g, x), g->N, g->rows, g->K, offsets, y,
                         g->y_ld, 0, 0, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
 }
@@ -389,7 +394,7 @@ beam_status_t beam_moe_grouped_matmul_dx(const beam_moe_grouped_t* g, const void
   if (!valid_grouped(g)) return BEAM_ERR_INVALID_ARG;
   if (g->rows == 0) return BEAM_OK;
   if (!dy || !w || !offsets || !dx || !aligned16(workspace)) return BEAM_ERR_INVALID_ARG;
-  return grouped_launch(*g, beam::kProductRows, rows_tile(*g), w_k_inner(*g), false,
+  return grouped_launch(*g, beam::kProductRows, rows_tile(*g, g->K), w_k_inner(*g), false,
                         operand_w(*g, w), operand_y(*g, dy), g->K, g->rows, g->N, offsets, dx,
                         g->x_ld, 0, 0, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
 }

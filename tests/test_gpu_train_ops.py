@@ -181,6 +181,24 @@ def test_many_groups_of_two_row_blocks(pkg, counts, N, K, dt):
         close(pkg.grouped_matmul_dx(dy, w, off), dx, mag, N)
 
 
+@pytest.mark.parametrize("counts", [[130, 127, 1, 0, 65, 100], [257, 600, 0, 31, 513, 129],
+                                    [513, 400, 700, 0, 256, 767], [17, 1, 63, 64, 0, 65]], ids=str)
+@pytest.mark.parametrize("N,K", [(520, 136), (136, 700)])
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_products_over_many_groups(pkg, counts, N, K, out):
+    """72 groups: more tiles of every height than run at once."""
+    counts = counts * 12
+    g = gen(sum(counts) + K)
+    off = bounds(counts)
+    E, n = len(counts), sum(counts)
+    x, dy = randn(g, n, K), randn(g, n, N)
+    for w in (randn(g, E, N, K, scale=0.1), randn(g, E, K, N, scale=0.1).transpose(1, 2)):
+        y, mag = plain_product(x, w, off)
+        close(pkg.grouped_matmul(x, w, off, out_dtype=out), y, mag, K)
+        dx, mag = plain_product(dy, w.transpose(1, 2), off)
+        close(pkg.grouped_matmul_dx(dy, w, off, out_dtype=out), dx, mag, N)
+
+
 @pytest.mark.parametrize("N", [1, 7, 8, 33, 130, 1000])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 def test_zero_rows_of_any_alignment(pkg, N, out):
