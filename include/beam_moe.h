@@ -484,7 +484,11 @@ beam_status_t beam_moe_ep_combine(const beam_moe_config_t *cfg, const float *y_b
  * gradients, the gated activation with the routing weight, and the
  * orthogonalised update of stacked weights.  Conventions as above, except
  * that sizes are free (no multiples), row strides are arguments, and only
- * `workspace` has to be 16-byte aligned; elements are naturally aligned. */
+ * `workspace` has to be 16-byte aligned; elements are naturally aligned.
+ * Every kernel, a call's first included, is launched with programmatic stream
+ * serialization and waits for the one before it on the stream before it
+ * touches memory (the update's chain of products is an ordinary cooperative
+ * launch).  No result may overlap an operand unless it says so. */
 
 typedef enum {
   BEAM_DTYPE_BF16 = 0,
