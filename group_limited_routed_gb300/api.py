@@ -737,11 +737,13 @@ class OpWorkspace:
     """Caller-owned device workspace of one training operator (a status word,
     then scratch); calls that share it must be on one stream."""
 
-    def __init__(self, nbytes: int, device=None):
+    def __init__(self, nbytes: int, device=None, clear: bool = True):
         self.nbytes = int(nbytes)
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8,
                                device=device if device is not None else torch.device("cuda"))
-        self.buf[:256].zero_()
+        # (a call's own workspace has no one to read its status word)
+        if clear:
+            self.buf[:256].zero_()
 
     @property
     def ptr(self) -> int:
@@ -908,7 +910,7 @@ def _grouped_ws(d, a, b, stream) -> OpWorkspace:
     """A workspace for one call, when the caller keeps none."""
     with _on(stream, a.device):
         return OpWorkspace(_grouped_size(d, bool(a.data_ptr() % 16 or b.data_ptr() % 16)),
-                           a.device)
+                           a.device, clear=False)
 
 
 @_plans
@@ -1130,7 +1132,8 @@ def orthogonalize(m, steps: int = 5, coeffs=(3.4445, -4.7750, 2.0315), eps: floa
             stack = m.reshape(d.batch, d.rows, d.cols)
     if ws is None:
         with _on(stream, dev):
-            ws = OpWorkspace(orthogonalize_workspace_size(d.batch, d.rows, d.cols, m.dtype), dev)
+            ws = OpWorkspace(orthogonalize_workspace_size(d.batch, d.rows, d.cols, m.dtype), dev,
+                             clear=False)
     with _current(dev):
         _check(lib().beam_moe_orthogonalize(ref, stack.data_ptr(), out.data_ptr(), ws.ptr,
                                             ws.nbytes, _raw_stream(stream, dev.index)),
