@@ -55,10 +55,10 @@
 // L2's); k blocks of their own sizes one behind the other in the ring (deeper
 // for small tiles, but the roles' bookkeeping then takes 590 cycles a block of
 // 512: 1024-row groups 480 -> 499 us).  For 16-bit weight gradients: both
-// buffers of a tile read before either is stored (400-row groups 149 -> 165
-// us), 64 KB of staging (110 -> 114 at 256 rows, 149 -> 163 at 400: a stage
-// less), 128-byte rows staged by two warps (107 -> 113), vector stores by the
-// warps (107 -> 130).
+// buffers of a tile read before either is stored (400-row groups 139 -> 144
+// us, 32 uneven groups 227 -> 238), 64 KB of staging (256 rows 107 -> 112 us,
+// 400 rows 146 -> 151: a stage less), 128-byte rows staged by two warps (107 ->
+// 113), vector stores by the warps (107 -> 130).
 //
 // Every wait is bounded (gemm::Waiter); after an abort all roles still reach
 // the cluster barrier that precedes the release of TMEM.

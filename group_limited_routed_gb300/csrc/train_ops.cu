@@ -31,16 +31,59 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 
 // ------------------------------------------------------------ aligned copies
-// A warp takes 512 elements of a row of the destination, a lane 8 at a time:
-// the store is one 16-byte word.  The source row starts anywhere (element
+// A warp takes 512 elements of eight rows of the destination, a lane 8 at a
+// time: the store is one 16-byte word.  The source row starts anywhere (element
 // aligned), so it is read in 4-byte words from the 4-byte boundary at or
 // before it -- five words hold the eight elements -- and shifted by one
 // element where it starts on an odd one.  Matrices of groups without rows are
 // left out.  Memory bound: 2 bytes read, 2 written per element.
 constexpr int kPackSpan = 512;
+// (1 row a warp starts blocks for longer than it copies; products with odd k, us
+// for 1 / 4 / 8 / 32 rows: 6000 rows, 24 x 2047 x 1365 146 / 114 / 111 / 123, 11
+// rows, 47 x 1064 x 551 37 / 22 / 21 / 38, 20 rows, 133 x 3400 x 4823 1192 / 580 /
+// 474 / 413)
+constexpr int kPackRows = 8;
 
 int64_t pack_units(const PackArgs& p) {
-  return p.zs * p.rows * ((p.ld + kPackSpan - 1) / kPackSpan);
+  return p.zs * ((p.rows + kPackRows - 1) / kPackRows) * ((p.ld + kPackSpan - 1) / kPackSpan);
+}
+
+// Elements [first, first + kPackSpan) of a row, and zeros behind its end.
+__device__ __forceinline__ void pack_row(const uint16_t* src, uint16_t* dst, int cols, int ld,
+                                         int first, int lane) {
+  const bool odd = (reinterpret_cast<uintptr_t>(src) & 2u) != 0;
+  // words[k] holds elements 2k - odd and 2k + 1 - odd of the row
+  const uint32_t* words = reinterpret_cast<const uint32_t*>(src - (odd ? 1 : 0));
+  const int whole = (cols + (odd ? 1 : 0)) / 2;  // words wholly at or before the row's end
+  uint32_t w[kPackSpan / 256][5];
+#pragma unroll
+  for (int h = 0; h < kPackSpan / 256; ++h) {
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+      const int at = (first + h * 256) / 2 + lane * 4 + k;
+      // the first word of an odd row begins one element before it, the
+      // last word may end one after it: those are read by the element
+      w[h][k] = 0u;
+      if (at < whole && !(odd && at == 0)) {
+        w[h][k] = words[at];
+      } else {
+        const int e = 2 * at - (odd ? 1 : 0);
+        if (e >= 0 && e < cols) w[h][k] = src[e];
+        if (e + 1 >= 0 && e + 1 < cols) w[h][k] |= static_cast<uint32_t>(src[e + 1]) << 16;
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < kPackSpan / 256; ++h) {
+    const int c = first + h * 256 + lane * 8;
+    if (c >= ld) continue;
+    uint4 v;
+    v.x = odd ? __funnelshift_r(w[h][0], w[h][1], 16) : w[h][0];
+    v.y = odd ? __funnelshift_r(w[h][1], w[h][2], 16) : w[h][1];
+    v.z = odd ? __funnelshift_r(w[h][2], w[h][3], 16) : w[h][2];
+    v.w = odd ? __funnelshift_r(w[h][3], w[h][4], 16) : w[h][3];
+    *reinterpret_cast<uint4*>(dst + c) = v;
+  }
 }
 
 // One launch copies a call's one or two such operands (units_a warps' pieces
@@ -55,45 +98,17 @@ __global__ void __launch_bounds__(256)
     const PackArgs& p = at_unit < units_a ? a : b;
     const int64_t unit = at_unit < units_a ? at_unit : at_unit - units_a;
     const int spans = (p.ld + kPackSpan - 1) / kPackSpan;
-    const int64_t row = unit / spans;
-    const int first = static_cast<int>(unit - row * spans) * kPackSpan;
-    const int64_t z = row / p.rows;
+    const int64_t per_z = (p.rows + kPackRows - 1) / kPackRows;
+    const int64_t part = unit / spans;
+    const int first = static_cast<int>(unit - part * spans) * kPackSpan;
+    const int64_t z = part / per_z;
     if (p.offsets && p.offsets[z + 1] <= p.offsets[z]) continue;
-    const uint16_t* src = p.src + z * p.sz + (row - z * p.rows) * p.sr;
-    const bool odd = (reinterpret_cast<uintptr_t>(src) & 2u) != 0;
-    // words[k] holds elements 2k - odd and 2k + 1 - odd of the row
-    const uint32_t* words = reinterpret_cast<const uint32_t*>(src - (odd ? 1 : 0));
-    const int whole = (p.cols + (odd ? 1 : 0)) / 2;  // words wholly at or before the row's end
-    uint16_t* dst = p.dst + row * p.ld;
-    uint32_t w[kPackSpan / 256][5];
-#pragma unroll
-    for (int h = 0; h < kPackSpan / 256; ++h) {
-#pragma unroll
-      for (int k = 0; k < 5; ++k) {
-        const int at = (first + h * 256) / 2 + lane * 4 + k;
-        // the first word of an odd row begins one element before it, the
-        // last word may end one after it: those are read by the element
-        w[h][k] = 0u;
-        if (at < whole && !(odd && at == 0)) {
-          w[h][k] = words[at];
-        } else {
-          const int e = 2 * at - (odd ? 1 : 0);
-          if (e >= 0 && e < p.cols) w[h][k] = src[e];
-          if (e + 1 >= 0 && e + 1 < p.cols) w[h][k] |= static_cast<uint32_t>(src[e + 1]) << 16;
-        }
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < kPackSpan / 256; ++h) {
-      const int c = first + h * 256 + lane * 8;
-      if (c >= p.ld) continue;
-      uint4 v;
-      v.x = odd ? __funnelshift_r(w[h][0], w[h][1], 16) : w[h][0];
-      v.y = odd ? __funnelshift_r(w[h][1], w[h][2], 16) : w[h][1];
-      v.z = odd ? __funnelshift_r(w[h][2], w[h][3], 16) : w[h][2];
-      v.w = odd ? __funnelshift_r(w[h][3], w[h][4], 16) : w[h][3];
-      *reinterpret_cast<uint4*>(dst + c) = v;
-    }
+    const int64_t row = (part - z * per_z) * kPackRows;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kPackRows), p.rows - row));
+    const uint16_t* src = p.src + z * p.sz + row * p.sr;
+    uint16_t* dst = p.dst + (z * p.rows + row) * p.ld;
+    for (int r = 0; r < rows; ++r)
+      pack_row(src + r * p.sr, dst + static_cast<int64_t>(r) * p.ld, p.cols, p.ld, first, lane);
   }
 }
 
