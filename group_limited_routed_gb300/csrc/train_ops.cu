@@ -1,6 +1,7 @@
 // Memory-bound kernels of the training operators: aligned copies of operands
-// TMA cannot address, the gated activation with its gradient, and the scaled
-// start of the orthogonalised update.
+// TMA cannot address, the sums of a weight gradient's parts, the gated
+// activation with its gradient, and the scaled start of the orthogonalised
+// update.
 #include "train_ops.cuh"
 
 #include <cuda_bf16.h>
@@ -337,6 +338,23 @@ __device__ __forceinline__ void load_row8(const NormArgs& p, int64_t base, int c
   }
 }
 
+// The sum over the block's threads, in thread 0.
+__device__ __forceinline__ void block_sum(ScaledSum& acc, int* se, float* sf) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const int e = __shfl_xor_sync(kAll, acc.exp, o);
+    const float f = __shfl_xor_sync(kAll, acc.sum, o);
+    acc.add(e, f);
+  }
+  if (threadIdx.x % 32 == 0) {
+    se[threadIdx.x / 32] = acc.exp;
+    sf[threadIdx.x / 32] = acc.sum;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int k = 1; k < 8; ++k) acc.add(se[k], sf[k]);
+}
+
 // First pass: each block's largest magnitude and sum of squares, in one read.
 template <int TYPE, bool VEC>
 __global__ void __launch_bounds__(256) amax_kernel(const NormArgs p) {
@@ -357,19 +375,8 @@ __global__ void __launch_bounds__(256) amax_kernel(const NormArgs p) {
     acc.add8(v, m);
   }
   m = block_max(m, s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const int e = __shfl_xor_sync(kAll, acc.exp, o);
-    const float f = __shfl_xor_sync(kAll, acc.sum, o);
-    acc.add(e, f);
-  }
-  if (threadIdx.x % 32 == 0) {
-    se[threadIdx.x / 32] = acc.exp;
-    sf[threadIdx.x / 32] = acc.sum;
-  }
-  __syncthreads();
+  block_sum(acc, se, sf);
   if (threadIdx.x == 0) {
-    for (int k = 1; k < 8; ++k) acc.add(se[k], sf[k]);
     p.amax[z * kNormBlocks + blockIdx.x] = m;
     p.sum_exp[z * kNormBlocks + blockIdx.x] = acc.exp;
     p.sumsq[z * kNormBlocks + blockIdx.x] = acc.sum;
@@ -407,10 +414,15 @@ __global__ void __launch_bounds__(256) scale_kernel(const NormArgs p) {
     *reinterpret_cast<uint4*>(p.hi + dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     if (p.lo) *reinterpret_cast<uint4*>(p.lo + dst) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    ScaledSum acc;
-    for (int q = 0; q < p.blocks; ++q)
-      acc.add(p.sum_exp[z * kNormBlocks + q], p.sumsq[z * kNormBlocks + q]);
+  if (blockIdx.x != 0) return;
+  // (a thread a part: one thread over all of them took 10 us)
+  __shared__ int se[8];
+  __shared__ float sf[8];
+  ScaledSum acc;
+  if (threadIdx.x < p.blocks)
+    acc.add(p.sum_exp[z * kNormBlocks + threadIdx.x], p.sumsq[z * kNormBlocks + threadIdx.x]);
+  block_sum(acc, se, sf);
+  if (threadIdx.x == 0) {
     const float inv = inverse_norm(amax, acc, k, p.eps);
     p.alpha_gram[z] = p.scale_gram * inv * inv;
     p.alpha_step[z] = p.scale_step * inv;
