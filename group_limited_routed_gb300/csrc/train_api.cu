@@ -342,20 +342,26 @@ bool ortho_layout(int32_t batch, int32_t rows, int32_t cols, int32_t dtype, Orth
 
 // Rows per tile of a chain of products (ortho_chain.cu): 256 keep the tensor
 // cores busiest (0.36 us per 64-wide k block for twice the rows of 128 in
-// 0.26), 128 spread small products over more CTA pairs.  The estimate is the
-// waves of each product times its k blocks; measured, in us for 128 / 256:
-// 512 x 1024 128 / 169, 1536 x 1536 197 / 245, 4 x 1024 x 2048 246 / 257,
-// 2048 x 4096 423 / 393, 8 x 2560 x 5120 (by rule) 256.
+// 0.275), 128 spread small products over more CTA pairs and end sooner (3.4 us
+// a product beside its k blocks, 4.3 with 256).  The estimate is the waves of
+// each product times its k blocks, whole waves for one matrix, where each
+// product waits for the last; measured, in us for 128 / 256: 512 x 1024 128 /
+// 169, 1536 x 1536 197 / 245, 2048 x 4096 423 / 393, 4 x 1024 x 1024 177 / 205,
+// 16 x 512 x 1024 185 / 209, 7 x 864 x 2288 349 / 338, 8 x 1189 x 1952 540 /
+// 400, 8 x 2560 x 5120 (by rule) 256.
 int chain_tile(int64_t batch, int64_t R, int64_t C, int64_t pairs) {
   const int64_t m = std::min(R, C), mt = (m + 255) / 256;
-  auto cost = [&](int64_t nt, double block_us) {
-    auto waves = [&](int64_t tiles) { return static_cast<double>((tiles + pairs - 1) / pairs); };
+  auto cost = [&](int64_t nt, double block_us, double product_us) {
+    auto waves = [&](int64_t tiles) {
+      const double w = static_cast<double>(tiles) / pairs;
+      return batch == 1 ? std::ceil(w) : std::max(1., w);
+    };
     const int64_t sym = batch * (mt * ((m + nt - 1) / nt) - 256 / nt * (mt * (mt - 1) / 2));
     const int64_t step = batch * ((C + 255) / 256) * ((R + nt - 1) / nt);
     const int64_t km = (m + 63) / 64, kn = (std::max(R, C) + 63) / 64;
-    return block_us * (waves(sym) * (kn + km) + waves(step) * km);
+    return block_us * (waves(sym) * (kn + km) + waves(step) * km) + 3 * product_us;
   };
-  return cost(256, 0.36) <= cost(128, 0.26) ? 256 : 128;
+  return cost(256, 0.36, 4.3) <= cost(128, 0.275, 3.4) ? 256 : 128;
 }
 
 template <typename T>
