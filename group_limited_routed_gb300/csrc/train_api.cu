@@ -231,13 +231,15 @@ beam_status_t grouped_launch(const beam_moe_grouped_t& g, int kind, int nt, bool
                              const int32_t* offsets, void* out, int64_t ld_out, int64_t z_out,
                              int accumulate, void* ws, size_t ws_bytes, cudaStream_t s) {
   const bool pack_a = !a.in_place(), pack_b = !b.in_place();
-  const int32_t parts = kind == beam::kProductGroups ? grad_parts(g) : 1;
+  int32_t parts = kind == beam::kProductGroups ? grad_parts(g) : 1;
   size_t need = kAlign;
   const size_t at_a = need;
   if (pack_a) need += a.packed_bytes();
   const size_t at_b = need;
   if (pack_b) need += b.packed_bytes();
   const size_t at_parts = need;
+  // (a workspace made for other sizes may hold fewer)
+  while (parts > 1 && ws_bytes < need + parts_bytes(g, parts)) --parts;
   need += parts_bytes(g, parts);
   if (ws_bytes < need) return BEAM_ERR_WORKSPACE;
   beam::host::DevInfo dev;

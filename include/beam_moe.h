@@ -515,8 +515,9 @@ typedef struct {
 /* Bytes of workspace the three products need: a status word, room for an
  * aligned copy of every operand whose strides are not multiples of 8 elements
  * (with unaligned != 0, of all: bases may then be unaligned too), and for FP32
- * parts of a weight gradient of few tiles and many rows.  0 for an invalid
- * description. */
+ * parts of a weight gradient of few tiles and many rows (fewer are taken where
+ * they do not fit: a workspace made for more rows does for fewer).  0 for an
+ * invalid description. */
 size_t beam_moe_grouped_matmul_workspace_size(const beam_moe_grouped_t *g, int32_t unaligned);
 
 /* y[r] = W[e] x[r] for every row r of every group e (single-token batches
@@ -534,7 +535,7 @@ beam_status_t beam_moe_grouped_matmul_dx(const beam_moe_grouped_t *g, const void
 
 /* The weight gradient dW[e] = sum over the group's rows of dy[r] x[r]^T
  * (out_dtype is dW's type), dense [n_groups, N, K]; zero for a group without
- * rows.  Sums in an order that sizes alone decide.  accumulate != 0 (F32 only) adds to dW instead.  w_stride_* must be
+ * rows.  Sums in an order that the sizes (the workspace's too) decide.  accumulate != 0 (F32 only) adds to dW instead.  w_stride_* must be
  * valid but are not used. */
 beam_status_t beam_moe_grouped_matmul_dw(const beam_moe_grouped_t *g, const void *dy,
                                          const void *x, const int32_t *offsets, int32_t accumulate,

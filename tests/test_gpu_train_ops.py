@@ -322,6 +322,20 @@ def test_weight_gradients_over_many_rows(pkg, counts, N, K):
     close(total, ref + base.double(), mag + base.double().abs(), n)
 
 
+def test_weight_gradient_in_a_smaller_workspace(pkg):
+    """Room for some of the parts or none: fewer are taken."""
+    g = gen(71)
+    off = bounds([9000])
+    dy, x = randn(g, 9000, 136), randn(g, 9000, 264)
+    ref, mag = plain_dw(dy, x, off)
+    full = pkg.grouped_matmul_workspace_size(9000, 1, 136, 264)
+    assert full > 136 * 264 * 8
+    for nbytes in (4096, 136 * 264 * 8 + 8192, full):
+        ws = pkg.OpWorkspace(nbytes)
+        close(pkg.grouped_matmul_dw(dy, x, off, out_dtype=torch.float32, ws=ws), ref, mag, 9000)
+        close(pkg.grouped_matmul_dw(dy, x, off, ws=ws), ref, mag, 9000)
+
+
 @pytest.mark.parametrize("N,K", [(264, 1096), (129, 513), (1, 1), (513, 7)])
 @pytest.mark.parametrize("out", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 def test_gradients_of_groups_without_rows(pkg, N, K, out):
